@@ -13,6 +13,9 @@ Entry points (same names as the C ABI):
     qlora_linear_fwd_multi(qt, X, A_stack, B_stack, adapter_idx, s) -> (Y, XA): one adapter per token
     qlora_linear_bwd(qt, X, dY, A, B, s, XA=None, need_dx=True) -> (dX bf16 or None, dA fp32, dB fp32)
     qlora_get_codebook()                              -> 16 float levels
+Microscaled 4-bit formats (MXFP4, NVFP4):
+    qlora_mx_quantize(W, fmt, transpose, per_row)     -> MXTensor
+    qlora_mx_dequantize(q)                            -> bf16 [rows, cols]
 """
 from __future__ import annotations
 
@@ -84,10 +87,25 @@ _lib.qlora_time_next_gemm.restype = ctypes.c_int
 _lib.qlora_selftest_bounded_wait.argtypes = [_i64, _vp, _vp]
 _lib.qlora_selftest_bounded_wait.restype = ctypes.c_int
 
+class _MxTensorC(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("global_scale", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("format", ctypes.c_int32), ("scale_per_row", ctypes.c_int32)]
+
+
+_MX = ctypes.POINTER(_MxTensorC)
+_lib.qlora_mx_sizes.argtypes = [_i64, _i64, _i32, _i32, _szp, _szp, _szp, _szp]
+_lib.qlora_mx_sizes.restype = ctypes.c_int
+_lib.qlora_mx_quantize.argtypes = [_vp, _i32, _MX, _vp, _sz, _vp]
+_lib.qlora_mx_quantize.restype = ctypes.c_int
+_lib.qlora_mx_dequantize.argtypes = [_MX, _vp, _vp]
+_lib.qlora_mx_dequantize.restype = ctypes.c_int
+
 EXPORTED = ["qlora_status_string", "qlora_get_codebook", "qlora_get_levels", "qlora_nf4_sizes", "qlora_quantize_nf4_dq",
             "qlora_dequantize", "qlora_linear_workspace_size", "qlora_linear_fwd", "qlora_linear_fwd_multi",
             "qlora_linear_bwd", "qlora_read_device_errors", "qlora_kernel_launches",
-            "qlora_time_next_gemm", "qlora_quantize_nf4_dq_noalloc", "qlora_selftest_bounded_wait"]
+            "qlora_time_next_gemm", "qlora_quantize_nf4_dq_noalloc", "qlora_selftest_bounded_wait",
+            "qlora_mx_sizes", "qlora_mx_quantize", "qlora_mx_dequantize"]
 
 # Largest weight the allocation-free quantize variant accepts.
 NOALLOC_MAX_ELEMENTS = 134217728
@@ -357,3 +375,133 @@ def qlora_time_next_gemm(start: torch.cuda.Event, stop: torch.cuda.Event) -> Non
     """Bracket the calling thread's next fused dequant-GEMM launch with two CUDA events."""
     _check(_lib.qlora_time_next_gemm(ctypes.c_void_p(start.cuda_event), ctypes.c_void_p(stop.cuda_event)),
            "qlora_time_next_gemm")
+
+
+# ---------------------------------------------------------------- microscaled 4-bit formats
+# The formats (qlora_mx_format) and the elements of one of their blocks.
+MX_FORMATS = {"mxfp4": 0, "nvfp4": 1}
+MX_BLOCK = {"mxfp4": 32, "nvfp4": 16}
+
+
+def _mx_bytes(rows: int, cols: int, fmt: str) -> tuple:
+    """(codes, scales) bytes of a microscaled matrix, as qlora_mx_sizes."""
+    return rows * ((cols + 31) // 32 * 16), (rows + 127) // 128 * (-(-cols // (4 * MX_BLOCK[fmt]))) * 512
+
+
+@dataclass
+class MXTensor:
+    """A microscaled 4-bit matrix: packed e2m1 codes, one scale byte per block
+    of 32 (MXFP4, E8M0) or 16 (NVFP4, E4M3) elements of a row in the tile order
+    qlora.h gives, and for NVFP4 a float scale, one or one per row."""
+    codes: torch.Tensor                     # uint8 [rows * 16 * ceil(cols / 32)]
+    scales: torch.Tensor                    # uint8, tiles of 512 bytes
+    global_scale: torch.Tensor | None       # float32 [1] or [rows] (NVFP4)
+    rows: int
+    cols: int
+    fmt: str = "mxfp4"                      # "mxfp4" or "nvfp4"
+
+    @property
+    def scale_per_row(self) -> bool:
+        return self.global_scale is not None and self.rows != 1 and self.global_scale.numel() == self.rows
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.codes, self.scales, self.global_scale) if t is not None)
+
+    def c_struct(self) -> _MxTensorC:
+        """The C descriptor, after checking that the buffers hold what it describes."""
+        c, s, g = self.codes, self.scales, self.global_scale
+        if self.fmt not in MX_FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(MX_FORMATS)}")
+        need_c, need_s = _mx_bytes(self.rows, self.cols, self.fmt)
+        if not (c.dtype == s.dtype == torch.uint8 and c.is_contiguous() and s.is_contiguous() and c.is_cuda
+                and c.device == s.device):
+            raise ValueError("codes and scales must be contiguous uint8 tensors on one CUDA device")
+        if c.numel() < need_c or s.numel() < need_s:
+            raise ValueError(f"a {self.rows}x{self.cols} {self.fmt} tensor needs {need_c} bytes of codes and {need_s} of scales")
+        if (g is None) != (self.fmt == "mxfp4"):
+            raise ValueError("global_scale belongs to nvfp4 and only to it")
+        if g is not None and not (g.dtype == torch.float32 and g.is_contiguous() and g.device == c.device
+                                  and g.numel() in (1, self.rows)):
+            raise ValueError("global_scale must be a float32 tensor of 1 or `rows` elements on the codes' device")
+        return _MxTensorC(c.data_ptr(), s.data_ptr(), 0 if g is None else g.data_ptr(), self.rows, self.cols,
+                          MX_FORMATS[self.fmt], 1 if self.scale_per_row else 0)
+
+
+def empty_mx(rows: int, cols: int, device, fmt: str = "mxfp4", per_row: bool = False) -> MXTensor:
+    """An MXTensor with buffers for a [rows, cols] matrix."""
+    if fmt not in MX_FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(MX_FORMATS)}")
+    if per_row and fmt != "nvfp4":
+        raise ValueError("a scale per row belongs to nvfp4")
+    nc, ns = _mx_bytes(rows, cols, fmt)
+    g = torch.empty(rows if per_row else 1, dtype=torch.float32, device=device) if fmt == "nvfp4" else None
+    return MXTensor(torch.empty(nc, dtype=torch.uint8, device=device), torch.empty(ns, dtype=torch.uint8, device=device),
+                    g, rows, cols, fmt)
+
+
+def _on(device, where: str, fn, *args):
+    """Call a C entry point with the tensors' device current and its current
+    stream as the last argument."""
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), where)
+
+
+def qlora_mx_sizes(rows: int, cols: int, fmt: str = "mxfp4", per_row: bool = False) -> dict:
+    """Buffer sizes in bytes of a microscaled matrix."""
+    v = [ctypes.c_size_t() for _ in range(4)]
+    _check(_lib.qlora_mx_sizes(rows, cols, MX_FORMATS[fmt], int(per_row), *[ctypes.byref(x) for x in v]), "qlora_mx_sizes")
+    return dict(codes=v[0].value, scales=v[1].value, global_scale=v[2].value, workspace=v[3].value)
+
+
+def qlora_mx_quantize(W: torch.Tensor, fmt: str = "mxfp4", transpose: bool = False, per_row: bool = False,
+                      out: MXTensor | None = None, workspace: torch.Tensor | None = None) -> MXTensor:
+    """Quantise a bf16 [rows, cols] matrix along its rows, or with `transpose`
+    its transpose (the weight operand of qlora_mx_linear_bwd).  `per_row` gives
+    an NVFP4 matrix one global scale per row instead of one in all; `out`, when
+    given, fixes the format and the form."""
+    _need_bf16_cuda("W", W)
+    if W.dim() != 2:
+        raise ValueError("W must be a matrix")
+    rows, cols = (W.shape[1], W.shape[0]) if transpose else (W.shape[0], W.shape[1])
+    if out is None:
+        out = empty_mx(rows, cols, W.device, fmt, per_row)
+    elif (out.rows, out.cols) != (rows, cols) or out.device != W.device:
+        raise ValueError(f"out describes {out.rows}x{out.cols} on {out.device}, the result is {rows}x{cols} on {W.device}")
+    if rows == 0 or cols == 0:
+        return out
+    c = out.c_struct()
+    if workspace is None and out.fmt == "nvfp4" and not out.scale_per_row:
+        workspace = torch.empty(qlora_mx_sizes(rows, cols, "nvfp4")["workspace"], dtype=torch.uint8, device=W.device)
+    _on(W.device, "qlora_mx_quantize", _lib.qlora_mx_quantize, W.data_ptr(), int(transpose), c, _addr(workspace),
+        _size(workspace))
+    return out
+
+
+def qlora_mx_dequantize(q: MXTensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values of a microscaled matrix as a bf16 [rows, cols] tensor."""
+    if out is None:
+        out = torch.empty(q.rows, q.cols, dtype=torch.bfloat16, device=q.device)
+    else:
+        _need_bf16_cuda("out", out)
+        if out.shape != (q.rows, q.cols) or out.device != q.device:
+            raise ValueError(f"out must be a {q.rows}x{q.cols} tensor on {q.device}")
+    if q.rows == 0 or q.cols == 0:
+        return out
+    _on(q.device, "qlora_mx_dequantize", _lib.qlora_mx_dequantize, q.c_struct(), out.data_ptr())
+    return out
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _size(t) -> int:
+    """Bytes of a work buffer (0 for none)."""
+    return 0 if t is None else t.numel() * t.element_size()

@@ -29,22 +29,11 @@ namespace {
 constexpr int kBlock = 64;
 constexpr int kBlock2 = 256;
 constexpr int kMaxEncodeGrid = 2048;        // partial sums of the mean: one double per CTA
-constexpr int64_t kMaxDim = int64_t(1) << 31;
 constexpr int kMaxDevices = 64;
-
-struct DeviceInfo {
-  bool ready = false;
-  bool sm100 = false;
-  int num_sms = 0;
-  uint32_t* err = nullptr;
-};
 
 std::mutex g_mu;
 std::atomic<uint64_t> g_launches{0};
 thread_local cudaEvent_t t_gemm_start = nullptr, t_gemm_stop = nullptr;
-
-bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_bytes,
-                 uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
 
 cudaError_t fused_timed(FusedDir dir, int bn, const FusedArgs& fa, const CUtensorMap& act,
                         const CUtensorMap& lora, int num_sms, cudaStream_t cs) {
@@ -64,6 +53,8 @@ cudaError_t fused_timed(FusedDir dir, int bn, const FusedArgs& fa, const CUtenso
 }
 DeviceInfo g_dev[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode_tiled = nullptr;
+
+}  // namespace
 
 qlora_status device_info(DeviceInfo* out) {
   int dev = 0;
@@ -96,9 +87,6 @@ qlora_status device_info(DeviceInfo* out) {
   return QLORA_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
 // 2-D bf16 tensor map, 128-byte swizzle: dims {inner, outer}, row pitch in
 // bytes, box {64, box_outer}.  Out-of-bounds elements read as zero.
 bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_bytes,
@@ -127,6 +115,8 @@ bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t oute
                                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+namespace {
 
 // m-tiles per rasterization group of the fused kernel: the packed codes of one
 // group (128 rows or columns of W times `contraction` weights, half a byte

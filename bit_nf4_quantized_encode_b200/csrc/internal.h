@@ -1,14 +1,41 @@
 // internal.h -- host-side helpers shared by the C entry points (api.cu,
-// noalloc.cu, selftest.cu): launch counting and validation of a quantized
-// weight's descriptor.  Not part of the public ABI.
+// mx_api.cu, noalloc.cu, selftest.cu): launch counting, validation of a
+// quantized weight's descriptor, the device's properties and tensor maps.  Not
+// part of the public ABI.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
 
 #include "codec.h"
 #include "nf4_tables.h"
 #include "qlora.h"
 
 namespace qlora {
+
+constexpr int64_t kMaxDim = int64_t(1) << 31;
+
+struct DeviceInfo {
+  bool ready = false;
+  bool sm100 = false;
+  int num_sms = 0;
+  uint32_t* err = nullptr;     // the library's error flag on the device
+};
+
+// Properties of the current device; QLORA_ERR_UNSUPPORTED on a non-sm_100 device.
+qlora_status device_info(DeviceInfo* out);
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Tensor maps (after device_info): 2-D bf16 with 128-byte swizzle and box
+// {64, box_outer}; 2-D uint8 with the given box and swizzle.
+bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_bytes,
+              uint32_t box_outer);
+bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_bytes,
+                 uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
 
 // Returns e; when it is cudaSuccess, adds n to the process-wide count of
 // kernels the library has launched (qlora_kernel_launches).

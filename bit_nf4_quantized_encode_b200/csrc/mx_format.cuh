@@ -1,0 +1,85 @@
+// mx_format.cuh -- the microscaled 4-bit formats on the device (sm_100a):
+// e2m1 elements, one scale per block of 32 (MXFP4, E8M0) or 16 (NVFP4, E4M3),
+// and where a scale byte lies in its tile.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "mx.h"
+
+namespace qlora {
+
+// Byte of the scale of block `blk` of row `row`: tiles of 128 rows x 4 blocks,
+// 512 bytes, row-tile major (kt tiles a row), the layout the tensor core's
+// 32-lane x 16-byte scale copies read without rearranging.
+__host__ __device__ __forceinline__ int64_t mx_scale_offset(int64_t row, int64_t blk, int64_t kt) {
+  return ((row >> 7) * kt + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3);
+}
+
+// Eight floats -> eight e2m1 codes (element j in bits 4j .. 4j+3): nearest,
+// ties to the even code, values above 6 saturate.
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(w) : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return w;
+}
+
+// E8M0 byte of a block whose largest magnitude has the bits of a non-negative
+// finite float: floor(log2 amax) - 2, at least -127, biased by 127 (6 = 1.5 * 2^2
+// is the largest level).  Subnormal floats have exponent field 0 and clamp too.
+__device__ __forceinline__ uint32_t mx_e8m0(uint32_t amax_bits) {
+  const int e = static_cast<int>(amax_bits >> 23) - 2;
+  return e > 0 ? static_cast<uint32_t>(e) : 0u;
+}
+// 2^(127 - byte) for byte <= 253, exact.
+__device__ __forceinline__ float mx_e8m0_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// The value of an E8M0 byte (255: NaN).
+__device__ __forceinline__ float mx_e8m0_value(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7FC00000u : (byte == 0u ? 0x00400000u : byte << 23));
+}
+
+// E4M3 byte of a non-negative float <= 448 (ties to even).
+__device__ __forceinline__ uint32_t mx_e4m3(float v) {
+  uint16_t h;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(0.0f), "f"(v));
+  return h & 0xFFu;
+}
+
+// The NVFP4 global scale of magnitudes up to `amax` (bits of a non-negative
+// finite float): the smallest power of two g with amax <= 6 * 448 * g
+// (2688 = 1.3125 * 2^11), at least 2^-126; 1 for amax = 0.  A power of two, so
+// that x / g is exact and every comparison below is the one of exact numbers.
+__device__ __forceinline__ float mx_global_scale(uint32_t amax_bits) {
+  if (amax_bits == 0u) return 1.0f;
+  int e = static_cast<int>(amax_bits >> 23) - 127 - 11 + ((amax_bits & 0x7FFFFFu) > 0x280000u ? 1 : 0);
+  if (e < -126) e = -126;
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+// 1 / g of a power of two in [2^-126, 2^127).
+__device__ __forceinline__ float mx_pow2_inverse(float g) { return __uint_as_float((254u << 23) - __float_as_uint(g)); }
+
+// Quotient v / s rounded to nearest, from r = RN(1 / s): one Newton step on the
+// remainder.  Where v / s is exactly half way between two levels it is
+// representable and the step returns it exactly, so the tie stays a tie; every
+// other quotient of an 8-bit by a 4-bit significand is 2^-9 away from one.  The
+// step turns -0 into +0, so the sign is put back.
+__device__ __forceinline__ float mx_quotient(float v, float s, float r) {
+  const float q = __fmul_rn(v, r);
+  return copysignf(__fmaf_rn(__fmaf_rn(-q, s, v), r, q), v);
+}
+
+// bf16 bits -> magnitude bits with non-finite values as zero, and whether any was seen.
+__device__ __forceinline__ uint32_t mx_finite_mag(uint32_t bits16, bool& bad) {
+  const uint32_t m = bits16 & 0x7FFFu;
+  if (m >= 0x7F80u) { bad = true; return 0u; }
+  return m;
+}
+
+}  // namespace qlora

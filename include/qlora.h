@@ -234,6 +234,74 @@ QLORA_EXPORT qlora_status qlora_linear_bwd(const qlora_nf4_tensor* W, const uint
                               void* workspace, size_t workspace_bytes, qlora_stream_t stream);
 
 /*
+ * Microscaled 4-bit floating point: e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and sign) with one scale per block of consecutive elements of a row.  The
+ * tensor cores multiply two such operands directly.
+ *   QLORA_MXFP4  blocks of 32, an E8M0 scale 2^E with
+ *                E = max(-127, floor(log2 amax) - 2) (OCP Microscaling Formats
+ *                v1.0, section 6.3): code = e2m1(x / 2^E);
+ *   QLORA_NVFP4  blocks of 16, an E4M3 scale S and a float g, one for the
+ *                tensor or one per row: g is the smallest power of two (at
+ *                least 2^-126) with amax_all <= 6 * 448 g, 1 when amax_all = 0;
+ *                S = e4m3((amax / g) / 6), code = e2m1((x / g) / S), 0 when S = 0.
+ * e2m1() and e4m3() round to nearest, ties to even; codes and scales are those
+ * of exact arithmetic.  A block holding a value that is not finite gets the
+ * scale NaN (and takes no part in g); the other blocks are as without it.
+ */
+typedef enum { QLORA_MXFP4 = 0, QLORA_NVFP4 = 1 } qlora_mx_format;
+
+/*
+ * A microscaled matrix [rows, cols].  Caller-owned device memory:
+ *   codes        [rows][pitch] bytes, pitch = 16 * ceil(cols / 32); element 2j
+ *                of a row in the low four bits of byte j, element 2j + 1 in the
+ *                high ones; past cols code 0.
+ *   scales       one byte per block (E8M0, or E4M3), in tiles of 128 rows x 4
+ *                blocks: the byte of row r, block b is at
+ *                ((r / 128) * ceil(ceil(cols / block) / 4) + b / 4) * 512
+ *                + (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4;
+ *                the bytes of rows and blocks that do not exist must not be
+ *                NaN (the encoder writes 0).
+ *   global_scale QLORA_NVFP4 only: float [1], or [rows] when scale_per_row.
+ *                The encoder writes powers of two; any positive finite float
+ *                is taken when read.
+ *   value = e2m1(code) * scale [* global_scale].
+ */
+typedef struct {
+  uint8_t* codes;
+  uint8_t* scales;
+  float* global_scale;
+  int64_t rows;
+  int64_t cols;
+  int32_t format;          /* a qlora_mx_format */
+  int32_t scale_per_row;   /* QLORA_NVFP4: 0 or 1; QLORA_MXFP4: 0 */
+} qlora_mx_tensor;
+
+/*
+ * Byte sizes of the buffers of a microscaled [rows, cols] matrix (global_scale
+ * is 0 bytes for QLORA_MXFP4) and of the work buffer qlora_mx_quantize needs
+ * (0 but for QLORA_NVFP4 with one global scale).  Any output pointer may be NULL.
+ * Errors: QLORA_ERR_SHAPE (a size < 0 or > 2^31 - 256), QLORA_ERR_UNSUPPORTED.
+ */
+QLORA_EXPORT qlora_status qlora_mx_sizes(int64_t rows, int64_t cols, int32_t format, int32_t scale_per_row,
+                                         size_t* codes_bytes, size_t* scales_bytes, size_t* global_scale_bytes,
+                                         size_t* workspace_bytes);
+
+/*
+ * Quantises a bf16 matrix.  transpose = 0: W is [out->rows, out->cols]; 1: W is
+ * [out->cols, out->rows] and its transpose is what is quantised (blocks along
+ * W's rows: the backward operand of a weight).  transpose with scale_per_row is
+ * QLORA_ERR_UNSUPPORTED.  A zero-sized matrix is a no-op.
+ */
+QLORA_EXPORT qlora_status qlora_mx_quantize(const uint16_t* W, int32_t transpose, const qlora_mx_tensor* out,
+                                            void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
+/*
+ * W_out [rows, cols] bf16 = the values, rounded to nearest (exact for what the
+ * encoder wrote, unless the value is below bf16's smallest subnormal).
+ */
+QLORA_EXPORT qlora_status qlora_mx_dequantize(const qlora_mx_tensor* W, uint16_t* W_out, qlora_stream_t stream);
+
+/*
  * Device error flag of the calling thread's current device: bit 0 is set when
  * a kernel's internal wait gave up after its time limit (a bug, reported
  * instead of hanging); bit 2 when a kernel's shared-memory window did not fit
