@@ -16,7 +16,7 @@
 #include "gemm.h"
 #include "gemv.h"
 #include "internal.h"
-#include "lora.h"
+#include "lora_branch.h"
 #include "nf4_tables.h"
 #include "qlora.h"
 
@@ -157,78 +157,17 @@ const float* plain_absmax(const qlora_nf4_tensor* t) { return t->blocksize2 == 0
 qlora_status cuda_status(cudaError_t e) { return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA; }
 
 // ------------------------------------------------------------------ linear layout
-struct LinearShape {
-  int64_t rows, cols, m;
-  int r, rpad, lora_steps;
-  bool decode;      // M <= 16: token tile 16, split-K
-};
-
 qlora_status check_linear(const qlora_nf4_tensor* W, int64_t M, int32_t r, LinearShape* sh) {
-  qlora_status st = check_tensor(W);
-  if (st != QLORA_OK) return st;
-  if (M < 1 || M > kMaxDim) return QLORA_ERR_SHAPE;
-  if (W->rows < 8 || W->cols < 64 || W->cols % 64 != 0 || W->rows % 8 != 0) return QLORA_ERR_SHAPE;
-  if (r < 8 || r > 256 || r % 8 != 0) return QLORA_ERR_SHAPE;
-  sh->rows = W->rows;
-  sh->cols = W->cols;
-  sh->m = M;
-  sh->r = r;
-  sh->lora_steps = (r + 63) / 64;
-  sh->rpad = 64 * sh->lora_steps;
-  sh->decode = M <= 16;
-  return QLORA_OK;
-}
-
-// Work buffer layout: fp32 accumulators first (one memset clears them all),
-// then bf16 staging.  Offsets in bytes, each 256-aligned.
-// The work buffer's split slots are sized independently of the device (for up
-// to this many SMs); a launch picks its own split count within that space.
-constexpr int kSizingSms = 256;
-constexpr int kMaxRankSplits = 32;
-
-// One rank-r contraction's tiling: tiles of 128 rows x 64 columns, K splits.
-struct RankPlan {
-  int m_tiles, n_tiles, ksteps, splits;
-  int tiles() const { return m_tiles * n_tiles; }
-};
-RankPlan rank_tiling(int64_t mdim, int64_t contraction, int lora_steps) {
-  RankPlan p;
-  p.m_tiles = static_cast<int>((mdim + 127) / 128);
-  p.n_tiles = lora_steps;
-  p.ksteps = static_cast<int>((contraction + 63) / 64);
-  p.splits = 1;
-  return p;
-}
-// Splits of a launch with `tiles` tiles in all (the problems of one launch
-// share them) and `ksteps` k-steps, within `slot_bytes` of slot space.
-int launch_splits(int tiles, int ksteps, int num_sms, size_t slot_bytes) {
-  // a split count s > 1 needs tiles * s partial tiles of slot space
-  const size_t per_split = static_cast<size_t>(tiles) * 64 * 128 * sizeof(float);
-  size_t cap = kMaxRankSplits;
-  if (per_split > 0 && slot_bytes / per_split < cap) cap = slot_bytes / per_split;
-  return rank_splits(tiles, ksteps, num_sms, cap < 2 ? 1 : static_cast<int>(cap));
-}
-// The plan of a launch must fit its slot region; checked before every launch.
-bool slots_fit(int tiles, int splits, size_t slot_bytes) {
-  return rank_slot_bytes(tiles, splits) <= slot_bytes;
-}
-// Slot space of a launch: the most any of these SM counts plans for, so a
-// buffer sized without a device lets the launch use its own best split count.
-size_t sized_slots(int tiles, int ksteps) {
-  static const int kSmCounts[] = {96, 108, 114, 120, 128, 132, 144, 148, 152, 160, 170, 188, 192, 224, kSizingSms};
-  size_t most = 0;
-  for (int sms : kSmCounts) {
-    const size_t b = rank_slot_bytes(tiles, rank_splits(tiles, ksteps, sms, kMaxRankSplits));
-    if (b > most) most = b;
-  }
-  return most;
+  const qlora_status st = check_tensor(W);
+  return st != QLORA_OK ? st : linear_shape(W->rows, W->cols, M, r, sh);
 }
 
 // Work buffer layout: the region cleared by one memset first (counters, and
 // the decode backward's split-K dX accumulator), then the rest.  Offsets in
 // bytes, each 256-aligned; every size is independent of the device.
 struct FwdLayout {
-  size_t cnt, slots, xa_slices, sxa, rank_cnt, rank_slots, rank_slot_bytes, clear_end, total;
+  size_t cnt, slots, xa_slices, total;
+  XaLayout xa;
 };
 FwdLayout fwd_layout(const LinearShape& s) {
   FwdLayout l{};
@@ -239,52 +178,11 @@ FwdLayout fwd_layout(const LinearShape& s) {
     l.cnt = o;      o = round_up(o + m_tiles * 8 * 4, 256);
     l.slots = o;    o = round_up(o + size_t(gemv_slot_floats(int64_t(m_tiles), int64_t(steps))) * 4, 256);
     l.xa_slices = o; o = round_up(o + size_t(kMaxXaSplits) * 16 * s.rpad * 4, 256);
-    l.clear_end = 0;
     l.total = o;
     return l;
   }
-  // k_rank (X A^T -> bf16(s X A^T)) then the fused dequant-GEMM
-  const RankPlan xa = rank_tiling(s.m, s.cols, s.lora_steps);
-  l.rank_cnt = o;   o = round_up(o + size_t(xa.tiles()) * 4, 256);
-  l.clear_end = o;
-  l.rank_slot_bytes = sized_slots(xa.tiles(), xa.ksteps);
-  l.rank_slots = o; o = round_up(o + l.rank_slot_bytes, 256);
-  l.sxa = o;        o = round_up(o + size_t(s.m) * s.rpad * 2, 256);
-  l.total = o;
-  return l;
-}
-
-// Backward: launch 1 = dY B (and X A^T when it is not supplied), launch 2 =
-// the fused dX, launch 3 = dY^T (s X A^T) and X^T (s dY B) (more than 16
-// tokens; with fewer, k_small_grads from the fp32 G and X A^T).  Launch 1's
-// slot space covers both of its forms.
-struct BwdLayout {
-  size_t cnt1, cnt2, dx_acc, clear_end, slots1, slots1_bytes, slots2, slots2_bytes, g, xa, sg, sxa, total;
-  RankPlan g_plan, xa_plan, db_plan, da_plan;
-};
-BwdLayout bwd_layout(const LinearShape& s) {
-  BwdLayout l{};
-  l.g_plan = rank_tiling(s.m, s.rows, s.lora_steps);
-  l.xa_plan = rank_tiling(s.m, s.cols, s.lora_steps);
-  l.db_plan = rank_tiling(s.rows, s.m, s.lora_steps);
-  l.da_plan = rank_tiling(s.cols, s.m, s.lora_steps);
-  const int k1 = l.g_plan.ksteps > l.xa_plan.ksteps ? l.g_plan.ksteps : l.xa_plan.ksteps;
-  const size_t alone = sized_slots(l.g_plan.tiles(), l.g_plan.ksteps);
-  const size_t both = sized_slots(l.g_plan.tiles() + l.xa_plan.tiles(), k1);
-  l.slots1_bytes = alone > both ? alone : both;
-  l.slots2_bytes = s.decode ? 0 : sized_slots(l.db_plan.tiles() + l.da_plan.tiles(), l.db_plan.ksteps);
-  size_t o = 0;
-  l.cnt1 = o;   o = round_up(o + size_t(l.g_plan.tiles() + l.xa_plan.tiles()) * 4, 256);
-  l.cnt2 = o;   o = round_up(o + size_t(l.db_plan.tiles() + l.da_plan.tiles()) * 4, 256);
-  l.dx_acc = o; if (s.decode) o = round_up(o + size_t(s.m) * s.cols * 4, 256);
-  l.clear_end = o;
-  l.slots1 = o; o = round_up(o + l.slots1_bytes, 256);
-  l.slots2 = o; o = round_up(o + l.slots2_bytes, 256);
-  l.g = o;      if (s.decode) o = round_up(o + size_t(s.m) * s.rpad * 4, 256);
-  l.xa = o;     if (s.decode) o = round_up(o + size_t(s.m) * s.rpad * 4, 256);
-  l.sg = o;     o = round_up(o + size_t(s.m) * s.rpad * 2, 256);
-  l.sxa = o;    o = round_up(o + size_t(s.m) * s.rpad * 2, 256);
-  l.total = o;
+  l.xa = xa_layout(s, 0);      // k_rank (X A^T -> bf16(s X A^T)) then the fused dequant-GEMM
+  l.total = l.xa.end;
   return l;
 }
 
@@ -293,24 +191,6 @@ int choose_splits(int tiles, int ksteps, int num_sms) {
   if (sp > ksteps) sp = ksteps;
   if (sp < 1) sp = 1;
   return sp;
-}
-
-// One rank-r problem of a k_rank launch.
-RankProblem rank_problem(const RankPlan& pl, int64_t mdim, int64_t ndim, bool a_mn, bool b_mn, int unit_begin,
-                         float* slots, uint32_t* counters) {
-  RankProblem p{};
-  p.mdim = mdim;
-  p.ndim = ndim;
-  p.ksteps = pl.ksteps;
-  p.m_tiles = pl.m_tiles;
-  p.n_tiles = pl.n_tiles;
-  p.splits = pl.splits;
-  p.unit_begin = unit_begin;
-  p.a_mn = a_mn ? 1 : 0;
-  p.b_mn = b_mn ? 1 : 0;
-  p.slots = slots;
-  p.counters = counters;
-  return p;
 }
 
 // Decode-shaped forward (M <= 16): X A^T slices and the zeroed tile counters
@@ -512,17 +392,9 @@ qlora_status qlora_dequantize(const qlora_nf4_tensor* W, uint16_t* W_out, qlora_
 
 qlora_status qlora_linear_workspace_size(int64_t rows, int64_t cols, int64_t M, int32_t r,
                                          size_t* fwd_bytes, size_t* bwd_bytes) {
-  if (rows < 8 || cols < 64 || rows > kMaxDim || cols > kMaxDim || cols % 64 || rows % 8)
-    return QLORA_ERR_SHAPE;
-  if (M < 1 || M > kMaxDim || r < 8 || r > 256 || r % 8) return QLORA_ERR_SHAPE;
   LinearShape sh;
-  sh.rows = rows;
-  sh.cols = cols;
-  sh.m = M;
-  sh.r = r;
-  sh.lora_steps = (r + 63) / 64;
-  sh.rpad = 64 * sh.lora_steps;
-  sh.decode = M <= 16;
+  const qlora_status st = linear_shape(rows, cols, M, r, &sh);
+  if (st != QLORA_OK) return st;
   if (fwd_bytes) *fwd_bytes = fwd_layout(sh).total;
   if (bwd_bytes) *bwd_bytes = bwd_layout(sh).total;
   return QLORA_OK;
@@ -552,24 +424,8 @@ qlora_status qlora_linear_fwd(const qlora_nf4_tensor* W, const uint16_t* X, int6
 
   // 1) X A^T (fp32 to XA_out when asked) and bf16(s X A^T), zero-padded to a
   //    multiple of 64 columns, as the LoRA k-step operand of the fused GEMM
-  uint16_t* sxa = reinterpret_cast<uint16_t*>(ws + L.sxa);
-  RankPlan xp = rank_tiling(sh.m, sh.cols, sh.lora_steps);
-  xp.splits = launch_splits(xp.tiles(), xp.ksteps, d.num_sms, L.rank_slot_bytes);
-  if (!slots_fit(xp.tiles(), xp.splits, L.rank_slot_bytes)) return QLORA_ERR_WORKSPACE;
-  if (xp.splits > 1 && cudaMemsetAsync(ws, 0, L.clear_end, cs) != cudaSuccess) return QLORA_ERR_CUDA;
-  CUtensorMap x_k, a_k;
-  if (!make_map(&x_k, X, sh.cols, sh.m, sh.cols * 2, 128) ||
-      !make_map(&a_k, A, sh.cols, sh.r, sh.cols * 2, 64))
-    return QLORA_ERR_CUDA;
-  RankArgs ra{};
-  ra.p[0] = rank_problem(xp, sh.m, sh.r, false, false, 0, reinterpret_cast<float*>(ws + L.rank_slots),
-                         reinterpret_cast<uint32_t*>(ws + L.rank_cnt));
-  ra.p[0].out_f32 = XA_out; ra.p[0].ld_f32 = sh.r;
-  ra.p[0].out_bf16 = sxa; ra.p[0].ld_bf16 = sh.rpad; ra.p[0].bf16_cols = sh.rpad; ra.p[0].bf16_scale = s;
-  ra.nprob = 1;
-  ra.total_units = xp.tiles() * xp.splits;
-  ra.err = d.err;
-  if (counted(launch_rank(ra, x_k, a_k, x_k, a_k, d.num_sms, cs)) != cudaSuccess) return QLORA_ERR_CUDA;
+  uint16_t* sxa = reinterpret_cast<uint16_t*>(ws + L.xa.sxa);
+  if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, RankDivide(), d, cs)) != QLORA_OK) return st;
 
   // 2) Y = X deq(W)^T + (s XA) B^T  (fused dequant GEMM)
   const int bn = 256;
@@ -637,57 +493,11 @@ qlora_status qlora_linear_bwd(const qlora_nf4_tensor* W, const uint16_t* X, cons
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* dx_acc = reinterpret_cast<float*>(ws + L.dx_acc);
-  float* g32 = sh.decode ? reinterpret_cast<float*>(ws + L.g) : nullptr;     // fp32 G and X A^T: few-token grads
-  float* xa32 = sh.decode ? reinterpret_cast<float*>(ws + L.xa) : nullptr;
   uint16_t* sg = reinterpret_cast<uint16_t*>(ws + L.sg);
-  uint16_t* sxa = reinterpret_cast<uint16_t*>(ws + L.sxa);
-  const bool recompute = XA == nullptr;
-
-  if (L.clear_end && cudaMemsetAsync(ws, 0, L.clear_end, cs) != cudaSuccess) return QLORA_ERR_CUDA;
 
   // 1) G = dY B -> bf16(s G) (+ fp32 G for few tokens), and X A^T -> bf16(s X A^T)
   //    (recomputed when not supplied, else converted from the caller's fp32)
-  CUtensorMap dy_k, b_mn, x_k, a_k;
-  if (!make_map(&dy_k, dY, sh.rows, sh.m, sh.rows * 2, 128) ||
-      !make_map(&b_mn, B, sh.r, sh.rows, sh.r * 2, 64) ||
-      !make_map(&x_k, X, sh.cols, sh.m, sh.cols * 2, 128) ||
-      !make_map(&a_k, A, sh.cols, sh.r, sh.cols * 2, 64))
-    return QLORA_ERR_CUDA;
-  {
-    // splits for this device and this form of launch 1, within the slot space
-    if (recompute) {
-      const int k1 = L.g_plan.ksteps > L.xa_plan.ksteps ? L.g_plan.ksteps : L.xa_plan.ksteps;
-      L.g_plan.splits = L.xa_plan.splits =
-          launch_splits(L.g_plan.tiles() + L.xa_plan.tiles(), k1, d.num_sms, L.slots1_bytes);
-    } else {
-      L.g_plan.splits = launch_splits(L.g_plan.tiles(), L.g_plan.ksteps, d.num_sms, L.slots1_bytes);
-    }
-    if (!slots_fit(L.g_plan.tiles() + (recompute ? L.xa_plan.tiles() : 0), L.g_plan.splits, L.slots1_bytes))
-      return QLORA_ERR_WORKSPACE;
-    RankArgs ra{};
-    uint32_t* cnt = reinterpret_cast<uint32_t*>(ws + L.cnt1);
-    float* slots = reinterpret_cast<float*>(ws + L.slots1);
-    ra.p[0] = rank_problem(L.g_plan, sh.m, sh.r, false, true, 0, slots, cnt);
-    ra.p[0].out_f32 = g32; ra.p[0].ld_f32 = sh.rpad;
-    ra.p[0].out_bf16 = sg; ra.p[0].ld_bf16 = sh.rpad; ra.p[0].bf16_cols = sh.rpad; ra.p[0].bf16_scale = s;
-    ra.nprob = 1;
-    ra.total_units = L.g_plan.tiles() * L.g_plan.splits;
-    if (recompute) {
-      ra.p[1] = rank_problem(L.xa_plan, sh.m, sh.r, false, false, ra.total_units,
-                             slots + rank_slot_bytes(L.g_plan.tiles(), L.g_plan.splits) / 4,
-                             cnt + L.g_plan.tiles());
-      ra.p[1].out_f32 = xa32; ra.p[1].ld_f32 = sh.rpad;
-      ra.p[1].out_bf16 = sh.decode ? nullptr : sxa;
-      ra.p[1].ld_bf16 = sh.rpad; ra.p[1].bf16_cols = sh.rpad; ra.p[1].bf16_scale = s;
-      ra.nprob = 2;
-      ra.total_units += L.xa_plan.tiles() * L.xa_plan.splits;
-    } else if (!sh.decode) {
-      ra.cvt_in = XA; ra.cvt_rows = sh.m; ra.cvt_cols = sh.r; ra.cvt_ld_in = sh.r;
-      ra.cvt_out = sxa; ra.cvt_ld_out = sh.rpad; ra.cvt_cols_out = sh.rpad; ra.cvt_scale = s;
-    }
-    ra.err = d.err;
-    if (counted(launch_rank(ra, dy_k, b_mn, x_k, a_k, d.num_sms, cs)) != cudaSuccess) return QLORA_ERR_CUDA;
-  }
+  if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L, RankDivide(), d, cs)) != QLORA_OK) return st;
 
   // 2) dX = dY deq(W) + (s G) A   (fused dequant GEMM, deq(W)^T as the MN-major operand)
   if (dX) {
@@ -718,42 +528,8 @@ qlora_status qlora_linear_bwd(const qlora_nf4_tensor* W, const uint16_t* X, cons
       return QLORA_ERR_CUDA;
   }
 
-  // 3) LoRA gradients.  Few tokens: fp32 on CUDA cores from the fp32 G and X A^T.
-  if (sh.decode) {
-    const float* xa = recompute ? xa32 : XA;
-    const int64_t ld_xa = recompute ? sh.rpad : sh.r;
-    if (counted(launch_small_grads(g32, sh.rpad, xa, ld_xa, X, dY, sh.m, sh.rows, sh.cols, sh.r, s,
-                                   dA, dB, d.num_sms, cs)) != cudaSuccess)
-      return QLORA_ERR_CUDA;
-    return QLORA_OK;
-  }
-  //    Many tokens, one launch of two contractions over the tokens (bf16 operands):
-  //    dB = dY^T (s X A^T) [rows, r] and dA = (X^T (s G))^T [r, cols], stored transposed.
-  CUtensorMap dy_mn, sxa_mn, x_mn, sg_mn;
-  if (!make_map(&dy_mn, dY, sh.rows, sh.m, sh.rows * 2, 64) ||
-      !make_map(&sxa_mn, sxa, sh.rpad, sh.m, sh.rpad * 2, 64) ||
-      !make_map(&x_mn, X, sh.cols, sh.m, sh.cols * 2, 64) ||
-      !make_map(&sg_mn, sg, sh.rpad, sh.m, sh.rpad * 2, 64))
-    return QLORA_ERR_CUDA;
-  L.db_plan.splits = L.da_plan.splits =
-      launch_splits(L.db_plan.tiles() + L.da_plan.tiles(), L.db_plan.ksteps, d.num_sms, L.slots2_bytes);
-  if (!slots_fit(L.db_plan.tiles() + L.da_plan.tiles(), L.db_plan.splits, L.slots2_bytes))
-    return QLORA_ERR_WORKSPACE;
-  RankArgs rb{};
-  uint32_t* cnt2 = reinterpret_cast<uint32_t*>(ws + L.cnt2);
-  float* slots2 = reinterpret_cast<float*>(ws + L.slots2);
-  rb.p[0] = rank_problem(L.db_plan, sh.rows, sh.r, true, true, 0, slots2, cnt2);
-  rb.p[0].out_f32 = dB; rb.p[0].ld_f32 = sh.r;
-  const int u0 = L.db_plan.tiles() * L.db_plan.splits;
-  rb.p[1] = rank_problem(L.da_plan, sh.cols, sh.r, true, true, u0,
-                         slots2 + rank_slot_bytes(L.db_plan.tiles(), L.db_plan.splits) / 4,
-                         cnt2 + L.db_plan.tiles());
-  rb.p[1].out_f32 = dA; rb.p[1].ld_f32 = sh.cols; rb.p[1].transpose = 1;
-  rb.nprob = 2;
-  rb.total_units = u0 + L.da_plan.tiles() * L.da_plan.splits;
-  rb.err = d.err;
-  if (counted(launch_rank(rb, dy_mn, sxa_mn, x_mn, sg_mn, d.num_sms, cs)) != cudaSuccess) return QLORA_ERR_CUDA;
-  return QLORA_OK;
+  // 3) LoRA gradients
+  return run_lora_grads(sh, X, dY, s, XA, dA, dB, ws, &L, d, cs);
 }
 
 qlora_status qlora_read_device_errors(uint32_t* flags, int clear) {

@@ -73,6 +73,23 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// bf16(s * v) of row `row`, columns c0 .. c0 + 63 below bf16_cols; columns past
+// ndim hold zeros (zero-filled operand).
+__device__ __forceinline__ void store_bf16_row(const RankProblem& p, uint16_t* out, int64_t row, int64_t c0,
+                                               const float (&v)[64], float s) {
+  uint16_t* dst = out + row * p.ld_bf16 + c0;
+#pragma unroll
+  for (int c = 0; c < 64; c += 8)
+    if (c0 + c < p.bf16_cols) {
+      uint4 q;
+      q.x = pack_bf16x2(__fmul_rn(s, v[c]), __fmul_rn(s, v[c + 1]));
+      q.y = pack_bf16x2(__fmul_rn(s, v[c + 2]), __fmul_rn(s, v[c + 3]));
+      q.z = pack_bf16x2(__fmul_rn(s, v[c + 4]), __fmul_rn(s, v[c + 5]));
+      q.w = pack_bf16x2(__fmul_rn(s, v[c + 6]), __fmul_rn(s, v[c + 7]));
+      *reinterpret_cast<uint4*>(dst + c) = q;
+    }
+}
+
 // The final values of row `row`, columns c0 .. c0 + 63 of problem p's D.
 __device__ __forceinline__ void store_final(const RankProblem& p, int64_t row, int64_t c0, const float (&v)[64]) {
   if (row >= p.mdim) return;
@@ -88,20 +105,8 @@ __device__ __forceinline__ void store_final(const RankProblem& p, int64_t row, i
         if (c0 + c < p.ndim) *reinterpret_cast<float4*>(dst + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
     }
   }
-  if (p.out_bf16) {
-    uint16_t* dst = p.out_bf16 + row * p.ld_bf16 + c0;
-#pragma unroll
-    for (int c = 0; c < 64; c += 8)
-      if (c0 + c < p.bf16_cols) {           // columns past ndim hold zeros (zero-filled operand)
-        const float s = p.bf16_scale;
-        uint4 q;
-        q.x = pack_bf16x2(__fmul_rn(s, v[c]), __fmul_rn(s, v[c + 1]));
-        q.y = pack_bf16x2(__fmul_rn(s, v[c + 2]), __fmul_rn(s, v[c + 3]));
-        q.z = pack_bf16x2(__fmul_rn(s, v[c + 4]), __fmul_rn(s, v[c + 5]));
-        q.w = pack_bf16x2(__fmul_rn(s, v[c + 6]), __fmul_rn(s, v[c + 7]));
-        *reinterpret_cast<uint4*>(dst + c) = q;
-      }
-  }
+  if (p.out_bf16) store_bf16_row(p, p.out_bf16, row, c0, v, p.bf16_scale);
+  if (p.out_div) store_bf16_row(p, p.out_div, row, c0, v, p.bf16_scale / (p.row_div[row] * p.all_div[0]));
 }
 
 __global__ void __launch_bounds__(kThreads, 1)

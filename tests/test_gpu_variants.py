@@ -166,3 +166,24 @@ def test_linear_variants_full_size(qb, quant_type, dq):
     rows = np.sort(rng.choice(8192, 64, replace=False))
     _linear_variant(qb, quant_type, dq, 8192, 8192, 8192, 64, proj=1, rows_sample=rows)
     _linear_variant(qb, quant_type, dq, 8192, 8192, 4, 64, proj=1, check_bwd=False)
+
+
+@pytest.mark.parametrize("n,k,m,r", [(136, 1024, 129, 136), (72, 4096, 40, 64), (1024, 64, 129, 136)])
+def test_bwd_recomputed_xa_of_a_much_longer_contraction(qb, n, k, m, r):
+    """dY B (contraction n) and the recomputed X A^T (contraction k) share a
+    launch whose split count follows the longer one; a split of the shorter one
+    that is left without a k-step must not add anything."""
+    s = 16.0 / r
+    w, X, A = workloads.weight((n, k)), workloads.activations(m, k), workloads.lora_a(r, k)
+    B, dY = workloads.lora_b(n, r), workloads.grad_output(m, n)
+    qt = qb.qlora_quantize_nf4_dq(w.cuda())
+    filler = torch.full((64, 1 << 20), float("nan"), device="cuda")          # leave NaN where work buffers will be
+    del filler
+    dX, dA, dB = qb.qlora_linear_bwd(qt, X.cuda(), dY.cuda(), A.cuda(), B.cuda(), s)
+    torch.cuda.synchronize()
+    assert qb.qlora_read_device_errors() == 0
+    Wd = oracle.dequant_tensor(oracle.quantize(workloads.bf16_bits(w)))
+    ref = oracle.linear_bwd(Wd, *[t.float().numpy() for t in (X, dY, A, B)], s)
+    for name, got, want in zip(("dX", "dA", "dB"), (dX, dA, dB), ref):
+        err = np.max(np.abs(got.float().cpu().numpy() - want)) / np.sqrt(np.mean(want * want))
+        assert err <= 2e-2, f"{name}: {err}"
