@@ -16,6 +16,8 @@ Entry points (same names as the C ABI):
 Microscaled 4-bit formats (MXFP4, NVFP4):
     qlora_mx_quantize(W, fmt, transpose, per_row)     -> MXTensor
     qlora_mx_dequantize(q)                            -> bf16 [rows, cols]
+    qlora_mx_linear_fwd(q, X, A, B, s)                -> (Y bf16, XA fp32 or None)
+    qlora_mx_linear_bwd(qT, dY, X, A, B, s, XA)       -> (dX bf16 or None, dA fp32, dB fp32)
 """
 from __future__ import annotations
 
@@ -100,12 +102,20 @@ _lib.qlora_mx_quantize.argtypes = [_vp, _i32, _MX, _vp, _sz, _vp]
 _lib.qlora_mx_quantize.restype = ctypes.c_int
 _lib.qlora_mx_dequantize.argtypes = [_MX, _vp, _vp]
 _lib.qlora_mx_dequantize.restype = ctypes.c_int
+_lib.qlora_mx_linear_workspace_size.argtypes = [_i64, _i64, _i32, _i64, _i32, _szp, _szp]
+_lib.qlora_mx_linear_workspace_size.restype = ctypes.c_int
+_lib.qlora_mx_linear_fwd.argtypes = [_MX, _vp, _i64, _vp, _vp, _i32, ctypes.c_float, _vp, _vp, _vp, _sz, _vp]
+_lib.qlora_mx_linear_fwd.restype = ctypes.c_int
+_lib.qlora_mx_linear_bwd.argtypes = [_MX, _vp, _vp, _i64, _vp, _vp, _i32, ctypes.c_float, _vp, _vp, _vp, _vp, _vp,
+                                     _sz, _vp]
+_lib.qlora_mx_linear_bwd.restype = ctypes.c_int
 
 EXPORTED = ["qlora_status_string", "qlora_get_codebook", "qlora_get_levels", "qlora_nf4_sizes", "qlora_quantize_nf4_dq",
             "qlora_dequantize", "qlora_linear_workspace_size", "qlora_linear_fwd", "qlora_linear_fwd_multi",
             "qlora_linear_bwd", "qlora_read_device_errors", "qlora_kernel_launches",
             "qlora_time_next_gemm", "qlora_quantize_nf4_dq_noalloc", "qlora_selftest_bounded_wait",
-            "qlora_mx_sizes", "qlora_mx_quantize", "qlora_mx_dequantize"]
+            "qlora_mx_sizes", "qlora_mx_quantize", "qlora_mx_dequantize",
+            "qlora_mx_linear_workspace_size", "qlora_mx_linear_fwd", "qlora_mx_linear_bwd"]
 
 # Largest weight the allocation-free quantize variant accepts.
 NOALLOC_MAX_ELEMENTS = 134217728
@@ -505,3 +515,99 @@ def _addr(t):
 def _size(t) -> int:
     """Bytes of a work buffer (0 for none)."""
     return 0 if t is None else t.numel() * t.element_size()
+
+
+def qlora_mx_linear_workspace_size(rows: int, cols: int, fmt: str, m: int, r: int = 0) -> tuple:
+    """(forward, backward) work-buffer bytes of a layer W [rows, cols]; r = 0: no adapter."""
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(_lib.qlora_mx_linear_workspace_size(rows, cols, MX_FORMATS[fmt], m, r, f, b), "qlora_mx_linear_workspace_size")
+    return f.value, b.value
+
+
+def _need(name: str, t: torch.Tensor, dtype, shape: tuple, device):
+    if not (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _mx_workspace(workspace, need: int, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def qlora_mx_linear_fwd(q: MXTensor, X: torch.Tensor, A: torch.Tensor | None = None, B: torch.Tensor | None = None,
+                        s: float = 0.0, save_xa: bool = True, Y: torch.Tensor | None = None,
+                        XA: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Y = deq(q(X)) deq(W)^T [+ s (X A^T) B^T] over a microscaled weight W
+    [rows, cols]; X is quantised in W's format.  Without an adapter (A and B
+    None) any sizes are taken.  Returns (Y bf16, X A^T fp32 or None)."""
+    c, dev = q.c_struct(), q.device
+    m = X.shape[0]
+    _need("X", X, torch.bfloat16, (m, q.cols), dev)
+    r = 0
+    if (A is None) != (B is None):
+        raise ValueError("A and B come together")
+    if A is not None:
+        r = A.shape[0]
+        _need("A", A, torch.bfloat16, (r, q.cols), dev)
+        _need("B", B, torch.bfloat16, (q.rows, r), dev)
+    if Y is None:
+        Y = torch.empty(m, q.rows, dtype=torch.bfloat16, device=dev)
+    else:
+        _need("Y", Y, torch.bfloat16, (m, q.rows), dev)
+    if not (r and save_xa):
+        XA = None
+    elif XA is None:
+        XA = torch.empty(m, r, dtype=torch.float32, device=dev)
+    else:
+        _need("XA", XA, torch.float32, (m, r), dev)
+    workspace = _mx_workspace(workspace, qlora_mx_linear_workspace_size(q.rows, q.cols, q.fmt, m, r)[0], dev)
+    _on(dev, "qlora_mx_linear_fwd", _lib.qlora_mx_linear_fwd, c, X.data_ptr(), m, _addr(A), _addr(B), r, float(s),
+        Y.data_ptr(), _addr(XA), workspace.data_ptr(), _size(workspace))
+    return Y, XA
+
+
+def qlora_mx_linear_bwd(qT: MXTensor, dY: torch.Tensor, X: torch.Tensor | None = None, A: torch.Tensor | None = None,
+                        B: torch.Tensor | None = None, s: float = 0.0, XA: torch.Tensor | None = None,
+                        need_dx: bool = True, dX: torch.Tensor | None = None, dA: torch.Tensor | None = None,
+                        dB: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Backward of qlora_mx_linear_fwd.  qT holds the layer's weight transposed,
+    [cols, rows] (qlora_mx_quantize(W, transpose=True)).  Returns (dX bf16 or
+    None, dA fp32, dB fp32); without an adapter dA and dB are None."""
+    c, dev = qT.c_struct(), qT.device
+    rows, cols, m, r = qT.cols, qT.rows, dY.shape[0], 0
+    _need("dY", dY, torch.bfloat16, (m, rows), dev)
+    if (A is None) != (B is None):
+        raise ValueError("A and B come together")
+    if A is not None:
+        r = A.shape[0]
+        if X is None:
+            raise ValueError("the adapter's gradients need X")
+        _need("X", X, torch.bfloat16, (m, cols), dev)
+        _need("A", A, torch.bfloat16, (r, cols), dev)
+        _need("B", B, torch.bfloat16, (rows, r), dev)
+        if XA is not None:
+            _need("XA", XA, torch.float32, (m, r), dev)
+        if dA is None:
+            dA = torch.empty(r, cols, dtype=torch.float32, device=dev)
+        else:
+            _need("dA", dA, torch.float32, (r, cols), dev)
+        if dB is None:
+            dB = torch.empty(rows, r, dtype=torch.float32, device=dev)
+        else:
+            _need("dB", dB, torch.float32, (rows, r), dev)
+    else:
+        X = XA = dA = dB = None
+    if not need_dx:
+        dX = None
+    elif dX is None:
+        dX = torch.empty(m, cols, dtype=torch.bfloat16, device=dev)
+    else:
+        _need("dX", dX, torch.bfloat16, (m, cols), dev)
+    workspace = _mx_workspace(workspace, qlora_mx_linear_workspace_size(rows, cols, qT.fmt, m, r)[1], dev)
+    _on(dev, "qlora_mx_linear_bwd", _lib.qlora_mx_linear_bwd, c, _addr(X), dY.data_ptr(), m, _addr(A), _addr(B), r,
+        float(s), _addr(XA), _addr(dX), _addr(dA), _addr(dB), workspace.data_ptr(), _size(workspace))
+    return dX, dA, dB

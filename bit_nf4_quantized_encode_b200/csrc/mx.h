@@ -48,4 +48,32 @@ cudaError_t launch_mx_dequant(int fmt, const uint8_t* codes, const uint8_t* scal
                               int per_row, int64_t rows, int64_t cols, int64_t pitch, int64_t kt, uint16_t* out,
                               int num_sms, cudaStream_t stream);
 
+// The product D[token, row] = sum_k x[token, k] w[row, k] of two microscaled
+// operands plus a rank-r bf16 term, on the tensor cores' block-scaled
+// instructions.
+struct MxGemmArgs {
+  const uint8_t* w_scales;   // scale tiles of the weight [rows, k]
+  const uint8_t* x_scales;   // and of the activations [m, k]
+  int64_t kt;                // scale tiles along k (the same for both)
+  const float* w_global;     // NVFP4: [1] or [rows]; null: none
+  int w_per_row;
+  const float* x_global;     // NVFP4: [m]; null: none
+  int64_t rows, m, k;
+  int ksteps;                // ceil(k / 256)
+  int lora_steps;            // 64-wide steps of the rank-r term (0: none)
+  int lora_mn;               // its weight-side operand: 0 [rows, r], 1 [r, rows] (rows contiguous)
+  uint16_t* out;             // bf16 [m, rows]
+  int m_tiles, t_tiles;      // tiles of 128 rows, of the kernel's token tile
+  int m_group;               // row tiles swept across all token tiles before the next group
+  int splits;                // CTAs (one cluster) that share a tile's contraction: 1, 2, 4 or 8
+  uint32_t* err;
+};
+// Token tile for m tokens (16, 32, 64 or 128; below 128 only one tile).
+int mx_token_tile(int64_t m);
+// Tensor maps: w / x the codes as uint8 [rows or m][pitch], 128B swizzle, box
+// {128, 128} / {128, token tile}; lora_w bf16, box {64, 128} ([rows, r]) or
+// {64, 64} ([r, rows]); lora_x bf16 [m, 64 lora_steps], box {64, token tile}.
+cudaError_t launch_mx_gemm(int fmt, const MxGemmArgs& a, const CUtensorMap& w, const CUtensorMap& x,
+                           const CUtensorMap& lora_w, const CUtensorMap& lora_x, int num_sms, cudaStream_t stream);
+
 }  // namespace qlora

@@ -4,9 +4,12 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
+#include "gemm.h"
 #include "internal.h"
+#include "lora_branch.h"
 #include "mx.h"
 #include "qlora.h"
 
@@ -32,6 +35,133 @@ qlora_status check_mx(const qlora_mx_tensor* t) {
 
 size_t quantize_workspace(int format, int per_row) {
   return format == QLORA_NVFP4 && !per_row ? round_up(kMxAmaxGrid * sizeof(uint32_t), 256) : 0;
+}
+
+// ------------------------------------------------------------------ linear layer
+// Quantised activations [m, k] in a work buffer, from offset `base`.
+struct ActLayout {
+  size_t codes, scales, global, end;
+};
+ActLayout act_layout(int format, int64_t m, int64_t k, size_t base) {
+  ActLayout l{};
+  size_t o = base;
+  l.codes = o;  o = round_up(o + static_cast<size_t>(m) * mx_pitch(k), 256);
+  l.scales = o; o = round_up(o + static_cast<size_t>(mx_scale_bytes(format, m, k)), 256);
+  l.global = o; if (format == QLORA_NVFP4) o = round_up(o + static_cast<size_t>(m) * 4, 256);
+  l.end = o;
+  return l;
+}
+
+struct MxFwdLayout {
+  XaLayout xa;
+  ActLayout act;
+};
+MxFwdLayout mx_fwd_layout(int format, int64_t cols, int64_t m, int r, const LinearShape& sh) {
+  MxFwdLayout l{};
+  if (r) l.xa = xa_layout(sh, 0);
+  l.act = act_layout(format, m, cols, l.xa.end);
+  return l;
+}
+struct MxBwdLayout {
+  BwdLayout lora;
+  size_t sg_div;           // NVFP4: bf16(s G / (gx gw))
+  ActLayout act;
+};
+MxBwdLayout mx_bwd_layout(int format, int64_t rows, int64_t m, int r, const LinearShape& sh) {
+  MxBwdLayout l{};
+  if (r) l.lora = bwd_layout(sh);
+  size_t o = round_up(l.lora.total, 256);
+  l.sg_div = o;
+  if (r && format == QLORA_NVFP4) o = round_up(o + static_cast<size_t>(m) * sh.rpad * 2, 256);
+  l.act = act_layout(format, m, rows, o);
+  return l;
+}
+
+// Sizes of the layer W [rows, cols] with M tokens and rank r (0: no adapter).
+qlora_status mx_layer_shape(int64_t rows, int64_t cols, int64_t M, int32_t r, LinearShape* sh) {
+  if (r != 0) return rows > kMxMaxDim || cols > kMxMaxDim || M > kMxMaxDim ? QLORA_ERR_SHAPE
+                                                                             : linear_shape(rows, cols, M, r, sh);
+  if (rows < 1 || cols < 1 || rows > kMxMaxDim || cols > kMxMaxDim || M < 1 || M > kMxMaxDim) return QLORA_ERR_SHAPE;
+  return QLORA_OK;
+}
+
+// K splits (CTAs of one cluster) of a product of `tiles` tiles: as many as
+// leave every CTA two k-steps and do not exceed two CTAs an SM.
+int mx_splits(int64_t tiles, int ksteps, int num_sms) {
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= 2 * static_cast<int64_t>(num_sms) && ksteps >= 4 * s) s *= 2;
+  return s;
+}
+
+// Row tiles swept across all token tiles before the next group: about 48 MB of
+// weight codes, so that they stay in L2 meanwhile.
+int mx_group(int m_tiles, int64_t pitch) {
+  int64_t g = (int64_t{48} << 20) / (128 * pitch);
+  if (g < 1) g = 1;
+  return static_cast<int>(g > m_tiles ? m_tiles : g);
+}
+
+// q(X) into the work buffer (NVFP4: a global scale per token).
+cudaError_t quantize_acts(const qlora_mx_tensor* W, const uint16_t* X, int64_t M, uint8_t* ws, const ActLayout& L,
+                          const DeviceInfo& d, cudaStream_t cs) {
+  MxQuantArgs a{};
+  a.in = X;
+  a.in_rows = a.rows = a.tile_rows = M;
+  a.in_cols = a.cols = W->cols;
+  a.codes = ws + L.codes;
+  a.scales = ws + L.scales;
+  a.global_scale = reinterpret_cast<float*>(ws + L.global);
+  a.pitch = mx_pitch(W->cols);
+  a.kt = mx_tiles_k(W->format, W->cols);
+  a.per_row = W->format == QLORA_NVFP4;
+  return counted(launch_mx_quant(W->format, false, a, d.num_sms, cs));
+}
+
+// out [M, W->rows] = q(X) deq(W)^T + lora_x lora_w (see mx_gemm.cu).
+qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const ActLayout& L, const uint16_t* lora_w,
+                         bool lora_mn, const uint16_t* lora_x, int r, int lora_steps, uint16_t* out,
+                         const DeviceInfo& d, cudaStream_t cs) {
+  const int bn = mx_token_tile(M);
+  const int64_t pitch = mx_pitch(W->cols);
+  MxGemmArgs a{};
+  a.w_scales = W->scales;
+  a.x_scales = ws + L.scales;
+  a.kt = mx_tiles_k(W->format, W->cols);
+  if (W->format == QLORA_NVFP4) {
+    a.w_global = W->global_scale;
+    a.w_per_row = W->scale_per_row;
+    a.x_global = reinterpret_cast<const float*>(ws + L.global);
+  }
+  a.rows = W->rows;
+  a.m = M;
+  a.k = W->cols;
+  a.ksteps = static_cast<int>((W->cols + 255) / 256);
+  a.lora_steps = lora_steps;
+  a.lora_mn = lora_mn ? 1 : 0;
+  a.out = out;
+  const int64_t m_tiles = (W->rows + 127) / 128, t_tiles = (M + bn - 1) / bn;
+  if (m_tiles * t_tiles > (int64_t{1} << 28)) return QLORA_ERR_SHAPE;
+  a.m_tiles = static_cast<int>(m_tiles);
+  a.t_tiles = static_cast<int>(t_tiles);
+  a.m_group = mx_group(a.m_tiles, pitch);
+  a.splits = mx_splits(m_tiles * t_tiles, a.ksteps, d.num_sms);
+  a.err = d.err;
+  CUtensorMap w, x, lw, lx;
+  const uint64_t up = static_cast<uint64_t>(pitch);
+  if (!make_map_u8(&w, W->codes, up, static_cast<uint64_t>(W->rows), up, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map_u8(&x, ws + L.codes, up, static_cast<uint64_t>(M), up, 128, static_cast<uint32_t>(bn),
+                   CU_TENSOR_MAP_SWIZZLE_128B))
+    return QLORA_ERR_CUDA;
+  if (lora_steps) {
+    const uint64_t rpad = static_cast<uint64_t>(lora_steps) * 64, n = static_cast<uint64_t>(W->rows);
+    if (!(lora_mn ? make_map(&lw, lora_w, n, r, n * 2, 64) : make_map(&lw, lora_w, r, n, static_cast<uint64_t>(r) * 2, 128)) ||
+        !make_map(&lx, lora_x, rpad, static_cast<uint64_t>(M), rpad * 2, static_cast<uint32_t>(bn)))
+      return QLORA_ERR_CUDA;
+  } else {
+    lw = w;
+    lx = x;
+  }
+  return counted(launch_mx_gemm(W->format, a, w, x, lw, lx, d.num_sms, cs)) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 }  // namespace
@@ -104,6 +234,90 @@ qlora_status qlora_mx_dequantize(const qlora_mx_tensor* W, uint16_t* W_out, qlor
                                    reinterpret_cast<cudaStream_t>(stream))) == cudaSuccess
              ? QLORA_OK
              : QLORA_ERR_CUDA;
+}
+
+qlora_status qlora_mx_linear_workspace_size(int64_t rows, int64_t cols, int32_t format, int64_t M, int32_t r,
+                                            size_t* fwd_bytes, size_t* bwd_bytes) {
+  if (format != QLORA_MXFP4 && format != QLORA_NVFP4) return QLORA_ERR_UNSUPPORTED;
+  LinearShape sh{};
+  const qlora_status st = mx_layer_shape(rows, cols, M, r, &sh);
+  if (st != QLORA_OK) return st;
+  if (fwd_bytes) *fwd_bytes = mx_fwd_layout(format, cols, M, r, sh).act.end;
+  if (bwd_bytes) *bwd_bytes = mx_bwd_layout(format, rows, M, r, sh).act.end;
+  return QLORA_OK;
+}
+
+qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, int64_t M, const uint16_t* A,
+                                 const uint16_t* B, int32_t r, float s, uint16_t* Y, float* XA_out, void* workspace,
+                                 size_t workspace_bytes, qlora_stream_t stream) {
+  qlora_status st = check_mx(W);
+  if (st != QLORA_OK) return st;
+  LinearShape sh{};
+  if ((st = mx_layer_shape(W->rows, W->cols, M, r, &sh)) != QLORA_OK) return st;
+  if (r && W->scale_per_row) return QLORA_ERR_UNSUPPORTED;
+  if (!X || !Y || !workspace || (r && (!A || !B))) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(workspace) ||
+      (r && (!aligned16(A) || !aligned16(B) || (XA_out && !aligned16(XA_out)))))
+    return QLORA_ERR_ALIGN;
+  if (r && !std::isfinite(s)) return QLORA_ERR_SHAPE;
+  const MxFwdLayout L = mx_fwd_layout(W->format, W->cols, M, r, sh);
+  if (workspace_bytes < L.act.end) return QLORA_ERR_WORKSPACE;
+  DeviceInfo d;
+  if ((st = device_info(&d)) != QLORA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (quantize_acts(W, X, M, ws, L.act, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
+  const uint16_t* sxa = nullptr;
+  if (r) {
+    RankDivide div;
+    if (W->format == QLORA_NVFP4) {
+      div.row = reinterpret_cast<const float*>(ws + L.act.global);
+      div.all = W->global_scale;
+    }
+    if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, div, d, cs)) != QLORA_OK) return st;
+    sxa = reinterpret_cast<const uint16_t*>(ws + L.xa.sxa);
+  }
+  return run_mx_gemm(W, M, ws, L.act, B, false, sxa, r, r ? sh.lora_steps : 0, Y, d, cs);
+}
+
+qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, const uint16_t* dY, int64_t M,
+                                 const uint16_t* A, const uint16_t* B, int32_t r, float s, const float* XA,
+                                 uint16_t* dX, float* dA, float* dB, void* workspace, size_t workspace_bytes,
+                                 qlora_stream_t stream) {
+  qlora_status st = check_mx(WT);
+  if (st != QLORA_OK) return st;
+  const int64_t rows = WT->cols, cols = WT->rows;          // the layer's W is [rows, cols]
+  LinearShape sh{};
+  if ((st = mx_layer_shape(rows, cols, M, r, &sh)) != QLORA_OK) return st;
+  if (r && WT->scale_per_row) return QLORA_ERR_UNSUPPORTED;
+  if (!dY || !workspace || (!r && !dX) || (r && (!X || !A || !B || !dA || !dB))) return QLORA_ERR_NULL;
+  if (!aligned16(dY) || !aligned16(workspace) || (dX && !aligned16(dX)) ||
+      (r && (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(dA) || !aligned16(dB) ||
+             (XA && !aligned16(XA)))))
+    return QLORA_ERR_ALIGN;
+  if (r && !std::isfinite(s)) return QLORA_ERR_SHAPE;
+  MxBwdLayout L = mx_bwd_layout(WT->format, rows, M, r, sh);
+  if (workspace_bytes < L.act.end) return QLORA_ERR_WORKSPACE;
+  DeviceInfo d;
+  if ((st = device_info(&d)) != QLORA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (dX && quantize_acts(WT, dY, M, ws, L.act, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
+  const uint16_t* sg = nullptr;
+  if (r) {
+    // G = dY B and X A^T as the backward over an NF4 weight has them
+    RankDivide div;
+    sg = reinterpret_cast<const uint16_t*>(ws + L.lora.sg);
+    if (dX && WT->format == QLORA_NVFP4) {
+      div.row = reinterpret_cast<const float*>(ws + L.act.global);
+      div.all = WT->global_scale;
+      div.out = reinterpret_cast<uint16_t*>(ws + L.sg_div);
+      sg = div.out;
+    }
+    if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L.lora, div, d, cs)) != QLORA_OK) return st;
+  }
+  if (dX && (st = run_mx_gemm(WT, M, ws, L.act, A, true, sg, r, r ? sh.lora_steps : 0, dX, d, cs)) != QLORA_OK) return st;
+  return r ? run_lora_grads(sh, X, dY, s, XA, dA, dB, ws, &L.lora, d, cs) : QLORA_OK;
 }
 
 }  // extern "C"

@@ -302,6 +302,47 @@ QLORA_EXPORT qlora_status qlora_mx_quantize(const uint16_t* W, int32_t transpose
 QLORA_EXPORT qlora_status qlora_mx_dequantize(const qlora_mx_tensor* W, uint16_t* W_out, qlora_stream_t stream);
 
 /*
+ * Work-buffer sizes of qlora_mx_linear_fwd / qlora_mx_linear_bwd for a layer
+ * W [rows, cols] of the given format, M token rows and LoRA rank r (0: no
+ * adapter).  As for qlora_linear_workspace_size, a work buffer needs no
+ * initialisation and two calls that may run at the same time must not share one.
+ */
+QLORA_EXPORT qlora_status qlora_mx_linear_workspace_size(int64_t rows, int64_t cols, int32_t format, int64_t M, int32_t r,
+                                            size_t* fwd_bytes, size_t* bwd_bytes);
+
+/*
+ * Forward of a linear layer over a frozen microscaled weight, both operands of
+ * the product 4 bits wide:
+ *   Y = deq(q(X)) deq(W)^T + s (X A^T) B^T
+ * q quantises every token in W's format (QLORA_NVFP4: with a global scale per
+ * token, so a token's result does not depend on the others).  W [rows, cols],
+ * X [M, cols] bf16, Y [M, rows] bf16; sums are fp32, Y is rounded once.
+ *   r = 0: no adapter; A, B and XA_out are ignored, any rows, cols, M >= 1.
+ *   r > 0: A [r, cols], B [rows, r] bf16 and XA_out [M, r] float (or NULL) with
+ *   the requirements of qlora_linear_fwd; the rank-r term is taken as
+ *   bf16(s X A^T) B^T.  Not with scale_per_row (QLORA_ERR_UNSUPPORTED).
+ * Bit-reproducible from run to run on the same device.
+ */
+QLORA_EXPORT qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, int64_t M, const uint16_t* A,
+                                 const uint16_t* B, int32_t r, float s, uint16_t* Y, float* XA_out, void* workspace,
+                                 size_t workspace_bytes, qlora_stream_t stream);
+
+/*
+ * Backward of the same layer.  WT is the transpose of the layer's weight,
+ * quantised along the weight's rows (qlora_mx_quantize with transpose = 1), so
+ * that this product too takes two 4-bit operands; q is passed straight through:
+ *   G  = dY B
+ *   dX = deq(q(dY)) deq(WT)^T + s G A     [M, cols] bf16 (skipped when dX is NULL)
+ *   dB = s dY^T (X A^T), dA = s G^T X     [rows, r], [r, cols] float, as qlora_linear_bwd
+ * WT [cols, rows], dY [M, rows].  r = 0: no adapter; X, A, B, XA, dA, dB are
+ * ignored and dX is required.  XA: X A^T of the forward, or NULL to recompute it.
+ */
+QLORA_EXPORT qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, const uint16_t* dY, int64_t M,
+                                 const uint16_t* A, const uint16_t* B, int32_t r, float s, const float* XA,
+                                 uint16_t* dX, float* dA, float* dB, void* workspace, size_t workspace_bytes,
+                                 qlora_stream_t stream);
+
+/*
  * Device error flag of the calling thread's current device: bit 0 is set when
  * a kernel's internal wait gave up after its time limit (a bug, reported
  * instead of hanging); bit 2 when a kernel's shared-memory window did not fit

@@ -142,3 +142,221 @@ def test_zero_sized_and_given_destinations(qb):
         qb.qlora_mx_quantize(w, out=qb.empty_mx(96, 40, w.device))
     back = torch.empty(40, 96, dtype=torch.bfloat16, device="cuda")
     assert qb.qlora_mx_dequantize(out, back) is back
+
+
+# ---------------------------------------------------------------- the linear layer
+def product_bound(y, x, w):
+    """What the product may be off by: Y is rounded to bf16 once (half a step,
+    2^-8 of the value); before that the tensor core adds 64 products at a time
+    to an fp32 sum, each addition off by at most 2^-22 of the magnitudes that
+    went in (a truncated 24-bit sum and its inner alignment)."""
+    return np.abs(y) * 2.0 ** -8 + (x.shape[1] / 64 + 2) * 2.0 ** -22 * (np.abs(x) @ np.abs(w).T) + 1e-37
+
+
+def check(got, want, bound, name):
+    got = f64(got)
+    assert got.shape == want.shape
+    over = np.abs(got - want) - bound
+    assert np.all(over <= 0), f"{name}: {np.sum(~(over <= 0))} of {over.size} off, worst {over.max():.3g} over the bound"
+
+
+def lora_terms(x, a, b, s):
+    """s (x a^T) b^T and what taking bf16(s x a^T) may put it off by, with the fp32 sum of x a^T."""
+    xa = s * (x @ a.T)
+    slack = np.abs(xa) * 2.0 ** -8 + abs(s) * (x.shape[1] / 16 + 2) * 2.0 ** -22 * (np.abs(x) @ np.abs(a).T)
+    return xa @ b.T, slack @ np.abs(b).T + (b.shape[1] / 16 + 2) * 2.0 ** -22 * (np.abs(xa) @ np.abs(b).T)
+
+
+LAYERS = [(1, 1, 1), (8, 64, 1), (128, 256, 1), (64, 64, 16), (300, 520, 17), (392, 640, 33), (256, 4096, 65),
+          (130, 130, 129), (2048, 8192, 3), (1001, 1999, 77), (512, 1024, 300), (136, 90, 257), (4096, 96, 5),
+          (129, 7000, 64)]
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("rows,cols,m", LAYERS)
+def test_linear_fwd(qb, rows, cols, m, fmt):
+    w, x = f64(normal((rows, cols), 0.02, 1)), normal((m, cols), 1.0, 2)
+    q = upload(qb, w, fmt)
+    Y, XA = qb.qlora_mx_linear_fwd(q, x.cuda())
+    assert XA is None
+    wv, xv = mx.round_trip(w, fmt), mx.round_trip(f64(x), fmt, True)
+    check(Y, xv @ wv.T, product_bound(xv @ wv.T, xv, wv), "Y")
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("rows,cols,m,r", [(8, 64, 1, 8), (256, 256, 16, 8), (392, 640, 33, 64), (1000, 4096, 129, 136),
+                                           (2048, 704, 300, 256)])
+def test_linear_fwd_with_an_adapter(qb, rows, cols, m, r, fmt):
+    w, x = f64(normal((rows, cols), 0.02, 1)), normal((m, cols), 1.0, 2)
+    a, b, s = normal((r, cols), 0.02, 3), normal((rows, r), 0.02, 4), 16.0 / r
+    q = upload(qb, w, fmt)
+    Y, XA = qb.qlora_mx_linear_fwd(q, x.cuda(), a.cuda(), b.cuda(), s)
+    wv, xv = mx.round_trip(w, fmt), mx.round_trip(f64(x), fmt, True)
+    term, slack = lora_terms(f64(x), f64(a), f64(b), s)
+    want = xv @ wv.T + term
+    check(Y, want, product_bound(want, xv, wv) + slack, "Y")
+    check(XA, f64(x) @ f64(a).T, (cols / 16 + 2) * 2.0 ** -22 * (np.abs(f64(x)) @ np.abs(f64(a)).T), "XA")
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("rows,cols,m", [(1, 1, 1), (1999, 1001, 77), (640, 392, 16), (4096, 256, 300)])
+def test_linear_bwd_without_an_adapter(qb, rows, cols, m, fmt):
+    w, dy = normal((rows, cols), 0.02, 1), normal((m, rows), 1e-3, 2)
+    qt = qb.qlora_mx_quantize(w.cuda(), fmt, transpose=True)
+    dX, dA, dB = qb.qlora_mx_linear_bwd(qt, dy.cuda())
+    assert dA is None and dB is None
+    wt, gv = mx.round_trip(f64(w).T, fmt), mx.round_trip(f64(dy), fmt, True)
+    check(dX, gv @ wt.T, product_bound(gv @ wt.T, gv, wt), "dX")
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("given_xa,need_dx", [(True, True), (False, True), (False, False)])
+@pytest.mark.parametrize("rows,cols,m,r", [(256, 320, 7, 8), (392, 640, 200, 64), (136, 1024, 129, 136)])
+def test_linear_bwd_with_an_adapter(qb, rows, cols, m, r, given_xa, need_dx, fmt):
+    w, dy, x = normal((rows, cols), 0.02, 1), normal((m, rows), 1e-3, 2), normal((m, cols), 1.0, 5)
+    a, b, s = normal((r, cols), 0.02, 3), normal((rows, r), 0.02, 4), 16.0 / r
+    qt = qb.qlora_mx_quantize(w.cuda(), fmt, transpose=True)
+    xa = (x.float() @ a.float().T).cuda() if given_xa else None
+    dX, dA, dB = qb.qlora_mx_linear_bwd(qt, dy.cuda(), x.cuda(), a.cuda(), b.cuda(), s, XA=xa, need_dx=need_dx)
+    X, dY, A, B = f64(x), f64(dy), f64(a), f64(b)
+    term, slack = lora_terms(dY, B.T, A.T, s)
+    if need_dx:
+        wt, gv = mx.round_trip(f64(w).T, fmt), mx.round_trip(dY, fmt, True)
+        want = gv @ wt.T + term
+        check(dX, want, product_bound(want, gv, wt) + slack, "dX")
+    else:
+        assert dX is None
+    # the rank-r operands of the gradients are taken as bf16 (2^-8 of each), the sums before and after in fp32
+    sums = (max(rows, cols, m) / 16 + 4) * 2.0 ** -22
+    G, XA = dY @ B, X @ A.T
+    g_off = np.abs(G) * 2.0 ** -8 + sums * (np.abs(dY) @ np.abs(B))
+    xa_off = np.abs(XA) * 2.0 ** -8 + sums * (np.abs(X) @ np.abs(A).T)
+    check(dA, s * G.T @ X, s * (g_off.T @ np.abs(X)) + sums * s * (np.abs(G).T @ np.abs(X)), "dA")
+    check(dB, s * dY.T @ XA, s * (np.abs(dY).T @ xa_off) + sums * s * (np.abs(dY).T @ np.abs(XA)), "dB")
+
+
+def test_gradient_against_differences(qb):
+    """<dX, v> against (f(x + h v) - f(x - h v)) / 2h of f(x) = <dy, Y(x)> with
+    x and x +- h v on the quantiser's grid, where q is the identity.  W too lies
+    on the grid in both directions (every block of rows and of columns holds a 6
+    and multiples of 1/2), and dy as well, so both sides are sums of products of
+    multiples of 1/2: exact but for one rounding of Y and dX to bf16 each."""
+    rows, cols, m = 64, 96, 32
+    rng = np.random.default_rng(0)
+    lv = np.array([-4.0, -3, -2, -1.5, -1, -0.5, 0, 0.5, 1, 1.5, 2, 3, 4])
+    w = rng.choice(lv, (rows, cols))
+    np.fill_diagonal(w[:, :64], 6.0)
+    w[0::32, :] = 6.0
+    w[:, 0::32] = 6.0
+    x = rng.choice([-2.0, -1, 0, 1, 2], (m, cols))
+    x[:, 0::32] = 6.0
+    v = rng.choice([-1.0, 0, 1], (m, cols))
+    v[:, 0::32] = 0.0
+    dy = rng.choice([-2.0, -1, 0, 1, 2, 4], (m, rows))
+    dy[:, 0::32] = 6.0
+    t = lambda z: torch.from_numpy(z).to(torch.bfloat16).cuda()  # noqa: E731
+    q, qt = qb.qlora_mx_quantize(t(w)), qb.qlora_mx_quantize(t(w), transpose=True)
+    assert np.array_equal(f64(qb.qlora_mx_dequantize(q)), w) and np.array_equal(f64(qb.qlora_mx_dequantize(qt)), w.T)
+    dX = f64(qb.qlora_mx_linear_bwd(qt, t(dy))[0])
+    up = f64(qb.qlora_mx_linear_fwd(q, t(x + v))[0])
+    down = f64(qb.qlora_mx_linear_fwd(q, t(x - v))[0])
+    left, right = (dX * v).sum(), (dy * (up - down)).sum() / 2
+    slack = 2.0 ** -8 * ((np.abs(dX) * np.abs(v)).sum() + (np.abs(dy) * (np.abs(up) + np.abs(down))).sum() / 2)
+    assert abs(left - right) <= slack
+    exact = ((dy @ w) * v).sum()
+    assert abs(left - exact) <= 2.0 ** -8 * (np.abs(dy @ w) * np.abs(v)).sum()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("m", [1, 40, 200])
+def test_linear_is_bit_reproducible_and_token_independent(qb, m, fmt):
+    """The same call twice gives the same bits, and a token's result does not
+    depend on which tokens share its tile."""
+    w, x = normal((520, 3000), 0.02, 1).cuda(), normal((m, 3000), 1.0, 2).cuda()
+    q = qb.qlora_mx_quantize(w, fmt)
+    first = qb.qlora_mx_linear_fwd(q, x)[0]
+    for _ in range(5):
+        assert torch.equal(qb.qlora_mx_linear_fwd(q, x)[0], first)
+    if m > 1:
+        other = x.clone()
+        other[1:] *= 100.0
+        assert torch.equal(qb.qlora_mx_linear_fwd(q, other)[0][0], first[0])
+
+
+def test_linear_nan_stays_in_its_row(qb):
+    w, x = normal((200, 512), 0.02, 1).cuda(), normal((20, 512), 1.0, 2).cuda()
+    for fmt in ("mxfp4", "nvfp4"):
+        q = qb.qlora_mx_quantize(w, fmt)
+        clean = qb.qlora_mx_linear_fwd(q, x)[0]
+        bad = x.clone()
+        bad[3, 100], bad[19, 0] = float("nan"), float("inf")
+        got = qb.qlora_mx_linear_fwd(q, bad)[0]
+        assert got[3].isnan().all() and got[19].isnan().all()
+        keep = [i for i in range(20) if i not in (3, 19)]
+        assert torch.equal(got[keep], clean[keep])
+
+
+def test_linear_refusals(qb):
+    q = qb.qlora_mx_quantize(normal((64, 128)).cuda(), "nvfp4")
+    x = normal((4, 128)).cuda()
+    a, b = normal((8, 128)).cuda(), normal((64, 8)).cuda()
+    for bad in (x.float(), x[:, :64], normal((128, 4)).cuda().t(), x.cpu()):
+        with pytest.raises(ValueError, match="X"):
+            qb.qlora_mx_linear_fwd(q, bad)
+    with pytest.raises(ValueError, match="together"):
+        qb.qlora_mx_linear_fwd(q, x, a)
+    with pytest.raises(ValueError, match="B"):
+        qb.qlora_mx_linear_fwd(q, x, a, b.t().contiguous())
+    with pytest.raises(qb.QloraError, match="work buffer"):
+        qb.qlora_mx_linear_fwd(q, x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(qb.QloraError, match="shape"):
+        qb.qlora_mx_linear_fwd(q, x[:0])
+    with pytest.raises(qb.QloraError, match="shape"):          # an adapter needs cols % 64 == 0
+        odd = qb.qlora_mx_quantize(normal((64, 72)).cuda())
+        qb.qlora_mx_linear_fwd(odd, normal((4, 72)).cuda(), normal((8, 72)).cuda(), b)
+    per_row = qb.qlora_mx_quantize(normal((64, 128)).cuda(), "nvfp4", per_row=True)
+    with pytest.raises(qb.QloraError, match="unsupported"):
+        qb.qlora_mx_linear_fwd(per_row, x, a, b)
+    with pytest.raises(ValueError, match="need X"):
+        qb.qlora_mx_linear_bwd(q, normal((4, 128)).cuda(), A=normal((8, 64)).cuda(), B=normal((128, 8)).cuda())
+
+
+def test_linear_with_a_scale_per_weight_row(qb):
+    w, x = f64(normal((200, 300), 0.02, 1)) * np.logspace(-3, 3, 200)[:, None], normal((5, 300), 1.0, 2)
+    w = f64(torch.from_numpy(w).to(torch.bfloat16))
+    q = upload(qb, w, "nvfp4", True)
+    wv, xv = mx.round_trip(w, "nvfp4", True), mx.round_trip(f64(x), "nvfp4", True)
+    check(qb.qlora_mx_linear_fwd(q, x.cuda())[0], xv @ wv.T, product_bound(xv @ wv.T, xv, wv), "Y")
+
+
+def test_rows_behind_the_last_token_are_left_as_they_were(qb):
+    w, x = normal((200, 320), 0.02, 1).cuda(), normal((77, 320), 1.0, 2).cuda()
+    q = qb.qlora_mx_quantize(w)
+    whole = torch.full((90, 200), 7.0, dtype=torch.bfloat16, device="cuda")
+    qb.qlora_mx_linear_fwd(q, x, Y=whole[:77])
+    assert (whole[77:] == 7).all() and torch.equal(whole[:77], qb.qlora_mx_linear_fwd(q, x)[0])
+
+
+@pytest.mark.parametrize("m", [3, 300])
+def test_linear_on_another_stream_and_in_a_graph(qb, m):
+    """A side stream while another call runs, and a captured call replayed on new inputs."""
+    w = normal((512, 2048), 0.02, 1).cuda()
+    q = qb.qlora_mx_quantize(w, "nvfp4")
+    xs = [normal((m, 2048), 1.0, i).cuda() for i in range(4)]
+    want = [qb.qlora_mx_linear_fwd(q, x)[0] for x in xs]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = [qb.qlora_mx_linear_fwd(q, x)[0] for x in xs]
+    again = [qb.qlora_mx_linear_fwd(q, x)[0] for x in xs]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and all(torch.equal(a, b) for a, b in zip(want, again))
+    static = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = qb.qlora_mx_linear_fwd(q, static)[0]
+    for x, y in zip(xs, want):
+        static.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, y)
