@@ -18,6 +18,7 @@ Microscaled 4-bit formats (MXFP4, NVFP4):
     qlora_mx_dequantize(q)                            -> bf16 [rows, cols]
     qlora_mx_linear_fwd(q, X, A, B, s)                -> (Y bf16, XA fp32 or None)
     qlora_mx_linear_bwd(qT, dY, X, A, B, s, XA)       -> (dX bf16 or None, dA fp32, dB fp32)
+    qlora_mx_moe_fwd(W13, W2, router, X, top_k)       -> (Y bf16, ids int32, probs fp32): experts for a few tokens
 """
 from __future__ import annotations
 
@@ -109,13 +110,18 @@ _lib.qlora_mx_linear_fwd.restype = ctypes.c_int
 _lib.qlora_mx_linear_bwd.argtypes = [_MX, _vp, _vp, _i64, _vp, _vp, _i32, ctypes.c_float, _vp, _vp, _vp, _vp, _vp,
                                      _sz, _vp]
 _lib.qlora_mx_linear_bwd.restype = ctypes.c_int
+_lib.qlora_mx_moe_workspace_size.argtypes = [_i32, _i64, _i64, _i64, _i32, _szp]
+_lib.qlora_mx_moe_workspace_size.restype = ctypes.c_int
+_lib.qlora_mx_moe_fwd.argtypes = [_MX, _MX, _vp, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.qlora_mx_moe_fwd.restype = ctypes.c_int
 
 EXPORTED = ["qlora_status_string", "qlora_get_codebook", "qlora_get_levels", "qlora_nf4_sizes", "qlora_quantize_nf4_dq",
             "qlora_dequantize", "qlora_linear_workspace_size", "qlora_linear_fwd", "qlora_linear_fwd_multi",
             "qlora_linear_bwd", "qlora_read_device_errors", "qlora_kernel_launches",
             "qlora_time_next_gemm", "qlora_quantize_nf4_dq_noalloc", "qlora_selftest_bounded_wait",
             "qlora_mx_sizes", "qlora_mx_quantize", "qlora_mx_dequantize",
-            "qlora_mx_linear_workspace_size", "qlora_mx_linear_fwd", "qlora_mx_linear_bwd"]
+            "qlora_mx_linear_workspace_size", "qlora_mx_linear_fwd", "qlora_mx_linear_bwd",
+            "qlora_mx_moe_workspace_size", "qlora_mx_moe_fwd"]
 
 # Largest weight the allocation-free quantize variant accepts.
 NOALLOC_MAX_ELEMENTS = 134217728
@@ -611,3 +617,43 @@ def qlora_mx_linear_bwd(qT: MXTensor, dY: torch.Tensor, X: torch.Tensor | None =
     _on(dev, "qlora_mx_linear_bwd", _lib.qlora_mx_linear_bwd, c, _addr(X), dY.data_ptr(), m, _addr(A), _addr(B), r,
         float(s), _addr(XA), _addr(dX), _addr(dA), _addr(dB), workspace.data_ptr(), _size(workspace))
     return dX, dA, dB
+
+
+def qlora_mx_moe_workspace_size(experts: int, hidden: int, inner: int, m: int, top_k: int) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.qlora_mx_moe_workspace_size(experts, hidden, inner, m, top_k, b), "qlora_mx_moe_workspace_size")
+    return b.value
+
+
+def qlora_mx_moe_fwd(W13: MXTensor, W2: MXTensor, router: torch.Tensor, X: torch.Tensor, top_k: int,
+                     Y: torch.Tensor | None = None, ids: torch.Tensor | None = None, probs: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None):
+    """A mixture-of-experts layer for at most 16 tokens: W13 stacks the experts'
+    gate and up rows [experts * 2 inner, hidden], W2 their down rows
+    [experts * hidden, inner], both MXFP4; router [experts, hidden] bf16.
+    Returns (Y bf16 [m, hidden], ids int32 [m, top_k], probs fp32 [m, top_k])."""
+    c13, c2, dev = W13.c_struct(), W2.c_struct(), W13.device
+    if W2.device != dev:
+        raise ValueError(f"W2 is on {W2.device}, W13 on {dev}")
+    m, experts, hidden = X.shape[0], router.shape[0], W13.cols
+    _need("X", X, torch.bfloat16, (m, hidden), dev)
+    _need("router", router, torch.bfloat16, (experts, hidden), dev)
+    if W13.rows != experts * 2 * W2.cols or W2.rows != experts * hidden:
+        raise ValueError(f"{experts} experts of hidden {hidden} and inner {W2.cols}: W13 must have {experts * 2 * W2.cols} rows "
+                         f"and W2 {experts * hidden}, not {W13.rows} and {W2.rows}")
+    if Y is None:
+        Y = torch.empty(m, hidden, dtype=torch.bfloat16, device=dev)
+    else:
+        _need("Y", Y, torch.bfloat16, (m, hidden), dev)
+    if ids is None:
+        ids = torch.empty(m, max(top_k, 0), dtype=torch.int32, device=dev)
+    else:
+        _need("ids", ids, torch.int32, (m, top_k), dev)
+    if probs is None:
+        probs = torch.empty(m, max(top_k, 0), dtype=torch.float32, device=dev)
+    else:
+        _need("probs", probs, torch.float32, (m, top_k), dev)
+    workspace = _mx_workspace(workspace, qlora_mx_moe_workspace_size(experts, hidden, W2.cols, m, top_k), dev)
+    _on(dev, "qlora_mx_moe_fwd", _lib.qlora_mx_moe_fwd, c13, c2, router.data_ptr(), experts, X.data_ptr(), m, top_k,
+        Y.data_ptr(), ids.data_ptr(), probs.data_ptr(), workspace.data_ptr(), _size(workspace))
+    return Y, ids, probs

@@ -164,6 +164,34 @@ qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const
   return counted(launch_mx_gemm(W->format, a, w, x, lw, lx, d.num_sms, cs)) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
+// ------------------------------------------------------------------ mixture of experts
+struct MoeLayout {
+  size_t x_codes, x_scales, h_codes, h_scales, part, list, n_used, counters, total;
+  int max_used;
+};
+qlora_status moe_layout(int32_t experts, int64_t hidden, int64_t inner, int64_t M, int32_t top_k, MoeLayout* l) {
+  if (M < 1 || M > kMoeMaxTokens || experts < 1 || experts > kMoeMaxExperts || top_k < 1 || top_k > kMoeMaxTopK ||
+      top_k > experts)
+    return QLORA_ERR_SHAPE;
+  if (hidden < 128 || inner < 128 || hidden % 128 || inner % 128 || hidden > (1 << 20) || inner > (1 << 20) ||
+      experts * 2 * inner > kMxMaxDim || experts * hidden > kMxMaxDim)
+    return QLORA_ERR_SHAPE;
+  const int64_t pairs = M * top_k;
+  l->max_used = static_cast<int>(pairs < experts ? pairs : experts);
+  size_t o = 0;
+  auto take = [&](size_t n) { const size_t at = o; o = round_up(o + n, 256); return at; };
+  l->x_codes = take(static_cast<size_t>(M) * hidden / 2);
+  l->x_scales = take(static_cast<size_t>(hidden) / 128 * 512);
+  l->h_codes = take(static_cast<size_t>(l->max_used) * 16 * inner / 2);
+  l->h_scales = take(static_cast<size_t>(l->max_used) * inner / 128 * 512);
+  l->part = take(static_cast<size_t>(pairs) * hidden * 4);
+  l->list = take(static_cast<size_t>(l->max_used) * sizeof(MoeExpert));
+  l->n_used = take(4);
+  l->counters = take(static_cast<size_t>(hidden) / 128 * 4);
+  l->total = o;
+  return QLORA_OK;
+}
+
 }  // namespace
 }  // namespace qlora
 
@@ -318,6 +346,69 @@ qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, c
   }
   if (dX && (st = run_mx_gemm(WT, M, ws, L.act, A, true, sg, r, r ? sh.lora_steps : 0, dX, d, cs)) != QLORA_OK) return st;
   return r ? run_lora_grads(sh, X, dY, s, XA, dA, dB, ws, &L.lora, d, cs) : QLORA_OK;
+}
+
+qlora_status qlora_mx_moe_workspace_size(int32_t experts, int64_t hidden, int64_t inner, int64_t M, int32_t top_k,
+                                         size_t* bytes) {
+  MoeLayout l{};
+  const qlora_status st = moe_layout(experts, hidden, inner, M, top_k, &l);
+  if (st == QLORA_OK && bytes) *bytes = l.total;
+  return st;
+}
+
+qlora_status qlora_mx_moe_fwd(const qlora_mx_tensor* W13, const qlora_mx_tensor* W2, const uint16_t* router,
+                              int32_t experts, const uint16_t* X, int64_t M, int32_t top_k, uint16_t* Y, int32_t* ids,
+                              float* probs, void* workspace, size_t workspace_bytes, qlora_stream_t stream) {
+  qlora_status st = check_mx(W13);
+  if (st == QLORA_OK) st = check_mx(W2);
+  if (st != QLORA_OK) return st;
+  if (W13->format != QLORA_MXFP4 || W2->format != QLORA_MXFP4) return QLORA_ERR_UNSUPPORTED;
+  const int64_t hidden = W13->cols, inner = W2->cols;
+  MoeLayout l{};
+  if ((st = moe_layout(experts, hidden, inner, M, top_k, &l)) != QLORA_OK) return st;
+  if (W13->rows != experts * 2 * inner || W2->rows != experts * hidden) return QLORA_ERR_SHAPE;
+  if (!router || !X || !Y || !ids || !probs || !workspace) return QLORA_ERR_NULL;
+  if (!aligned16(router) || !aligned16(X) || !aligned16(Y) || !aligned16(ids) || !aligned16(probs) ||
+      !aligned16(workspace))
+    return QLORA_ERR_ALIGN;
+  if (workspace_bytes < l.total) return QLORA_ERR_WORKSPACE;
+  DeviceInfo d;
+  if ((st = device_info(&d)) != QLORA_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  MxMoeArgs a{};
+  a.x = X;
+  a.router = router;
+  a.w13_scales = W13->scales;
+  a.w2_scales = W2->scales;
+  a.hidden = hidden;
+  a.inner = inner;
+  a.m = static_cast<int>(M);
+  a.experts = experts;
+  a.top_k = top_k;
+  a.splits = mx_moe_splits(static_cast<int64_t>(l.max_used) * (inner / 128), static_cast<int>((hidden + 255) / 256), d.num_sms);
+  a.y = Y;
+  a.ids = ids;
+  a.probs = probs;
+  a.x_codes = ws + l.x_codes;
+  a.x_scales = ws + l.x_scales;
+  a.h_codes = ws + l.h_codes;
+  a.h_scales = ws + l.h_scales;
+  a.part = reinterpret_cast<float*>(ws + l.part);
+  a.list = reinterpret_cast<MoeExpert*>(ws + l.list);
+  a.n_used = reinterpret_cast<int*>(ws + l.n_used);
+  a.counters = reinterpret_cast<uint32_t*>(ws + l.counters);
+  a.err = d.err;
+  const uint64_t hp = static_cast<uint64_t>(hidden) / 2, ip = static_cast<uint64_t>(inner) / 2;
+  CUtensorMap w13, w2, x, h;
+  if (!make_map_u8(&w13, W13->codes, hp, static_cast<uint64_t>(W13->rows), hp, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map_u8(&w2, W2->codes, ip, static_cast<uint64_t>(W2->rows), ip, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map_u8(&x, a.x_codes, hp, static_cast<uint64_t>(M), hp, 128, 16, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map_u8(&h, a.h_codes, ip, static_cast<uint64_t>(l.max_used) * 16, ip, 128, 16, CU_TENSOR_MAP_SWIZZLE_128B))
+    return QLORA_ERR_CUDA;
+  return counted(launch_mx_moe(a, w13, x, w2, h, l.max_used, d.num_sms, reinterpret_cast<cudaStream_t>(stream)), 3) ==
+                 cudaSuccess
+             ? QLORA_OK
+             : QLORA_ERR_CUDA;
 }
 
 }  // extern "C"

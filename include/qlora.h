@@ -343,6 +343,28 @@ QLORA_EXPORT qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const u
                                  qlora_stream_t stream);
 
 /*
+ * A whole mixture-of-experts feed-forward layer for a few tokens over frozen
+ * MXFP4 experts: routing, both products of every expert in use and their sum.
+ *   logits[t] = X[t] router^T (fp32); the top_k largest of a token are chosen,
+ *   the lowest index first among equal ones; p[t] = softmax of their logits;
+ *   [g; u] = deq(W13_e) deq(q(X[t])),  h = g / (1 + exp(-g)) * u,
+ *   Y[t] = sum_j p[t, j] deq(W2_e) deq(q(h)),  e = ids[t, j], in the order of j.
+ * W13 stacks the experts' [2 inner, hidden] (gate rows, then up rows), W2 their
+ * [hidden, inner]; router [experts, hidden] bf16, X, Y [M, hidden] bf16;
+ * ids [M, top_k] and probs [M, top_k] receive the routing.  q is the MXFP4
+ * quantiser.  The weights of an expert no token chose are not read.
+ * Requirements: 1 <= M <= 16, 1 <= top_k <= min(16, experts), experts <= 1024,
+ * hidden and inner multiples of 128 (at most 2^20), both weights QLORA_MXFP4.
+ * Bit-reproducible from run to run on the same device.  The work buffer is as
+ * for qlora_mx_linear_fwd.
+ */
+QLORA_EXPORT qlora_status qlora_mx_moe_workspace_size(int32_t experts, int64_t hidden, int64_t inner, int64_t M,
+                                         int32_t top_k, size_t* bytes);
+QLORA_EXPORT qlora_status qlora_mx_moe_fwd(const qlora_mx_tensor* W13, const qlora_mx_tensor* W2, const uint16_t* router,
+                              int32_t experts, const uint16_t* X, int64_t M, int32_t top_k, uint16_t* Y, int32_t* ids,
+                              float* probs, void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
+/*
  * Device error flag of the calling thread's current device: bit 0 is set when
  * a kernel's internal wait gave up after its time limit (a bug, reported
  * instead of hanging); bit 2 when a kernel's shared-memory window did not fit

@@ -360,3 +360,153 @@ def test_linear_on_another_stream_and_in_a_graph(qb, m):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, y)
+
+
+# ---------------------------------------------------------------- mixture of experts
+def moe_case(qb, experts, hidden, inner, m, seed=0, std=0.05):
+    w13, w2 = normal((experts * 2 * inner, hidden), std, seed), normal((experts * hidden, inner), std, seed + 1)
+    router, x = normal((experts, hidden), std, seed + 2), normal((m, hidden), 1.0, seed + 3)
+    q13, q2 = qb.qlora_mx_quantize(w13.cuda()), qb.qlora_mx_quantize(w2.cuda())
+    return q13, q2, router.cuda(), x.cuda()
+
+
+def moe_reference(qb, q13, q2, router, x, top_k):
+    """(ids, p, y, what y may be off by).  h reaches its quantiser off by the
+    product's own error; where that can move a code (or a block's scale) to its
+    neighbour, the difference of the two values counts."""
+    E, H, F = router.shape[0], q13.cols, q2.cols
+    w13 = f64(qb.qlora_mx_dequantize(q13)).reshape(E, 2, F, H)
+    w2 = f64(qb.qlora_mx_dequantize(q2)).reshape(E, H, F)
+    X = f64(x)
+    xv = mx.round_trip(X, "mxfp4")
+    logits = X @ f64(router).T
+    ids = np.argsort(-logits, axis=1, kind="stable")[:, :top_k]
+    top = np.take_along_axis(logits, ids, 1)
+    p = np.exp(top - top[:, :1])
+    p /= p.sum(1, keepdims=True)
+    y, off = np.zeros((len(X), H)), np.zeros((len(X), H))
+    with np.errstate(over="ignore"):
+        for t in range(len(X)):
+            for j, e in enumerate(ids[t]):
+                g, u = w13[e, 0] @ xv[t], w13[e, 1] @ xv[t]
+                dg, du = ((H / 64 + 2) * 2.0 ** -22 * (np.abs(w) @ np.abs(xv[t])) for w in w13[e])
+                silu = g / (1 + np.exp(-g))
+                h = silu * u
+                d = 1.1 * np.abs(u) * dg + np.abs(silu) * du + dg * du + 2.0 ** -20 * np.abs(h)     # |silu'| < 1.1
+                hv = mx.round_trip(h[None], "mxfp4")[0]
+                b, db = h.reshape(-1, 32), d.reshape(-1, 32)
+                slack = np.zeros_like(b)
+                for sign in (-1, 1):
+                    amax = np.maximum((np.abs(b) + sign * db).max(1), 0)
+                    exp = np.where(amax > 0, np.frexp(amax)[1] - 3, -127).clip(-127)
+                    step = 2.0 ** exp.astype(float)[:, None]
+                    for v in (b - db, b, b + db):
+                        val = mx.LEVELS[mx.nearest_code(np.abs(v) / step)] * np.sign(v) * step
+                        slack = np.maximum(slack, np.abs(val - hv.reshape(-1, 32)))
+                o = w2[e] @ hv
+                y[t] += p[t, j] * o
+                off[t] += p[t, j] * (np.abs(w2[e]) @ slack.ravel() + (F / 64 + 4) * 2.0 ** -22 * (np.abs(w2[e]) @ np.abs(hv))
+                                     + 2.0 ** -18 * np.abs(o))      # p: the logits' error, exp and a division
+    return ids, p, y, off + np.abs(y) * 2.0 ** -8 + 1e-37
+
+
+@pytest.mark.parametrize("experts,hidden,inner,m,top_k", [
+    (1, 128, 128, 1, 1), (4, 256, 128, 1, 2), (8, 384, 256, 16, 8), (16, 512, 384, 5, 3), (64, 1024, 128, 16, 6),
+    (33, 640, 128, 9, 16), (300, 256, 128, 16, 10), (5, 128, 1152, 3, 1), (2, 2048, 640, 16, 2)])
+def test_moe(qb, experts, hidden, inner, m, top_k):
+    q13, q2, router, x = moe_case(qb, experts, hidden, inner, m, experts + m)
+    ids, p, y, off = moe_reference(qb, q13, q2, router, x, top_k)
+    Y, got_ids, got_p = qb.qlora_mx_moe_fwd(q13, q2, router, x, top_k)
+    assert np.array_equal(got_ids.cpu().numpy(), ids)
+    assert np.all(np.abs(f64(got_p) - p) <= p * 2.0 ** -17)
+    check(Y, y, off, "Y")
+    for _ in range(3):
+        assert torch.equal(qb.qlora_mx_moe_fwd(q13, q2, router, x, top_k)[0], Y)
+
+
+def test_moe_ties_take_the_lowest_index(qb):
+    q13, q2, router, x = moe_case(qb, 40, 256, 128, 6)
+    router[:] = router[:1]
+    assert torch.equal(qb.qlora_mx_moe_fwd(q13, q2, router, x, 5)[1].cpu(), torch.arange(5, dtype=torch.int32).expand(6, 5))
+    router[20:] *= -1
+    router[0] = 0                                             # logit 0 between the two groups
+    ids = qb.qlora_mx_moe_fwd(q13, q2, router, x, 16)[1].cpu().numpy()
+    logits = f64(x) @ f64(router).T
+    assert np.array_equal(ids, np.argsort(-logits, axis=1, kind="stable")[:, :16])
+
+
+def test_moe_every_token_on_one_expert_and_far_apart_logits(qb):
+    q13, q2, router, x = moe_case(qb, 8, 256, 128, 16, 5)
+    x[:, 0] = 8.0
+    router[:, 0] = torch.arange(8, device="cuda").to(torch.bfloat16) * 40          # expert 7 always wins, by hundreds
+    ids, p, y, off = moe_reference(qb, q13, q2, router, x, 3)
+    Y, got_ids, got_p = qb.qlora_mx_moe_fwd(q13, q2, router, x, 3)
+    assert np.array_equal(got_ids.cpu().numpy(), ids) and (got_p[:, 0] == 1).all() and (got_p[:, 1:] == 0).all()
+    check(Y, y, off, "Y")
+
+
+def test_moe_nan_token_stays_alone(qb):
+    q13, q2, router, x = moe_case(qb, 8, 256, 128, 4, 7)
+    clean = qb.qlora_mx_moe_fwd(q13, q2, router, x, 2)[0]
+    bad = x.clone()
+    bad[2, 5] = float("nan")
+    Y, ids, _ = qb.qlora_mx_moe_fwd(q13, q2, router, bad, 2)
+    assert Y[2].isnan().all() and ((ids >= 0) & (ids < 8)).all()
+    assert torch.equal(Y[[0, 1, 3]], clean[[0, 1, 3]])
+
+
+def test_moe_in_a_graph_with_a_workspace_of_its_own(qb):
+    q13, q2, router, x = moe_case(qb, 16, 512, 256, 4, 9)
+    xs = [normal((4, 512), 1.0, 50 + i).cuda() for i in range(3)]
+    want = [qb.qlora_mx_moe_fwd(q13, q2, router, v, 4) for v in xs]
+    ws = torch.full((qb.qlora_mx_moe_workspace_size(16, 512, 256, 4, 4),), 0xFF, dtype=torch.uint8, device="cuda")
+    static = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = qb.qlora_mx_moe_fwd(q13, q2, router, static, 4, workspace=ws)
+    for v, w in zip(xs, want):
+        static.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, w))
+
+
+def test_moe_refusals(qb):
+    q13, q2, router, x = moe_case(qb, 4, 256, 128, 3)
+    with pytest.raises(ValueError, match="rows"):
+        qb.qlora_mx_moe_fwd(q13, q2, router[:3], x, 2)
+    with pytest.raises(ValueError, match="X"):
+        qb.qlora_mx_moe_fwd(q13, q2, router, x.float(), 2)
+    with pytest.raises(qb.QloraError, match="shape"):
+        qb.qlora_mx_moe_fwd(q13, q2, router, x, 5)
+    with pytest.raises(qb.QloraError, match="shape"):
+        qb.qlora_mx_moe_fwd(q13, q2, router, normal((17, 256)).cuda(), 2)
+    nv = qb.qlora_mx_quantize(normal((4 * 256, 256)).cuda(), "nvfp4")
+    with pytest.raises(qb.QloraError, match="unsupported"):
+        qb.qlora_mx_moe_fwd(nv, q2, router, x, 2)
+
+
+def test_layers_in_a_row(qb):
+    """A block as it would be used: a projection with its adapter, the routed
+    layer, a projection back; each step is checked in its own test, here the
+    chain must equal the same chain on dequantised inputs of each step."""
+    m, H, F, E = 8, 512, 256, 8
+    q13, q2, router, x = moe_case(qb, E, H, F, m, 21)
+    w1, w2 = normal((H, H), 0.05, 1).cuda(), normal((H, H), 0.05, 2).cuda()
+    a, b = normal((16, H), 0.05, 3).cuda(), normal((H, 16), 0.05, 4).cuda()
+    qa, qc = qb.qlora_mx_quantize(w1, "nvfp4"), qb.qlora_mx_quantize(w2, "mxfp4")
+    y1, _ = qb.qlora_mx_linear_fwd(qa, x, a, b, 0.5)
+    y2, _, _ = qb.qlora_mx_moe_fwd(q13, q2, router, y1, 2)
+    y3, _ = qb.qlora_mx_linear_fwd(qc, y2)
+    xv, wv = mx.round_trip(f64(x), "nvfp4", True), f64(qb.qlora_mx_dequantize(qa))
+    term, slack = lora_terms(f64(x), f64(a), f64(b), 0.5)
+    check(y1, xv @ wv.T + term, product_bound(xv @ wv.T + term, xv, wv) + slack, "first")
+    _, _, want, off = moe_reference(qb, q13, q2, router, y1, 2)
+    check(y2, want, off, "experts")
+    xv, wv = mx.round_trip(f64(y2), "mxfp4"), f64(qb.qlora_mx_dequantize(qc))
+    check(y3, xv @ wv.T, product_bound(xv @ wv.T, xv, wv), "last")
+    dy = normal((m, H), 1e-3, 9).cuda()
+    qct = qb.qlora_mx_quantize(w2, "mxfp4", transpose=True)
+    d2 = qb.qlora_mx_linear_bwd(qct, dy)[0]
+    gv, wt = mx.round_trip(f64(dy), "mxfp4"), f64(qb.qlora_mx_dequantize(qct))
+    check(d2, gv @ wt.T, product_bound(gv @ wt.T, gv, wt), "back")

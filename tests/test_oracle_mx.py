@@ -105,3 +105,43 @@ def test_binding_refuses_buffers_that_do_not_hold_the_matrix():
         qb.empty_mx(4, 4, "cpu", "mxfp4", per_row=True)
     with pytest.raises(ValueError, match="bf16"):
         qb.qlora_mx_quantize(torch.zeros(4, 32))
+
+
+def test_linear_refusals():
+    p, s = 0x100000, ctypes.c_float(0.5)
+    f, b, size = lib.qlora_mx_linear_fwd, lib.qlora_mx_linear_bwd, lib.qlora_mx_linear_workspace_size
+    W = _t(64, 128)
+    args = lambda w=W, x=p, m=4, a=p, bb=p, r=8, y=p, xa=None, ws=p, n=1 << 40: (w, x, m, a, bb, r, s, y, xa, ws, n, None)  # noqa: E731
+    assert f(*args(w=None)) == ERR_NULL and f(*args(x=None)) == ERR_NULL and f(*args(a=None)) == ERR_NULL
+    assert f(*args(x=p + 2)) == ERR_ALIGN and f(*args(xa=p + 4)) == ERR_ALIGN and f(*args(y=p + 8)) == ERR_ALIGN
+    assert f(*args(m=0)) == ERR_SHAPE and f(*args(r=12)) == ERR_SHAPE and f(*args(r=264)) == ERR_SHAPE
+    assert f(*args(r=-8)) == ERR_SHAPE
+    assert f(*args(w=_t(64, 72))) == ERR_SHAPE and f(*args(w=_t(60, 128))) == ERR_SHAPE
+    assert f(*args(w=_t(0, 128))) == ERR_SHAPE and f(*args(w=_t(64, 128, 7))) == ERR_UNSUP
+    assert f(*args(w=_t(64, 128, 1, 1))) == ERR_UNSUP                     # a scale per weight row with an adapter
+    assert f(*args(n=64)) == ERR_WS and f(W, p, 4, None, None, 0, s, p, None, p, 64, None) == ERR_WS
+    assert f(W, p, 4, p, p, 8, ctypes.c_float(float("inf")), p, None, p, 1 << 40, None) == ERR_SHAPE
+    bargs = lambda dx=p, da=p, x=p, r=8, xa=None, n=1 << 40: (W, x, p, 4, p, p, r, s, xa, dx, da, p, p, n, None)  # noqa: E731
+    assert b(*bargs(dx=None, r=0)) == ERR_NULL and b(*bargs(da=None)) == ERR_NULL and b(*bargs(x=None)) == ERR_NULL
+    assert b(*bargs(xa=p + 2)) == ERR_ALIGN and b(*bargs(n=64)) == ERR_WS
+    assert size(64, 128, 3, 4, 8, None, None) == ERR_UNSUP and size(64, 100, 0, 4, 8, None, None) == ERR_SHAPE
+    assert size(64, 100, 0, 4, 0, None, None) == OK and size(0, 100, 0, 4, 0, None, None) == ERR_SHAPE
+
+
+def test_moe_refusals():
+    p = 0x100000
+    f, size = lib.qlora_mx_moe_fwd, lib.qlora_mx_moe_workspace_size
+    W13, W2 = _t(4 * 2 * 128, 256), _t(4 * 256, 128)
+    args = lambda a=W13, b=W2, r=p, e=4, x=p, m=3, k=2, y=p, ids=p, pr=p, ws=p, n=1 << 40: \
+        (a, b, r, e, x, m, k, y, ids, pr, ws, n, None)  # noqa: E731
+    for key in ("a", "b", "r", "x", "y", "ids", "pr", "ws"):
+        assert f(*args(**{key: None})) == ERR_NULL
+    for key in ("r", "x", "y", "ids", "pr", "ws"):
+        assert f(*args(**{key: p + 4})) == ERR_ALIGN
+    for kw in (dict(m=0), dict(m=17), dict(k=0), dict(k=5), dict(e=0), dict(e=5), dict(a=_t(1024, 200)), dict(b=_t(1024, 120)),
+               dict(b=_t(1000, 128))):
+        assert f(*args(**kw)) == ERR_SHAPE, kw
+    assert f(*args(a=_t(1024, 256, 1))) == ERR_UNSUP
+    assert f(*args(n=64)) == ERR_WS
+    assert size(1025, 256, 128, 1, 1, None) == ERR_SHAPE and size(32, 256, 128, 1, 17, None) == ERR_SHAPE
+    assert size(4, 256, 128, 16, 4, None) == OK
