@@ -116,6 +116,17 @@ bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t oute
   return r == CUDA_SUCCESS;
 }
 
+bool make_map_scales(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_outer) {
+  const cuuint64_t dims[2] = {128, tiles};
+  const cuuint64_t strides[1] = {512};
+  const cuuint32_t box[2] = {128, box_outer};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box,
+                                    estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 namespace {
 
 // m-tiles per rasterization group of the fused kernel: the packed codes of one

@@ -36,6 +36,8 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, 
               uint32_t box_outer);
 bool make_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch_bytes,
                  uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
+// Scale tiles (512 bytes each, `tiles` of them) as 32-bit words, box {128, box_outer}, no swizzle.
+bool make_map_scales(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_outer);
 
 // Returns e; when it is cudaSuccess, adds n to the process-wide count of
 // kernels the library has launched (qlora_kernel_launches).

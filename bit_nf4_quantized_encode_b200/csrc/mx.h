@@ -76,6 +76,17 @@ int mx_token_tile(int64_t m);
 cudaError_t launch_mx_gemm(int fmt, const MxGemmArgs& a, const CUtensorMap& w, const CUtensorMap& x,
                            const CUtensorMap& lora_w, const CUtensorMap& lora_x, int num_sms, cudaStream_t stream);
 
+// The same product for many tokens (mx_pair.cu): pairs of CTAs on tiles of 256
+// rows x token_tile (256 or 128) tokens; m_tiles counts 256 rows, splits is 1.
+// Maps: w / x as above with boxes {128, 128} / {128, token_tile / 2}; the scale
+// tiles as 32-bit words [row tiles * kt][128], box {128, 2 (MXFP4) or 4};
+// lora_x with box {64, token_tile / 2}.
+struct MxPairMaps {
+  CUtensorMap w, x, w_scales, x_scales, lora_w, lora_x;
+};
+cudaError_t launch_mx_pair(int fmt, int token_tile, const MxGemmArgs& a, const MxPairMaps& m, int num_sms,
+                           cudaStream_t stream);
+
 // Mixture-of-experts layer for at most 16 tokens (mx_moe.cu).
 constexpr int kMoeMaxExperts = 1024, kMoeMaxTopK = 16, kMoeMaxTokens = 16;
 

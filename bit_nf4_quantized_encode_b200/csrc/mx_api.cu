@@ -117,11 +117,22 @@ cudaError_t quantize_acts(const qlora_mx_tensor* W, const uint16_t* X, int64_t M
   return counted(launch_mx_quant(W->format, false, a, d.num_sms, cs));
 }
 
+// Token tile of the pair kernel: the one whose waves of tiles over the pairs of
+// SMs take less time.
+int pair_token_tile(int64_t rows, int64_t m, int num_sms) {
+  const int64_t pairs = num_sms / 2, mt = (rows + 255) / 256;
+  const int64_t wide = (mt * ((m + 255) / 256) + pairs - 1) / pairs * 2;
+  const int64_t narrow = (mt * ((m + 127) / 128) + pairs - 1) / pairs;
+  return narrow < wide ? 128 : 256;
+}
+
 // out [M, W->rows] = q(X) deq(W)^T + lora_x lora_w (see mx_gemm.cu).
 qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const ActLayout& L, const uint16_t* lora_w,
                          bool lora_mn, const uint16_t* lora_x, int r, int lora_steps, uint16_t* out,
                          const DeviceInfo& d, cudaStream_t cs) {
-  const int bn = mx_token_tile(M);
+  const bool pair = M > 128;
+  const int bn = pair ? pair_token_tile(W->rows, M, d.num_sms) : mx_token_tile(M);
+  const int box_x = pair ? bn / 2 : bn;
   const int64_t pitch = mx_pitch(W->cols);
   MxGemmArgs a{};
   a.w_scales = W->scales;
@@ -139,29 +150,41 @@ qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const
   a.lora_steps = lora_steps;
   a.lora_mn = lora_mn ? 1 : 0;
   a.out = out;
-  const int64_t m_tiles = (W->rows + 127) / 128, t_tiles = (M + bn - 1) / bn;
-  if (m_tiles * t_tiles > (int64_t{1} << 28)) return QLORA_ERR_SHAPE;
+  const int64_t m_tiles = pair ? (W->rows + 255) / 256 : (W->rows + 127) / 128, t_tiles = (M + bn - 1) / bn;
+  const int64_t w_tiles = (W->rows + 127) / 128 * a.kt, x_tiles = (M + 127) / 128 * a.kt;
+  if (m_tiles * t_tiles > (int64_t{1} << 28) || w_tiles > kMxMaxDim || x_tiles > kMxMaxDim) return QLORA_ERR_SHAPE;
   a.m_tiles = static_cast<int>(m_tiles);
   a.t_tiles = static_cast<int>(t_tiles);
-  a.m_group = mx_group(a.m_tiles, pitch);
-  a.splits = mx_splits(m_tiles * t_tiles, a.ksteps, d.num_sms);
+  a.m_group = mx_group(a.m_tiles, pair ? 2 * pitch : pitch);
+  a.splits = pair ? 1 : mx_splits(m_tiles * t_tiles, a.ksteps, d.num_sms);
   a.err = d.err;
-  CUtensorMap w, x, lw, lx;
+  MxPairMaps m;
   const uint64_t up = static_cast<uint64_t>(pitch);
-  if (!make_map_u8(&w, W->codes, up, static_cast<uint64_t>(W->rows), up, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !make_map_u8(&x, ws + L.codes, up, static_cast<uint64_t>(M), up, 128, static_cast<uint32_t>(bn),
+  if (!make_map_u8(&m.w, W->codes, up, static_cast<uint64_t>(W->rows), up, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map_u8(&m.x, ws + L.codes, up, static_cast<uint64_t>(M), up, 128, static_cast<uint32_t>(box_x),
                    CU_TENSOR_MAP_SWIZZLE_128B))
     return QLORA_ERR_CUDA;
   if (lora_steps) {
     const uint64_t rpad = static_cast<uint64_t>(lora_steps) * 64, n = static_cast<uint64_t>(W->rows);
-    if (!(lora_mn ? make_map(&lw, lora_w, n, r, n * 2, 64) : make_map(&lw, lora_w, r, n, static_cast<uint64_t>(r) * 2, 128)) ||
-        !make_map(&lx, lora_x, rpad, static_cast<uint64_t>(M), rpad * 2, static_cast<uint32_t>(bn)))
+    if (!(lora_mn ? make_map(&m.lora_w, lora_w, n, r, n * 2, 64)
+                  : make_map(&m.lora_w, lora_w, r, n, static_cast<uint64_t>(r) * 2, 128)) ||
+        !make_map(&m.lora_x, lora_x, rpad, static_cast<uint64_t>(M), rpad * 2, static_cast<uint32_t>(box_x)))
       return QLORA_ERR_CUDA;
   } else {
-    lw = w;
-    lx = x;
+    m.lora_w = m.w;
+    m.lora_x = m.x;
   }
-  return counted(launch_mx_gemm(W->format, a, w, x, lw, lx, d.num_sms, cs)) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+  cudaError_t e;
+  if (pair) {
+    const uint32_t atoms = W->format == QLORA_MXFP4 ? 2 : 4;
+    if (!make_map_scales(&m.w_scales, W->scales, static_cast<uint64_t>(w_tiles), atoms) ||
+        !make_map_scales(&m.x_scales, a.x_scales, static_cast<uint64_t>(x_tiles), atoms))
+      return QLORA_ERR_CUDA;
+    e = launch_mx_pair(W->format, bn, a, m, d.num_sms, cs);
+  } else {
+    e = launch_mx_gemm(W->format, a, m.w, m.x, m.lora_w, m.lora_x, d.num_sms, cs);
+  }
+  return counted(e) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ mixture of experts

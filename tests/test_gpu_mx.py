@@ -169,7 +169,7 @@ def lora_terms(x, a, b, s):
 
 LAYERS = [(1, 1, 1), (8, 64, 1), (128, 256, 1), (64, 64, 16), (300, 520, 17), (392, 640, 33), (256, 4096, 65),
           (130, 130, 129), (2048, 8192, 3), (1001, 1999, 77), (512, 1024, 300), (136, 90, 257), (4096, 96, 5),
-          (129, 7000, 64)]
+          (129, 7000, 64), (300, 72, 129), (1030, 2100, 520), (520, 4096, 1030)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
