@@ -105,20 +105,21 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer, one per CTA
-    if (lane == 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      uint32_t it = 0;
-      bool alive = true;
-      for (int u = first; u < ntiles && alive; u += stride) {
-        const Tile w = tile_of(u, a);
-        const int row0 = w.mt * 256 + static_cast<int>(rank) * 128;
-        const int tok0 = w.tt * kBN + static_cast<int>(rank) * (kBN / 2);
-        for (int j = 0; j < nk; ++j, ++it) {
-          const uint32_t stage = it % kStages, phase = (it / kStages) & 1u;
-          if (!mbar_wait(&empty[stage], phase ^ 1u, a.err)) { alive = false; break; }
-          const uint32_t bar = cluster_map(smem_u32(&full[stage]), 0);
-          uint8_t* sA = smem_gen + stage * kStageBytes;
-          uint8_t* sB = sA + kABytes;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t full0 = cluster_map(smem_u32(full), 0);
+    uint32_t stage = 0, phase = 0;
+    bool alive = true;
+    for (int u = first; u < ntiles && alive; u += stride) {
+      const Tile w = tile_of(u, a);
+      const int row0 = w.mt * 256 + static_cast<int>(rank) * 128;
+      const int tok0 = w.tt * kBN + static_cast<int>(rank) * (kBN / 2);
+      const int ws0 = static_cast<int>(row0 / 128 * a.kt), xs0 = static_cast<int>(w.tt * kRB * a.kt);
+      for (int j = 0; j < nk; ++j) {
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1u, a.err)) { alive = false; break; }
+        const uint32_t bar = full0 + stage * 8u;
+        uint8_t* sA = smem_gen + stage * kStageBytes;
+        uint8_t* sB = sA + kABytes;
+        if (elect_one()) {
           if (j < a.ksteps) {
             uint8_t* sSa = sB + kBBytes;
             uint8_t* sSb = sSa + kAtoms * 512;
@@ -126,11 +127,10 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
             tma_load_2d_pair(sA, &wmap, j * 128, row0, bar);
             tma_load_2d_pair(sB, &xmap, j * 128, tok0, bar);
             // a row tile's scales past its last one are the next row tile's: loaded, not used
-            tma_load_2d_pair(sSa, &wsmap, 0, static_cast<int32_t>(row0 / 128 * a.kt) + j * kAtoms, bar);
+            tma_load_2d_pair(sSa, &wsmap, 0, ws0 + j * kAtoms, bar);
 #pragma unroll
             for (int b = 0; b < kRB; ++b)
-              tma_load_2d_pair(sSb + b * (kAtoms * 512), &xsmap, 0,
-                               static_cast<int32_t>((w.tt * kRB + b) * a.kt) + j * kAtoms, bar);
+              tma_load_2d_pair(sSb + b * (kAtoms * 512), &xsmap, 0, xs0 + b * static_cast<int>(a.kt) + j * kAtoms, bar);
           } else {
             const int r0 = (j - a.ksteps) * 64;
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (kABytes + kBBytes));
@@ -143,58 +143,63 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
             tma_load_2d_pair(sB, &lxmap, r0, tok0, bar);
           }
         }
+        __syncwarp();
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer, the leader's
-    if (rank == 0 && lane == 0) {
-      uint32_t it = 0, n = 0;
+    if (rank == 0) {
+      uint32_t stage = 0, phase = 0, n = 0;
       bool alive = true;
       const uint32_t lora_idesc = idesc_bf16(256, kBN, a.lora_mn != 0, false);
+      const uint64_t desc0 = smem_desc_sw128(smem0, 16, 1024);       // + (byte offset >> 4)
+      const uint64_t sdesc0 = smem_desc_scales(smem0);
       for (int u = first; u < ntiles && alive; u += stride, ++n) {
-        if (n > 0 && !mbar_wait(acc_free, (n - 1) & 1u, a.err)) break;
+        if (n > 0 && !mbar_wait_warp(acc_free, (n - 1) & 1u, a.err)) break;
         tc_fence_after();
         const uint32_t d = tmem + (n & 1u) * kAcc1;
-        for (int j = 0; j < nk; ++j, ++it) {
-          const uint32_t stage = it % kStages, phase = (it / kStages) & 1u;
-          if (!mbar_wait(&full[stage], phase, a.err)) { alive = false; break; }
+        for (int j = 0; j < nk; ++j) {
+          if (!mbar_wait_warp(&full[stage], phase, a.err)) { alive = false; break; }
           tc_fence_after();
-          const uint32_t sA = smem0 + stage * kStageBytes;
-          const uint32_t sB = sA + kABytes;
-          if (j < a.ksteps) {
-            const uint32_t sSa = sB + kBBytes, sSb = sSa + kAtoms * 512;
+          const uint32_t off = stage * (kStageBytes >> 4);
+          const uint64_t ad = desc0 + off, bd = ad + (kABytes >> 4);
+          if (elect_one()) {
+            if (j < a.ksteps) {
+              const uint64_t sa = sdesc0 + off + ((kABytes + kBBytes) >> 4), sb = sa + (kAtoms * 512 >> 4);
 #pragma unroll
-            for (int t = 0; t < kAtoms; ++t) {
-              tmem_cp_scales_pair(tmem + kSfa + 4 * t, smem_desc_scales(sSa + t * 512));
+              for (int t = 0; t < kAtoms; ++t) {
+                tmem_cp_scales_pair(tmem + kSfa + 4 * t, sa + t * 32);
 #pragma unroll
-              for (int b = 0; b < kRB; ++b)
-                tmem_cp_scales_pair(tmem + kSfb + 4 * (t * kRB + b), smem_desc_scales(sSb + (b * kAtoms + t) * 512));
+                for (int b = 0; b < kRB; ++b)
+                  tmem_cp_scales_pair(tmem + kSfb + 4 * (t * kRB + b), sb + (b * kAtoms + t) * 32);
+              }
+              const int slices = static_cast<int>(min(static_cast<int64_t>(4), (a.k - static_cast<int64_t>(j) * 256 + 63) / 64));
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                if (q < slices) {
+                  const uint32_t acc = (j | q) != 0 ? 1u : 0u;
+                  if (kFmt == kMxFp4)
+                    mma_fp4_pair<true>(d, ad + q * 2, bd + q * 2, idesc_mxf4(256, kBN, true, 2u * (q & 1)),
+                                       tmem + kSfa + 4 * (q >> 1), tmem + kSfb + 4 * kRB * (q >> 1), acc);
+                  else
+                    mma_fp4_pair<false>(d, ad + q * 2, bd + q * 2, idesc_mxf4(256, kBN, false, 0), tmem + kSfa + 4 * q,
+                                        tmem + kSfb + 4 * kRB * q, acc);
+                }
+              }
+            } else {
+              // A K = 16 slice: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
+              const uint64_t la = a.lora_mn ? smem_desc_sw128(smem0, 8192, 1024) + off : ad;
+              const uint32_t step = a.lora_mn ? 2048 >> 4 : 32 >> 4;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) mma_bf16_pair(d, la + q * step, bd + q * 2, lora_idesc, 1u);
             }
-            const int slices = static_cast<int>(min(static_cast<int64_t>(4), (a.k - static_cast<int64_t>(j) * 256 + 63) / 64));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (q >= slices) break;
-              const uint64_t ad = smem_desc_sw128(sA + q * 32, 16, 1024);
-              const uint64_t bd = smem_desc_sw128(sB + q * 32, 16, 1024);
-              const uint32_t acc = (j | q) != 0 ? 1u : 0u;
-              if (kFmt == kMxFp4)
-                mma_fp4_pair<true>(d, ad, bd, idesc_mxf4(256, kBN, true, 2u * (q & 1)), tmem + kSfa + 4 * (q >> 1),
-                                   tmem + kSfb + 4 * kRB * (q >> 1), acc);
-              else
-                mma_fp4_pair<false>(d, ad, bd, idesc_mxf4(256, kBN, false, 0), tmem + kSfa + 4 * q,
-                                    tmem + kSfb + 4 * kRB * q, acc);
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint64_t ad = a.lora_mn ? smem_desc_sw128(sA + q * 2048, 8192, 1024)
-                                            : smem_desc_sw128(sA + q * 32, 16, 1024);
-              mma_bf16_pair(d, ad, smem_desc_sw128(sB + q * 32, 16, 1024), lora_idesc, 1u);
-            }
+            mma_commit_pair(&empty[stage]);
+            if (j == nk - 1) mma_commit_pair(acc_full);
           }
-          mma_commit_pair(&empty[stage]);
+          __syncwarp();
+          if (++stage == kStages) { stage = 0; phase ^= 1u; }
         }
-        if (alive) mma_commit_pair(acc_full);
       }
     }
   } else {

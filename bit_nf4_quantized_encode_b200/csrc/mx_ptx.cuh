@@ -6,6 +6,22 @@
 
 namespace qlora {
 
+// ---------------------------------------------------------------- warp-uniform issue
+// The warps that issue TMA and MMA run their loops with all lanes and let one
+// elected lane issue: operands that are the same in all lanes by construction
+// go to the instructions straight from uniform registers.  With a loop of one
+// lane each operand is moved there first, 45-50 cycles per tcgen05.cp and over
+// 200 per tcgen05.mma, more than a 4-bit MMA takes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// mbar_wait by all lanes of a warp, with one answer.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, err)) != 0;
+}
+
 // ---------------------------------------------------------------- block-scaled MMA
 // D[tmem] (+)= A * B^T of 4-bit operands (64 along the contraction), each
 // element times its block's scale: kind::mxf4 (blocks of 32, E8M0) and
