@@ -16,6 +16,7 @@
 //
 // Every pass is bound by memory: 2 bytes in, 0.5 + 1/32 (1/16) out per element.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -41,28 +42,94 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t c
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Largest finite magnitude of eight bf16 values (bits), and whether any is not finite.
-__device__ __forceinline__ uint32_t mag8(const uint4& q, bool& bad) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  uint32_t m = 0;
+// Thirty-two consecutive elements: what one thread encodes, one MXFP4 block or
+// two NVFP4 blocks, so that no block is shared between threads.
+struct Elems32 {
+  uint4 q[4];
+};
+template <bool kVec>
+__device__ __forceinline__ Elems32 load32(const uint16_t* row, int64_t c, int64_t cols) {
+  Elems32 e;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m = max(m, w[i] & 0x7FFFu);
-    m = max(m, (w[i] >> 16) & 0x7FFFu);
-  }
-  if (m >= 0x7F80u) {                      // rare: look again, without the values that are not finite
-    bad = true;
-    m = 0;
-    bool b = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m = max(m, mx_finite_mag(w[i], b));
-      m = max(m, mx_finite_mag(w[i] >> 16, b));
-    }
-  }
-  return m;
+  for (int i = 0; i < 4; ++i) e.q[i] = load8<kVec>(row, c + 8 * i, cols);
+  return e;
 }
 
+// Per 16-bit half: the larger magnitude.
+__device__ __forceinline__ uint32_t mag_max2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
+__device__ __forceinline__ uint32_t mag16(const uint4& a, const uint4& b) {
+  uint32_t m = a.x & 0x7FFF7FFFu;
+  m = mag_max2(m, a.y); m = mag_max2(m, a.z); m = mag_max2(m, a.w);
+  m = mag_max2(m, b.x); m = mag_max2(m, b.y); m = mag_max2(m, b.z); m = mag_max2(m, b.w);
+  return m;
+}
+__device__ __forceinline__ uint32_t wider_half(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
+
+// Largest finite magnitude (bf16 bits) of what mag16 saw or, where that holds
+// values that are not finite, of the elements again without them.
+__device__ __forceinline__ uint32_t finite_mag(uint32_t m, const uint4& q) {
+  uint32_t top = wider_half(m);
+  if (top >= 0x7F80u) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    bool bad = false;
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max(mx_finite_mag(w[i], bad), mx_finite_mag(w[i] >> 16, bad)));
+  }
+  return top;
+}
+__device__ __forceinline__ uint32_t finite_mag8(const uint4& q) {
+  uint32_t m = q.x & 0x7FFF7FFFu;
+  m = mag_max2(m, q.y); m = mag_max2(m, q.z); m = mag_max2(m, q.w);
+  return finite_mag(m, q);
+}
+
+// Scale byte of a block with the largest magnitude `mag` (bf16 bits).
+template <int kFmt>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t mag, float inv_g) {
+  if (kFmt == kMxFp4) return mag >= 0x7F80u ? 255u : mx_e8m0(mag << 16);
+  return mag >= 0x7F80u ? 0x7Fu : mx_e4m3(__fdiv_rn(__fmul_rn(__uint_as_float(mag << 16), inv_g), 6.0f));
+}
+
+// Multiplier (MXFP4), or scale and its reciprocal (NVFP4), of a block's elements.
+struct BlockScale {
+  float s, r;
+  bool zero;                 // every code is 0: NaN scale or (NVFP4) scale 0
+};
+template <int kFmt>
+__device__ __forceinline__ BlockScale block_scale(uint32_t sb) {
+  BlockScale b;
+  if (kFmt == kMxFp4) {
+    b.zero = sb == 255u;
+    b.s = b.r = mx_e8m0_inverse(b.zero ? 127u : sb);
+  } else {
+    b.zero = sb == 0x7Fu || sb == 0u;
+    b.s = e4m3_to_f32(b.zero ? 0x38u : sb);
+    b.r = __frcp_rn(b.s);
+  }
+  return b;
+}
+template <int kFmt>
+__device__ __forceinline__ uint32_t encode8(float (&v)[8], const BlockScale& b, float inv_g) {
+  const uint64_t s = f32x2(kFmt == kMxFp4 ? b.s : -b.s, kFmt == kMxFp4 ? b.s : -b.s), r = f32x2(b.r, b.r);
+  const uint64_t ig = f32x2(inv_g, inv_g);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t x = f32x2(v[i], v[i + 1]);
+    float lo, hi;
+    if (kFmt == kMxFp4) {
+      f32x2_split(f32x2_mul(x, s), lo, hi);
+      v[i] = lo;
+      v[i + 1] = hi;
+    } else {
+      f32x2_split(mx_quotient2(f32x2_mul(x, ig), s, r), lo, hi);
+      v[i] = copysignf(lo, v[i]);
+      v[i + 1] = copysignf(hi, v[i + 1]);
+    }
+  }
+  const uint32_t c = mx_codes8(v);
+  return b.zero ? 0u : c;
+}
 __device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -72,56 +139,45 @@ __device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
   }
 }
 
-// The scale byte of a block (magnitude bits of bf16) and its eight codes per thread.
+// A warp's 1024 consecutive elements (32 per lane, from column c): codes and
+// scales to memory.  The four bytes of a scale tile's row leave as one word.
 template <int kFmt>
-__device__ __forceinline__ uint32_t scale_byte(uint32_t mag, bool bad, float inv_g) {
-  if (kFmt == kMxFp4) return bad ? 255u : mx_e8m0(mag << 16);
-  return bad ? 0x7Fu : mx_e4m3(__fdiv_rn(__fmul_rn(__uint_as_float(mag << 16), inv_g), 6.0f));
-}
-
-template <int kFmt>
-__device__ __forceinline__ uint32_t encode8(float (&v)[8], uint32_t sb, bool bad, float inv_g) {
-  if (bad) return 0u;
-  if (kFmt == kMxFp4) {
-    const float inv = mx_e8m0_inverse(sb);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], inv);
-  } else {
-    if (sb == 0u) return 0u;
-    const float s = e4m3_to_f32(sb), r = __frcp_rn(s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = mx_quotient(__fmul_rn(v[i], inv_g), s, r);
-  }
-  return mx_codes8(v);
-}
-
-// A warp's 256 consecutive elements (eight per lane, from column c): codes and
-// scales to memory.  Lanes of a block share its scale; the four bytes of a
-// scale tile's row leave as one word.
-template <int kFmt>
-__device__ __forceinline__ void emit256(const MxQuantArgs& a, int64_t row, int64_t c, const uint4& q, float inv_g) {
+__device__ __forceinline__ void emit1024(const MxQuantArgs& a, int64_t row, int64_t c, const Elems32& e, float inv_g) {
   const int lane = threadIdx.x & 31;
-  constexpr int kLanes = mx_block(kFmt) / 8;                 // lanes of a block
-  bool bad = false;
-  uint32_t mag = mag8(q, bad);
-  uint32_t key = bad ? (0x10000u | mag) : mag;
-#pragma unroll
-  for (int o = 1; o < kLanes; o <<= 1) {
-    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, key, o);
-    key = max(key & 0xFFFFu, other & 0xFFFFu) | ((key | other) & 0x10000u);
-  }
-  bad = (key >> 16) != 0;
-  mag = key & 0xFFFFu;
-  const uint32_t sb = scale_byte<kFmt>(mag, bad, inv_g);
+  uint4 out;
+  uint32_t* o = &out.x;
   float v[8];
-  unpack8(q, v);
-  const uint32_t codes = encode8<kFmt>(v, sb, bad, inv_g);
-  uint32_t word = sb << (8 * ((lane / kLanes) & 3));
-  word |= __shfl_xor_sync(0xFFFFFFFFu, word, kLanes);
-  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * kLanes);
-  if (row < a.rows && c < a.pitch * 2) *reinterpret_cast<uint32_t*>(a.codes + row * a.pitch + (c >> 1)) = codes;
-  const int64_t kt = c / (4 * mx_block(kFmt));
-  if ((lane & (4 * kLanes - 1)) == 0 && kt < a.kt)
+  uint32_t word;
+  if (kFmt == kMxFp4) {
+    const uint32_t sb = scale_byte<kFmt>(wider_half(__vmaxu2(mag16(e.q[0], e.q[1]), mag16(e.q[2], e.q[3]))), inv_g);
+    const BlockScale b = block_scale<kFmt>(sb);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      unpack8(e.q[i], v);
+      o[i] = encode8<kFmt>(v, b, inv_g);
+    }
+    word = sb << (8 * (lane & 3));
+    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
+    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
+  } else {
+    word = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t sb = scale_byte<kFmt>(wider_half(mag16(e.q[2 * h], e.q[2 * h + 1])), inv_g);
+      const BlockScale b = block_scale<kFmt>(sb);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        unpack8(e.q[2 * h + i], v);
+        o[2 * h + i] = encode8<kFmt>(v, b, inv_g);
+      }
+      word |= sb << (16 * (lane & 1) + 8 * h);
+    }
+    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
+  }
+  if (row < a.rows && c < a.pitch * 2) *reinterpret_cast<uint4*>(a.codes + row * a.pitch + (c >> 1)) = out;
+  constexpr int kTileElems = 4 * mx_block(kFmt);
+  const int64_t kt = c / kTileElems;
+  if ((lane & (kTileElems / 32 - 1)) == 0 && kt < a.kt)
     *reinterpret_cast<uint32_t*>(a.scales + mx_scale_offset(row, kt * 4, a.kt)) = word;
 }
 
@@ -147,8 +203,16 @@ __global__ void __launch_bounds__(kThreads) k_mx_amax(const uint16_t* in, int64_
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   uint32_t m = 0;
   bool bad = false;
-#pragma unroll 4
-  for (int64_t i = first; i < nvec; i += stride) m = max(m, mag8(__ldg(reinterpret_cast<const uint4*>(in) + i), bad));
+  constexpr int kBatch = 8;                  // loads in flight per thread
+  int64_t i = first;
+  for (; i + (kBatch - 1) * stride < nvec; i += kBatch * stride) {
+    uint4 q[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) q[j] = __ldg(reinterpret_cast<const uint4*>(in) + i + j * stride);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) m = max(m, finite_mag8(q[j]));
+  }
+  for (; i < nvec; i += stride) m = max(m, finite_mag8(__ldg(reinterpret_cast<const uint4*>(in) + i)));
   if (first < numel - nvec * 8) m = max(m, mx_finite_mag(in[nvec * 8 + first], bad));
   m = __reduce_max_sync(0xFFFFFFFFu, m);
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
@@ -159,7 +223,22 @@ __global__ void __launch_bounds__(kThreads) k_mx_amax(const uint16_t* in, int64_
   }
 }
 
-// One warp per 1024 elements of a row (four loads in flight per lane).
+// Units (row, segment) of a row-major walk with a fixed stride, without a
+// division per step.
+struct Walk {
+  int64_t row, seg, step_rows, step_segs, segs;
+  __device__ Walk(int64_t first, int64_t stride, int64_t per_row)
+      : row(first / per_row), seg(first - row * per_row), step_rows(stride / per_row),
+        step_segs(stride - step_rows * per_row), segs(per_row) {}
+  __device__ void next() {
+    row += step_rows;
+    seg += step_segs;
+    if (seg >= segs) { seg -= segs; ++row; }
+  }
+};
+
+// One warp per 1024 elements of a row.  With a global scale the rows go from the
+// last to the first: the maximum's pass has just left the last ones in L2.
 template <int kFmt, bool kVec>
 __global__ void __launch_bounds__(kThreads) k_mx_quant(const MxQuantArgs a) {
   float inv_g = 1.0f;
@@ -169,75 +248,68 @@ __global__ void __launch_bounds__(kThreads) k_mx_quant(const MxQuantArgs a) {
     if (blockIdx.x == 0 && threadIdx.x == 0) a.global_scale[0] = g;
   }
   const int lane = threadIdx.x & 31;
-  const int64_t segs = (a.kt * 4 * mx_block(kFmt) + 1023) / 1024;
-  const int64_t units = segs * a.tile_rows;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); u < units; u += stride) {
-    const int64_t row = u / segs, c0 = (u - row * segs) * 1024 + lane * 8;
-    const uint16_t* src = a.in + row * a.cols;
-    uint4 q[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      q[j] = row < a.rows ? load8<kVec>(src, c0 + j * 256, a.cols) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) emit256<kFmt>(a, row, c0 + j * 256, q[j], inv_g);
+  for (Walk w(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5),
+              static_cast<int64_t>(gridDim.x) * (kThreads / 32), (a.kt * 4 * mx_block(kFmt) + 1023) / 1024);
+       w.row < a.tile_rows; w.next()) {
+    const int64_t row = kFmt == kNvFp4 ? a.tile_rows - 1 - w.row : w.row, c = w.seg * 1024 + lane * 32;
+    Elems32 e{};
+    if (row < a.rows) e = load32<kVec>(a.in + row * a.cols, c, a.cols);
+    emit1024<kFmt>(a, row, c, e, inv_g);
   }
 }
 
-// NVFP4 with a global scale per row: one CTA per row.  The first 8192 elements
-// stay in registers between the row's maximum and its codes; the rest of a
-// longer row is read again (from L2).
-template <bool kVec>
-__global__ void __launch_bounds__(kThreads) k_mx_quant_rows(const MxQuantArgs a) {
-  __shared__ uint32_t s_max[kThreads / 32];
-  constexpr int kHeld = 4;
+// NVFP4 with a global scale per row: one CTA per row.  The first
+// kRowThreads * 32 * kHeld elements stay in registers between the row's maximum
+// and its codes; the rest of a longer row is read again (from L2).
+template <bool kVec, int kRowThreads, int kHeld>
+__global__ void __launch_bounds__(kRowThreads) k_mx_quant_rows(const MxQuantArgs a) {
+  __shared__ uint32_t s_max[32];
+  constexpr int kStep = kRowThreads * 32;
   const int64_t row = blockIdx.x;
   const uint16_t* src = a.in + row * a.cols;
   const int64_t span = a.kt * 64;
-  const int64_t c0 = threadIdx.x * 8;
-  uint4 held[kHeld];
+  const int64_t c0 = threadIdx.x * 32, w0 = (threadIdx.x & ~31) * 32;
+  Elems32 held[kHeld];
   uint32_t m = 0;
-  bool bad = false;
-  if (row < a.rows) {
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) held[j] = load8<kVec>(src, c0 + j * (kThreads * 8), a.cols);
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j) m = max(m, mag8(held[j], bad));
-#pragma unroll 4
-    for (int64_t c = c0 + kHeld * (kThreads * 8); c < a.cols; c += kThreads * 8)
-      m = max(m, mag8(load8<kVec>(src, c, a.cols), bad));
-  } else {
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j) held[j] = make_uint4(0, 0, 0, 0);
+  for (int j = 0; j < kHeld; ++j) {
+    held[j] = Elems32{};
+    if (row < a.rows) held[j] = load32<kVec>(src, c0 + j * kStep, a.cols);
   }
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, finite_mag8(held[j].q[i]));
+  if (row < a.rows)
+    for (int64_t c = kHeld * kStep + threadIdx.x * 8; c < a.cols; c += kRowThreads * 8)
+      m = max(m, finite_mag8(load8<kVec>(src, c, a.cols)));
   m = __reduce_max_sync(0xFFFFFFFFu, m);
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
-  m = s_max[0];
-#pragma unroll
-  for (int i = 1; i < kThreads / 32; ++i) m = max(m, s_max[i]);
+  m = __reduce_max_sync(0xFFFFFFFFu, s_max[threadIdx.x & (kRowThreads / 32 - 1)]);
   const float g = mx_global_scale(m << 16);
   const float inv_g = mx_pow2_inverse(g);
   if (threadIdx.x == 0 && row < a.rows) a.global_scale[row] = g;
-  // whole warps step together: emit256 shuffles
+  // whole warps step together: emit1024 shuffles
 #pragma unroll
   for (int j = 0; j < kHeld; ++j)
-    if ((threadIdx.x & ~31) * 8 + j * (kThreads * 8) < span)
-      emit256<kNvFp4>(a, row, c0 + j * (kThreads * 8), held[j], inv_g);
-  for (int64_t base = kHeld * (kThreads * 8) + (threadIdx.x & ~31) * 8; base < span; base += kThreads * 8) {
-    const int64_t c = base + (threadIdx.x & 31) * 8;
-    emit256<kNvFp4>(a, row, c, row < a.rows ? load8<kVec>(src, c, a.cols) : make_uint4(0, 0, 0, 0), inv_g);
+    if (w0 + j * kStep < span) emit1024<kNvFp4>(a, row, c0 + j * kStep, held[j], inv_g);
+  for (int64_t b = kHeld * kStep; w0 + b < span; b += kStep) {
+    Elems32 e{};
+    if (row < a.rows) e = load32<kVec>(src, c0 + b, a.cols);
+    emit1024<kNvFp4>(a, row, c0 + b, e, inv_g);
   }
 }
 
 // The transpose: result row k is column k of the input, blocks run along the
-// input's rows n.  A CTA takes 128 n x 64 k: rows of 128 bytes in, a column per
-// thread out of shared memory (32 n: one MXFP4 or two NVFP4 blocks, 16 bytes of codes).
-constexpr int kTileN = 128, kTileK = 64;
+// input's rows n.  A CTA takes 256 n x 64 k: rows of 128 bytes in; a thread then
+// takes 32 n of two neighbouring columns out of shared memory, whose magnitudes
+// it compares as pairs of 16 bits.
+constexpr int kTileN = 256, kTileK = 64;
 
 template <int kFmt, bool kVec>
 __global__ void __launch_bounds__(kThreads) k_mx_quant_t(const MxQuantArgs a) {
-  __shared__ uint16_t tile[kTileN][kTileK + 2];
+  __shared__ uint32_t tile[kTileN][kTileK / 2 + 1];
   float inv_g = 1.0f;
   if (kFmt == kNvFp4) {
     const float g = mx_global_scale(reduce_amax(a.amax, a.amax_n) << 16);
@@ -246,94 +318,121 @@ __global__ void __launch_bounds__(kThreads) k_mx_quant_t(const MxQuantArgs a) {
   }
   const int64_t n_tiles = (a.kt * 4 * mx_block(kFmt) + kTileN - 1) / kTileN;
   const int64_t k_tiles = (a.tile_rows + kTileK - 1) / kTileK;
-  for (int64_t u = blockIdx.x; u < n_tiles * k_tiles; u += gridDim.x) {
-    const int64_t k0 = u % k_tiles * kTileK, n0 = u / k_tiles * kTileN;
-    uint4 q[4];
+  for (Walk w(blockIdx.x, gridDim.x, k_tiles); w.row < n_tiles; w.next()) {
+    const int64_t k0 = w.seg * kTileK, n0 = (kFmt == kNvFp4 ? n_tiles - 1 - w.row : w.row) * kTileN;
+    uint4 q[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
       const int64_t n = n0 + (threadIdx.x >> 3) + 32 * j;
       q[j] = n < a.in_rows ? load8<kVec>(a.in + n * a.in_cols, k0 + (threadIdx.x & 7) * 8, a.in_cols)
                            : make_uint4(0, 0, 0, 0);
     }
     __syncthreads();                       // the tile's readers of the unit before are done
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(&tile[(threadIdx.x >> 3) + 32 * j][(threadIdx.x & 7) * 8]);
+    for (int j = 0; j < 8; ++j) {
+      uint32_t* dst = &tile[(threadIdx.x >> 3) + 32 * j][(threadIdx.x & 7) * 4];
       dst[0] = q[j].x; dst[1] = q[j].y; dst[2] = q[j].z; dst[3] = q[j].w;
     }
     __syncthreads();
-    const int kl = threadIdx.x & 63, nb = (threadIdx.x >> 6) * 32;
-    const int64_t k = k0 + kl, n = n0 + nb;
-    uint4 out;
-    uint32_t* ow = &out.x;
-    uint32_t sbytes = 0;
-    uint32_t mag = 0;
-    bool bad = false;
+    const int kp = threadIdx.x & 31, nb = (threadIdx.x >> 5) * 32;
+    const int64_t k = k0 + 2 * kp, n = n0 + nb;
+    uint32_t e[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) e[i] = tile[nb + i][kp];
     constexpr int kBlk = mx_block(kFmt);
+    uint4 out[2];
+    uint32_t sbytes[2] = {0, 0};
 #pragma unroll
     for (int b = 0; b < 32 / kBlk; ++b) {
-      mag = 0;
-      bad = false;
+      uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < kBlk; ++i) mag = max(mag, mx_finite_mag(tile[nb + b * kBlk + i][kl], bad));
-      const uint32_t sb = scale_byte<kFmt>(mag, bad, inv_g);
-      sbytes |= sb << (8 * b);
+      for (int i = 0; i < kBlk; ++i) m = mag_max2(m, e[b * kBlk + i]);
 #pragma unroll
-      for (int g8 = 0; g8 < kBlk / 8; ++g8) {
-        float v[8];
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t sb = scale_byte<kFmt>(h ? m >> 16 : m & 0xFFFFu, inv_g);
+        const BlockScale bs = block_scale<kFmt>(sb);
+        sbytes[h] |= sb << (8 * b);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = bf16_lo(tile[nb + b * kBlk + g8 * 8 + i][kl]);
-        ow[b * (kBlk / 8) + g8] = encode8<kFmt>(v, sb, bad, inv_g);
+        for (int g8 = 0; g8 < kBlk / 8; ++g8) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t x = e[b * kBlk + g8 * 8 + i];
+            v[i] = h ? bf16_hi(x) : bf16_lo(x);
+          }
+          (&out[h].x)[b * (kBlk / 8) + g8] = encode8<kFmt>(v, bs, inv_g);
+        }
       }
     }
-    if (k < a.rows && n < a.pitch * 2) *reinterpret_cast<uint4*>(a.codes + k * a.pitch + (n >> 1)) = out;
     const int64_t blk = n / kBlk;
-    if (k < a.tile_rows && blk < a.kt * 4) {
-      uint8_t* dst = a.scales + mx_scale_offset(k, blk, a.kt);
-      if (kFmt == kMxFp4) *dst = static_cast<uint8_t>(sbytes);
-      else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(sbytes);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (k + h < a.rows && n < a.pitch * 2) *reinterpret_cast<uint4*>(a.codes + (k + h) * a.pitch + (n >> 1)) = out[h];
+      if (k + h < a.tile_rows && blk < a.kt * 4) {
+        uint8_t* dst = a.scales + mx_scale_offset(k + h, blk, a.kt);
+        if (kFmt == kMxFp4) *dst = static_cast<uint8_t>(sbytes[h]);
+        else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(sbytes[h]);
+      }
     }
   }
 }
 
-// Eight codes (one 32-bit word, element j in bits 4j) times their scale -> bf16.
+// Eight codes (element j in bits 4j .. 4j+3) -> four pairs of halves, exact.
+__device__ __forceinline__ void mx_levels8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+
+// Codes times their scale -> bf16; one warp per 1024 elements of a row.
 template <int kFmt, bool kVec>
 __global__ void __launch_bounds__(kThreads)
 k_mx_dequant(const uint8_t* codes, const uint8_t* scales, const float* gs, int per_row, int64_t rows, int64_t cols,
              int64_t pitch, int64_t kt, uint16_t* out) {
-  const int64_t per = (cols + 7) / 8;
-  const int64_t units = rows * per;
+  const int lane = threadIdx.x & 31;
   const float g0 = (kFmt == kNvFp4 && !per_row) ? __ldg(gs) : 1.0f;
-#pragma unroll 4
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; u < units;
-       u += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t row = u / per, c = (u - row * per) * 8;
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes + row * pitch + (c >> 1)));
-    const uint32_t sb = __ldg(scales + mx_scale_offset(row, c / mx_block(kFmt), kt));
-    float s;
-    if (kFmt == kMxFp4) s = mx_e8m0_value(sb);
-    else s = e4m3_to_f32(sb);
-    const float g = kFmt == kNvFp4 ? (per_row ? __ldg(gs + row) : g0) : 1.0f;
-    uint32_t o[4];
+  for (Walk w(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5),
+              static_cast<int64_t>(gridDim.x) * (kThreads / 32), (cols + 1023) / 1024);
+       w.row < rows; w.next()) {
+    const int64_t c0 = w.seg * 1024 + lane * 8;
+    const float g = kFmt == kNvFp4 ? (per_row ? __ldg(gs + w.row) : g0) : 1.0f;
+    uint32_t word[4], sb[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float f[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t code = (w >> (8 * i + 4 * h)) & 15u;
-        const uint32_t m = code & 7u;                           // 0, 1/2, then (1 + m0/2) 2^(e-1)
-        const uint32_t bits = m < 2u ? (m ? 0x3F000000u : 0u) : (((m >> 1) + 126u) << 23) | ((m & 1u) << 22);
-        f[h] = __fmul_rn(__fmul_rn(__uint_as_float(bits | ((code & 8u) << 28)), s), g);
+    for (int j = 0; j < 4; ++j) {
+      const int64_t c = c0 + j * 256;
+      word[j] = sb[j] = 0;
+      if (c < cols) {
+        word[j] = __ldg(reinterpret_cast<const uint32_t*>(codes + w.row * pitch + (c >> 1)));
+        sb[j] = __ldg(scales + mx_scale_offset(w.row, c / mx_block(kFmt), kt));
       }
-      const __nv_bfloat162 p = __floats2bfloat162_rn(f[0], f[1]);
-      o[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
-    if constexpr (kVec) {
-      *reinterpret_cast<uint4*>(out + row * cols + c) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < cols) out[row * cols + c + i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+    for (int j = 0; j < 4; ++j) {
+      const int64_t c = c0 + j * 256;
+      if (c >= cols) continue;
+      const float s = kFmt == kMxFp4 ? mx_e8m0_value(sb[j]) : e4m3_to_f32(sb[j]);
+      uint32_t h[4], o[4];
+      mx_levels8(word[j], h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        float lo = __fmul_rn(f.x, s), hi = __fmul_rn(f.y, s);
+        if (kFmt == kNvFp4) { lo = __fmul_rn(lo, g); hi = __fmul_rn(hi, g); }
+        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+        o[i] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      uint16_t* dst = out + w.row * cols + c;
+      if constexpr (kVec) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i < cols) dst[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+      }
     }
   }
 }
@@ -349,7 +448,12 @@ cudaError_t quant_t(bool transpose, const MxQuantArgs& a, int num_sms, cudaStrea
     const int64_t units = (a.kt * 4 * mx_block(kFmt) + kTileN - 1) / kTileN * ((a.tile_rows + kTileK - 1) / kTileK);
     k_mx_quant_t<kFmt, kVec><<<grid_of(units, num_sms, 8), kThreads, 0, stream>>>(a);
   } else if (kFmt == kNvFp4 && a.per_row) {
-    k_mx_quant_rows<kVec><<<static_cast<unsigned>(a.tile_rows), kThreads, 0, stream>>>(a);
+    // registers for the whole row where that is possible
+    const unsigned grid = static_cast<unsigned>(a.tile_rows);
+    if (a.cols <= 4096) k_mx_quant_rows<kVec, 128, 1><<<grid, 128, 0, stream>>>(a);
+    else if (a.cols <= 8192) k_mx_quant_rows<kVec, 256, 1><<<grid, 256, 0, stream>>>(a);
+    else if (a.cols <= 16384) k_mx_quant_rows<kVec, 512, 1><<<grid, 512, 0, stream>>>(a);
+    else k_mx_quant_rows<kVec, 1024, 1><<<grid, 1024, 0, stream>>>(a);
   } else {
     const int64_t segs = (a.kt * 4 * mx_block(kFmt) + 1023) / 1024;
     const int64_t ctas = (segs * a.tile_rows + kThreads / 32 - 1) / (kThreads / 32);
@@ -375,8 +479,8 @@ cudaError_t launch_mx_quant(int fmt, bool transpose, const MxQuantArgs& a, int n
 cudaError_t launch_mx_dequant(int fmt, const uint8_t* codes, const uint8_t* scales, const float* global_scale,
                               int per_row, int64_t rows, int64_t cols, int64_t pitch, int64_t kt, uint16_t* out,
                               int num_sms, cudaStream_t stream) {
-  const int64_t units = rows * ((cols + 7) / 8);
-  const int grid = grid_of((units + kThreads - 1) / kThreads, num_sms, 8);
+  const int64_t units = rows * ((cols + 1023) / 1024);
+  const int grid = grid_of((units + kThreads / 32 - 1) / (kThreads / 32), num_sms, 8);
   const bool vec = cols % 8 == 0;
 #define QLORA_MX_DEQUANT(F, V) \
   k_mx_dequant<F, V><<<grid, kThreads, 0, stream>>>(codes, scales, global_scale, per_row, rows, cols, pitch, kt, out)

@@ -65,14 +65,35 @@ __device__ __forceinline__ float mx_global_scale(uint32_t amax_bits) {
 // 1 / g of a power of two in [2^-126, 2^127).
 __device__ __forceinline__ float mx_pow2_inverse(float g) { return __uint_as_float((254u << 23) - __float_as_uint(g)); }
 
-// Quotient v / s rounded to nearest, from r = RN(1 / s): one Newton step on the
-// remainder.  Where v / s is exactly half way between two levels it is
-// representable and the step returns it exactly, so the tie stays a tie; every
-// other quotient of an 8-bit by a 4-bit significand is 2^-9 away from one.  The
-// step turns -0 into +0, so the sign is put back.
-__device__ __forceinline__ float mx_quotient(float v, float s, float r) {
-  const float q = __fmul_rn(v, r);
-  return copysignf(__fmaf_rn(__fmaf_rn(-q, s, v), r, q), v);
+// Pairs of floats (sm_100's f32x2 arithmetic, each half rounded to nearest even
+// as the scalar operation is).
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void f32x2_split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+
+// Quotients v / s rounded to nearest, from r = RN(1 / s): one Newton step on the
+// remainder (minus_s = -s).  Where v / s is exactly half way between two levels
+// it is representable and the step returns it exactly, so the tie stays a tie;
+// every other quotient of an 8-bit by a 4-bit significand is 2^-8 away from one.
+// The step turns -0 into +0, so the caller puts the sign back.
+__device__ __forceinline__ uint64_t mx_quotient2(uint64_t v, uint64_t minus_s, uint64_t r) {
+  const uint64_t q = f32x2_mul(v, r);
+  return f32x2_fma(f32x2_fma(q, minus_s, v), r, q);
 }
 
 // bf16 bits -> magnitude bits with non-finite values as zero, and whether any was seen.
