@@ -40,6 +40,8 @@ struct MxQuantArgs {
   int per_row;
   uint32_t* amax;            // NVFP4, one global scale: partial maxima [amax_n]
   int amax_n;
+  uint32_t* zero;            // words cleared on the way (the counters of the next kernel)
+  int zero_n;
 };
 
 cudaError_t launch_mx_amax(const uint16_t* in, int64_t numel, uint32_t* partials, int grid, cudaStream_t stream);
@@ -55,37 +57,51 @@ struct MxGemmArgs {
   const uint8_t* w_scales;   // scale tiles of the weight [rows, k]
   const uint8_t* x_scales;   // and of the activations [m, k]
   int64_t kt;                // scale tiles along k (the same for both)
-  const float* w_global;     // NVFP4: [1] or [rows]; null: none
+  const float* w_global;     // NVFP4: [1] or [rows]
   int w_per_row;
-  const float* x_global;     // NVFP4: [m]; null: none
+  const float* x_global;     // NVFP4: [m]
   int64_t rows, m, k;
   int ksteps;                // ceil(k / 256)
   int lora_steps;            // 64-wide steps of the rank-r term (0: none)
   int lora_mn;               // its weight-side operand: 0 [rows, r], 1 [r, rows] (rows contiguous)
   uint16_t* out;             // bf16 [m, rows]
-  int m_tiles, t_tiles;      // tiles of 128 rows, of the kernel's token tile
-  int m_group;               // row tiles swept across all token tiles before the next group
-  int splits;                // CTAs (one cluster) that share a tile's contraction: 1, 2, 4 or 8
+  int m_tiles, t_tiles;      // tiles of rows (128, of a pair 256) and of tokens
+  // pairs: row tiles swept across all token tiles before the next group
+  int m_group;
+  // streams: partial tiles [runs][2][m][128] and the row tiles' counters (zero)
+  float* slots;
+  uint32_t* counters;
   uint32_t* err;
 };
-// Token tile for m tokens (16, 32, 64 or 128; below 128 only one tile).
-int mx_token_tile(int64_t m);
 // Tensor maps: w / x the codes as uint8 [rows or m][pitch], 128B swizzle, box
-// {128, 128} / {128, token tile}; lora_w bf16, box {64, 128} ([rows, r]) or
-// {64, 64} ([r, rows]); lora_x bf16 [m, 64 lora_steps], box {64, token tile}.
-cudaError_t launch_mx_gemm(int fmt, const MxGemmArgs& a, const CUtensorMap& w, const CUtensorMap& x,
-                           const CUtensorMap& lora_w, const CUtensorMap& lora_x, int num_sms, cudaStream_t stream);
-
-// The same product for many tokens (mx_pair.cu): pairs of CTAs on tiles of 256
-// rows x token_tile (256 or 128) tokens; m_tiles counts 256 rows, splits is 1.
-// Maps: w / x as above with boxes {128, 128} / {128, token_tile / 2}; the scale
-// tiles as 32-bit words [row tiles * kt][128], box {128, 2 (MXFP4) or 4};
-// lora_x with box {64, token_tile / 2}.
-struct MxPairMaps {
+// {128, 128} / {128, x rows}; w_scales / x_scales the scale tiles as 32-bit
+// words [row tiles * kt][128], box {128, 2 (MXFP4) or 4} (pairs only); lora_w
+// bf16, box {64, 128} ([rows, r]) or {64, 64} ([r, rows]); lora_x bf16
+// [m, 64 lora_steps], box {64, x rows}.
+struct MxMaps {
   CUtensorMap w, x, w_scales, x_scales, lora_w, lora_x;
 };
-cudaError_t launch_mx_pair(int fmt, int token_tile, const MxGemmArgs& a, const MxPairMaps& m, int num_sms,
+// Few tokens (mx_stream.cu): one tile of 16, 32 or 64 tokens (x rows the same).
+constexpr int kMxMaxRuns = 256;             // CTAs at most: the work buffer's slots are sized by it
+cudaError_t launch_mx_stream(int fmt, int token_tile, const MxGemmArgs& a, const MxMaps& m, int num_sms,
+                             cudaStream_t stream);
+// Many tokens (mx_pair.cu): tiles of 256 rows x 256 or 128 tokens (x rows half of it).
+cudaError_t launch_mx_pair(int fmt, int token_tile, const MxGemmArgs& a, const MxMaps& m, int num_sms,
                            cudaStream_t stream);
+
+// X A^T for at most 64 tokens (mx_xa.cu), as run_rank_xa gives it for more.
+struct MxXaArgs {
+  const uint16_t* x;         // bf16 [m, k]
+  const uint16_t* a;         // bf16 [r, k]
+  int64_t k;                 // a multiple of 64
+  int m, r, rpad;
+  float s;
+  float* xa;                 // fp32 [m, r] or null
+  uint16_t* sxa;             // bf16 [m, rpad]: s X A^T [/ (row_div all_div)], zero from column r
+  const float* row_div;      // [m] or null
+  const float* all_div;
+};
+cudaError_t launch_mx_xa(const MxXaArgs& a, cudaStream_t stream);
 
 // Mixture-of-experts layer for at most 16 tokens (mx_moe.cu).
 constexpr int kMoeMaxExperts = 1024, kMoeMaxTopK = 16, kMoeMaxTokens = 16;

@@ -52,28 +52,54 @@ ActLayout act_layout(int format, int64_t m, int64_t k, size_t base) {
   return l;
 }
 
-struct MxFwdLayout {
-  XaLayout xa;
+// Tokens up to which the product streams the weight (mx_stream.cu) rather than
+// tiling the tokens over pairs (mx_pair.cu).
+constexpr int64_t kMxStreamTokens = 64;
+
+// What one product needs beside its operands: a streamed one's counters (one per
+// 128 weight rows) and partial tiles.
+struct ProductLayout {
   ActLayout act;
+  size_t counters, slots, end;
 };
-MxFwdLayout mx_fwd_layout(int format, int64_t cols, int64_t m, int r, const LinearShape& sh) {
+ProductLayout product_layout(int format, int64_t rows, int64_t k, int64_t m, size_t base) {
+  ProductLayout l{};
+  l.act = act_layout(format, m, k, base);
+  size_t o = l.act.end;
+  l.counters = o;
+  l.slots = o;
+  if (m <= kMxStreamTokens) {
+    o = round_up(o + static_cast<size_t>((rows + 127) / 128) * 4, 256);
+    l.slots = o;
+    o += size_t{kMxMaxRuns} * 2 * m * 128 * sizeof(float);
+  }
+  l.end = o;
+  return l;
+}
+
+struct MxFwdLayout {
+  XaLayout xa;             // of its members only sxa for few tokens
+  ProductLayout product;
+};
+MxFwdLayout mx_fwd_layout(int format, int64_t rows, int64_t cols, int64_t m, int r, const LinearShape& sh) {
   MxFwdLayout l{};
-  if (r) l.xa = xa_layout(sh, 0);
-  l.act = act_layout(format, m, cols, l.xa.end);
+  if (r && m > kMxStreamTokens) l.xa = xa_layout(sh, 0);
+  else if (r) l.xa.end = round_up(static_cast<size_t>(m) * sh.rpad * 2, 256);
+  l.product = product_layout(format, rows, cols, m, l.xa.end);
   return l;
 }
 struct MxBwdLayout {
   BwdLayout lora;
   size_t sg_div;           // NVFP4: bf16(s G / (gx gw))
-  ActLayout act;
+  ProductLayout product;
 };
-MxBwdLayout mx_bwd_layout(int format, int64_t rows, int64_t m, int r, const LinearShape& sh) {
+MxBwdLayout mx_bwd_layout(int format, int64_t rows, int64_t cols, int64_t m, int r, const LinearShape& sh) {
   MxBwdLayout l{};
   if (r) l.lora = bwd_layout(sh);
   size_t o = round_up(l.lora.total, 256);
   l.sg_div = o;
   if (r && format == QLORA_NVFP4) o = round_up(o + static_cast<size_t>(m) * sh.rpad * 2, 256);
-  l.act = act_layout(format, m, rows, o);
+  l.product = product_layout(format, cols, rows, m, o);
   return l;
 }
 
@@ -85,14 +111,6 @@ qlora_status mx_layer_shape(int64_t rows, int64_t cols, int64_t M, int32_t r, Li
   return QLORA_OK;
 }
 
-// K splits (CTAs of one cluster) of a product of `tiles` tiles: as many as
-// leave every CTA two k-steps and do not exceed two CTAs an SM.
-int mx_splits(int64_t tiles, int ksteps, int num_sms) {
-  int s = 1;
-  while (s < 8 && tiles * s * 2 <= 2 * static_cast<int64_t>(num_sms) && ksteps >= 4 * s) s *= 2;
-  return s;
-}
-
 // Row tiles swept across all token tiles before the next group: about 48 MB of
 // weight codes, so that they stay in L2 meanwhile.
 int mx_group(int m_tiles, int64_t pitch) {
@@ -102,8 +120,9 @@ int mx_group(int m_tiles, int64_t pitch) {
 }
 
 // q(X) into the work buffer (NVFP4: a global scale per token).
-cudaError_t quantize_acts(const qlora_mx_tensor* W, const uint16_t* X, int64_t M, uint8_t* ws, const ActLayout& L,
+cudaError_t quantize_acts(const qlora_mx_tensor* W, const uint16_t* X, int64_t M, uint8_t* ws, const ProductLayout& P,
                           const DeviceInfo& d, cudaStream_t cs) {
+  const ActLayout& L = P.act;
   MxQuantArgs a{};
   a.in = X;
   a.in_rows = a.rows = a.tile_rows = M;
@@ -114,6 +133,10 @@ cudaError_t quantize_acts(const qlora_mx_tensor* W, const uint16_t* X, int64_t M
   a.pitch = mx_pitch(W->cols);
   a.kt = mx_tiles_k(W->format, W->cols);
   a.per_row = W->format == QLORA_NVFP4;
+  if (M <= kMxStreamTokens) {
+    a.zero = reinterpret_cast<uint32_t*>(ws + P.counters);
+    a.zero_n = static_cast<int>((W->rows + 127) / 128);
+  }
   return counted(launch_mx_quant(W->format, false, a, d.num_sms, cs));
 }
 
@@ -126,12 +149,13 @@ int pair_token_tile(int64_t rows, int64_t m, int num_sms) {
   return narrow < wide ? 128 : 256;
 }
 
-// out [M, W->rows] = q(X) deq(W)^T + lora_x lora_w (see mx_gemm.cu).
-qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const ActLayout& L, const uint16_t* lora_w,
+// out [M, W->rows] = q(X) deq(W)^T + lora_x lora_w (see mx_stream.cu).
+qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const ProductLayout& P, const uint16_t* lora_w,
                          bool lora_mn, const uint16_t* lora_x, int r, int lora_steps, uint16_t* out,
                          const DeviceInfo& d, cudaStream_t cs) {
-  const bool pair = M > 128;
-  const int bn = pair ? pair_token_tile(W->rows, M, d.num_sms) : mx_token_tile(M);
+  const ActLayout& L = P.act;
+  const bool pair = M > kMxStreamTokens;
+  const int bn = pair ? pair_token_tile(W->rows, M, d.num_sms) : M <= 16 ? 16 : M <= 32 ? 32 : 64;
   const int box_x = pair ? bn / 2 : bn;
   const int64_t pitch = mx_pitch(W->cols);
   MxGemmArgs a{};
@@ -155,10 +179,11 @@ qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const
   if (m_tiles * t_tiles > (int64_t{1} << 28) || w_tiles > kMxMaxDim || x_tiles > kMxMaxDim) return QLORA_ERR_SHAPE;
   a.m_tiles = static_cast<int>(m_tiles);
   a.t_tiles = static_cast<int>(t_tiles);
-  a.m_group = mx_group(a.m_tiles, pair ? 2 * pitch : pitch);
-  a.splits = pair ? 1 : mx_splits(m_tiles * t_tiles, a.ksteps, d.num_sms);
+  a.m_group = mx_group(a.m_tiles, 2 * pitch);
+  a.slots = reinterpret_cast<float*>(ws + P.slots);
+  a.counters = reinterpret_cast<uint32_t*>(ws + P.counters);
   a.err = d.err;
-  MxPairMaps m;
+  MxMaps m;
   const uint64_t up = static_cast<uint64_t>(pitch);
   if (!make_map_u8(&m.w, W->codes, up, static_cast<uint64_t>(W->rows), up, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map_u8(&m.x, ws + L.codes, up, static_cast<uint64_t>(M), up, 128, static_cast<uint32_t>(box_x),
@@ -182,7 +207,7 @@ qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const
       return QLORA_ERR_CUDA;
     e = launch_mx_pair(W->format, bn, a, m, d.num_sms, cs);
   } else {
-    e = launch_mx_gemm(W->format, a, m.w, m.x, m.lora_w, m.lora_x, d.num_sms, cs);
+    e = launch_mx_stream(W->format, bn, a, m, d.num_sms, cs);
   }
   return counted(e) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
@@ -293,8 +318,8 @@ qlora_status qlora_mx_linear_workspace_size(int64_t rows, int64_t cols, int32_t 
   LinearShape sh{};
   const qlora_status st = mx_layer_shape(rows, cols, M, r, &sh);
   if (st != QLORA_OK) return st;
-  if (fwd_bytes) *fwd_bytes = mx_fwd_layout(format, cols, M, r, sh).act.end;
-  if (bwd_bytes) *bwd_bytes = mx_bwd_layout(format, rows, M, r, sh).act.end;
+  if (fwd_bytes) *fwd_bytes = mx_fwd_layout(format, rows, cols, M, r, sh).product.end;
+  if (bwd_bytes) *bwd_bytes = mx_bwd_layout(format, rows, cols, M, r, sh).product.end;
   return QLORA_OK;
 }
 
@@ -311,24 +336,40 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, in
       (r && (!aligned16(A) || !aligned16(B) || (XA_out && !aligned16(XA_out)))))
     return QLORA_ERR_ALIGN;
   if (r && !std::isfinite(s)) return QLORA_ERR_SHAPE;
-  const MxFwdLayout L = mx_fwd_layout(W->format, W->cols, M, r, sh);
-  if (workspace_bytes < L.act.end) return QLORA_ERR_WORKSPACE;
+  const MxFwdLayout L = mx_fwd_layout(W->format, W->rows, W->cols, M, r, sh);
+  if (workspace_bytes < L.product.end) return QLORA_ERR_WORKSPACE;
   DeviceInfo d;
   if ((st = device_info(&d)) != QLORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (quantize_acts(W, X, M, ws, L.act, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
+  if (quantize_acts(W, X, M, ws, L.product, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
   const uint16_t* sxa = nullptr;
   if (r) {
     RankDivide div;
     if (W->format == QLORA_NVFP4) {
-      div.row = reinterpret_cast<const float*>(ws + L.act.global);
+      div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
       div.all = W->global_scale;
     }
-    if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, div, d, cs)) != QLORA_OK) return st;
     sxa = reinterpret_cast<const uint16_t*>(ws + L.xa.sxa);
+    if (M > kMxStreamTokens) {
+      if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, div, d, cs)) != QLORA_OK) return st;
+    } else {
+      MxXaArgs xa{};
+      xa.x = X;
+      xa.a = A;
+      xa.k = W->cols;
+      xa.m = static_cast<int>(M);
+      xa.r = r;
+      xa.rpad = sh.rpad;
+      xa.s = s;
+      xa.xa = XA_out;
+      xa.sxa = reinterpret_cast<uint16_t*>(ws + L.xa.sxa);
+      xa.row_div = div.row;
+      xa.all_div = div.all;
+      if (counted(launch_mx_xa(xa, cs)) != cudaSuccess) return QLORA_ERR_CUDA;
+    }
   }
-  return run_mx_gemm(W, M, ws, L.act, B, false, sxa, r, r ? sh.lora_steps : 0, Y, d, cs);
+  return run_mx_gemm(W, M, ws, L.product, B, false, sxa, r, r ? sh.lora_steps : 0, Y, d, cs);
 }
 
 qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, const uint16_t* dY, int64_t M,
@@ -347,27 +388,27 @@ qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, c
              (XA && !aligned16(XA)))))
     return QLORA_ERR_ALIGN;
   if (r && !std::isfinite(s)) return QLORA_ERR_SHAPE;
-  MxBwdLayout L = mx_bwd_layout(WT->format, rows, M, r, sh);
-  if (workspace_bytes < L.act.end) return QLORA_ERR_WORKSPACE;
+  MxBwdLayout L = mx_bwd_layout(WT->format, rows, cols, M, r, sh);
+  if (workspace_bytes < L.product.end) return QLORA_ERR_WORKSPACE;
   DeviceInfo d;
   if ((st = device_info(&d)) != QLORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (dX && quantize_acts(WT, dY, M, ws, L.act, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
+  if (dX && quantize_acts(WT, dY, M, ws, L.product, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
   const uint16_t* sg = nullptr;
   if (r) {
     // G = dY B and X A^T as the backward over an NF4 weight has them
     RankDivide div;
     sg = reinterpret_cast<const uint16_t*>(ws + L.lora.sg);
     if (dX && WT->format == QLORA_NVFP4) {
-      div.row = reinterpret_cast<const float*>(ws + L.act.global);
+      div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
       div.all = WT->global_scale;
       div.out = reinterpret_cast<uint16_t*>(ws + L.sg_div);
       sg = div.out;
     }
     if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L.lora, div, d, cs)) != QLORA_OK) return st;
   }
-  if (dX && (st = run_mx_gemm(WT, M, ws, L.act, A, true, sg, r, r ? sh.lora_steps : 0, dX, d, cs)) != QLORA_OK) return st;
+  if (dX && (st = run_mx_gemm(WT, M, ws, L.product, A, true, sg, r, r ? sh.lora_steps : 0, dX, d, cs)) != QLORA_OK) return st;
   return r ? run_lora_grads(sh, X, dY, s, XA, dA, dB, ws, &L.lora, d, cs) : QLORA_OK;
 }
 

@@ -223,6 +223,14 @@ __global__ void __launch_bounds__(kThreads) k_mx_amax(const uint16_t* in, int64_
   }
 }
 
+// What a kernel that reads the result may do meanwhile: start, and wait for this
+// grid before it reads.  Its counters are cleared here.
+__device__ __forceinline__ void open_dependents(const MxQuantArgs& a) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.zero_n; i += blockDim.x) a.zero[i] = 0u;
+}
+
 // Units (row, segment) of a row-major walk with a fixed stride, without a
 // division per step.
 struct Walk {
@@ -241,6 +249,7 @@ struct Walk {
 // last to the first: the maximum's pass has just left the last ones in L2.
 template <int kFmt, bool kVec>
 __global__ void __launch_bounds__(kThreads) k_mx_quant(const MxQuantArgs a) {
+  open_dependents(a);
   float inv_g = 1.0f;
   if (kFmt == kNvFp4) {
     const float g = mx_global_scale(reduce_amax(a.amax, a.amax_n) << 16);
@@ -263,6 +272,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_quant(const MxQuantArgs a) {
 // and its codes; the rest of a longer row is read again (from L2).
 template <bool kVec, int kRowThreads, int kHeld>
 __global__ void __launch_bounds__(kRowThreads) k_mx_quant_rows(const MxQuantArgs a) {
+  open_dependents(a);
   __shared__ uint32_t s_max[32];
   constexpr int kStep = kRowThreads * 32;
   const int64_t row = blockIdx.x;

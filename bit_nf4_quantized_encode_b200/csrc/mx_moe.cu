@@ -8,7 +8,7 @@
 //   k_moe_down   per expert in use: o = W2 q(h); y[t] = sum_j p[t, j] o_j[t],
 //                summed in the order of j by the CTA that completes a row tile.
 //
-// Both products are those of mx_gemm.cu: the weight is the 128-row operand of
+// Both products are those of mx_stream.cu: the weight is the 128-row operand of
 // tcgen05's block-scaled kind, the 16 token slots the other one, whichever of
 // them an expert serves.  An expert in use has its weight read once, whatever
 // the number of its tokens, which is what bounds the layer (17/32 byte per

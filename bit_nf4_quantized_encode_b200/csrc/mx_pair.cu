@@ -1,6 +1,6 @@
 // mx_pair.cu -- the product of two microscaled 4-bit operands for many tokens:
 // pairs of CTAs (cta_group::2) on one tile of 256 weight rows x 256 (or 128)
-// tokens (sm_100a).  The formula and the operands are those of mx_gemm.cu.
+// tokens (sm_100a).  The formula and the operands are those of mx_stream.cu.
 //
 // Why pairs: one CTA's 128 x 256 tile reads 12 KB of shared memory per 64 of the
 // contraction and TMA writes as much, which is what bounds it; a pair holds each
@@ -256,7 +256,7 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
 }
 
 template <int kFmt, int kBN>
-cudaError_t launch_t(const MxGemmArgs& a, const MxPairMaps& m, int num_sms, cudaStream_t stream) {
+cudaError_t launch_t(const MxGemmArgs& a, const MxMaps& m, int num_sms, cudaStream_t stream) {
   static std::atomic<uint64_t> attr_done{0};
   constexpr size_t smem = pair_smem(kFmt, kBN);
   int dev = 0;
@@ -285,7 +285,7 @@ cudaError_t launch_t(const MxGemmArgs& a, const MxPairMaps& m, int num_sms, cuda
 
 }  // namespace
 
-cudaError_t launch_mx_pair(int fmt, int token_tile, const MxGemmArgs& a, const MxPairMaps& m, int num_sms,
+cudaError_t launch_mx_pair(int fmt, int token_tile, const MxGemmArgs& a, const MxMaps& m, int num_sms,
                            cudaStream_t stream) {
   if (fmt == kMxFp4)
     return token_tile == 256 ? launch_t<kMxFp4, 256>(a, m, num_sms, stream) : launch_t<kMxFp4, 128>(a, m, num_sms, stream);

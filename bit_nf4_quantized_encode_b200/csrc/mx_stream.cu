@@ -1,0 +1,356 @@
+// mx_stream.cu -- the product of two microscaled 4-bit operands for few tokens
+// (at most 64) on tcgen05's block-scaled instructions (sm_100a).
+//
+//   out[t, n] = bf16( gx[t] gw[n] sum_k x[t, k] w[n, k]  +  lora_x[t] . lora_w[n] )
+//
+// x and w are e2m1 codes times block scales (E8M0 per 32 or E4M3 per 16), gx
+// and gw the global scales of NVFP4.  The tensor core multiplies by the block
+// scales itself and sums in fp32, so nothing is expanded: per 256 elements of
+// the contraction a stage holds 128 bytes of codes per row and the scale tiles,
+// which tcgen05.cp moves to TMEM.  The weight is the M operand (128 rows), the
+// tokens the N operand.  The rank-r term is a bf16 x bf16 product accumulated
+// into the same TMEM tile (64 ranks a step); with global scales its activation
+// side arrives divided by gx gw.
+//
+// The weight's bytes bound it, so every SM has to stream all the time: the steps
+// of all row tiles, one after the other, are dealt to the SMs in equal runs.  A
+// tile that two or more runs share is joined by the CTA that completes its count:
+// partial tiles lie in the work buffer and are summed in the order of the runs.
+// The first stages' weight tiles are requested before the kernel that quantises
+// the activations has ended.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "mx.h"
+#include "mx_ptx.cuh"
+
+namespace qlora {
+namespace {
+
+constexpr int kThreads = 6 * 32;            // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
+constexpr int kABytes = 128 * 128;          // 128 rows x 256 codes
+
+__host__ __device__ constexpr int atoms_of(int fmt) { return fmt == kMxFp4 ? 2 : 4; }
+__host__ __device__ constexpr int stream_stage(int fmt, int bn) { return kABytes + bn * 128 + 2 * atoms_of(fmt) * 512; }
+__host__ __device__ constexpr int stream_stages(int fmt, int bn) { return (224 * 1024 - 2048) / stream_stage(fmt, bn); }
+__host__ __device__ constexpr size_t stream_smem(int fmt, int bn) {
+  return 1024 + static_cast<size_t>(stream_stages(fmt, bn)) * stream_stage(fmt, bn) + 512;
+}
+__host__ __device__ constexpr uint32_t stream_cols(int fmt, int bn) {
+  const int need = 2 * bn + 2 * 4 * atoms_of(fmt);
+  uint32_t c = 32;
+  while (static_cast<int>(c) < need) c *= 2;
+  return c;
+}
+
+template <int kFmt, int kBN>
+__global__ void __launch_bounds__(kThreads, 1)
+k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+            const __grid_constant__ CUtensorMap lwmap, const __grid_constant__ CUtensorMap lxmap) {
+  constexpr int kStages = stream_stages(kFmt, kBN);
+  constexpr int kStageBytes = stream_stage(kFmt, kBN);
+  constexpr int kAtoms = atoms_of(kFmt);
+  constexpr uint32_t kCols = stream_cols(kFmt, kBN);
+  constexpr uint32_t kSfa = 2 * kBN, kSfb = kSfa + 4 * kAtoms;      // TMEM columns of the scales
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem_gen = smem_raw + (smem0 - smem_u32(smem_raw));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem_gen + kStages * kStageBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;      // [2]
+  uint64_t* acc_empty = acc_full + 2;        // [2]
+  uint64_t* epi_bar = acc_empty + 2;         // the 128 epilogue threads meet here (bounded waits)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
+  uint32_t* last_flag = tmem_slot + 1;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int per_tile = a.ksteps + a.lora_steps;
+  const int64_t total = static_cast<int64_t>(a.m_tiles) * per_tile;
+  const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+  const int tile0 = static_cast<int>(begin / per_tile), step0 = static_cast<int>(begin - static_cast<int64_t>(tile0) * per_tile);
+  const int nsteps = static_cast<int>(end - begin);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 128);
+    }
+    mbar_init(epi_bar, 128);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kCols);
+    tmem_relinquish();
+  }
+  if (warp == 0 && elect_one()) {
+    tma_prefetch_desc(&wmap);
+    tma_prefetch_desc(&xmap);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA producer
+    // weight side of step (tile, j) into a stage, with the stage's byte count
+    auto load_w = [&](int stage, int tile, int j) {
+      uint8_t* sA = smem_gen + stage * kStageBytes;
+      if (j < a.ksteps) {
+        const uint32_t sbytes = static_cast<uint32_t>(min(kAtoms, static_cast<int>(a.kt) - j * kAtoms) * 512);
+        mbar_arrive_expect_tx(&full[stage], kABytes + kBN * 128 + 2 * sbytes);
+        tma_load_2d(sA, &wmap, j * 128, tile * 128, &full[stage]);
+        bulk_load(sA + kABytes + kBN * 128, a.w_scales + (static_cast<int64_t>(tile) * a.kt + j * kAtoms) * 512, sbytes,
+                  &full[stage]);
+      } else {
+        const int r0 = (j - a.ksteps) * 64;
+        mbar_arrive_expect_tx(&full[stage], kABytes + kBN * 128);
+        if (a.lora_mn) {
+          tma_load_2d(sA, &lwmap, tile * 128, r0, &full[stage]);
+          tma_load_2d(sA + 8192, &lwmap, tile * 128 + 64, r0, &full[stage]);
+        } else {
+          tma_load_2d(sA, &lwmap, r0, tile * 128, &full[stage]);
+        }
+      }
+    };
+    auto load_x = [&](int stage, int j) {
+      uint8_t* sB = smem_gen + stage * kStageBytes + kABytes;
+      if (j < a.ksteps) {
+        const uint32_t sbytes = static_cast<uint32_t>(min(kAtoms, static_cast<int>(a.kt) - j * kAtoms) * 512);
+        tma_load_2d(sB, &xmap, j * 128, 0, &full[stage]);
+        bulk_load(sB + kBN * 128 + kAtoms * 512, a.x_scales + static_cast<int64_t>(j) * (kAtoms * 512), sbytes, &full[stage]);
+      } else {
+        tma_load_2d(sB, &lxmap, (j - a.ksteps) * 64, 0, &full[stage]);
+      }
+    };
+    const int early = min(kStages, nsteps);
+    int tile = tile0, j = step0;
+    for (int i = 0; i < early; ++i) {
+      if (elect_one()) load_w(i, tile, j);
+      __syncwarp();
+      if (++j == per_tile) { j = 0; ++tile; }
+    }
+    // the activations come from the kernel before this one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int jx = step0;
+    for (int i = 0; i < early; ++i) {
+      if (elect_one()) load_x(i, jx);
+      __syncwarp();
+      if (++jx == per_tile) jx = 0;
+    }
+    uint32_t stage = early == kStages ? 0 : early, phase = early == kStages ? 1 : 0;
+    for (int i = early; i < nsteps; ++i) {
+      if (!mbar_wait_warp(&empty[stage], phase ^ 1u, a.err)) break;
+      if (elect_one()) {
+        load_w(static_cast<int>(stage), tile, j);
+        load_x(static_cast<int>(stage), j);
+      }
+      __syncwarp();
+      if (++j == per_tile) { j = 0; ++tile; }
+      if (++stage == kStages) { stage = 0; phase ^= 1u; }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer
+    uint32_t stage = 0, phase = 0, seg = 0;
+    const uint32_t lora_idesc = idesc_bf16(128, kBN, a.lora_mn != 0, false);
+    const uint64_t desc0 = smem_desc_sw128(smem0, 16, 1024);         // + (byte offset >> 4)
+    const uint64_t sdesc0 = smem_desc_scales(smem0);
+    int j = step0;
+    bool fresh = true;
+    for (int i = 0; i < nsteps; ++i) {
+      const uint32_t ab = seg & 1u;
+      if (fresh && !mbar_wait_warp(&acc_empty[ab], ((seg >> 1) & 1u) ^ 1u, a.err)) break;
+      if (!mbar_wait_warp(&full[stage], phase, a.err)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + ab * kBN;
+      const uint32_t off = stage * (kStageBytes >> 4);
+      const uint64_t ad = desc0 + off, bd = ad + (kABytes >> 4);
+      const bool last = j == per_tile - 1 || i == nsteps - 1;        // of this run's part of the tile
+      if (elect_one()) {
+        if (j < a.ksteps) {
+          const uint64_t sa = sdesc0 + off + ((kABytes + kBN * 128) >> 4), sb = sa + (kAtoms * 512 >> 4);
+          const int atoms = min(kAtoms, static_cast<int>(a.kt) - j * kAtoms);
+#pragma unroll
+          for (int t = 0; t < kAtoms; ++t)
+            if (t < atoms) {
+              tmem_cp_scales(tmem + kSfa + 4 * t, sa + t * 32);
+              tmem_cp_scales(tmem + kSfb + 4 * t, sb + t * 32);
+            }
+          const int slices = static_cast<int>(min(static_cast<int64_t>(4), (a.k - static_cast<int64_t>(j) * 256 + 63) / 64));
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (q < slices) {
+              const uint32_t acc = !fresh || q != 0 ? 1u : 0u;
+              if (kFmt == kMxFp4)
+                mma_mxf4_ss(d, ad + q * 2, bd + q * 2, idesc_mxf4(128, kBN, true, 2u * (q & 1)), tmem + kSfa + 4 * (q >> 1),
+                            tmem + kSfb + 4 * (q >> 1), acc);
+              else
+                mma_nvf4_ss(d, ad + q * 2, bd + q * 2, idesc_mxf4(128, kBN, false, 0), tmem + kSfa + 4 * q,
+                            tmem + kSfb + 4 * q, acc);
+            }
+        } else {
+          // A K = 16 slice: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
+          const uint64_t la = a.lora_mn ? smem_desc_sw128(smem0, 8192, 1024) + off : ad;
+          const uint32_t step = a.lora_mn ? 2048 >> 4 : 32 >> 4;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mma_bf16_ss(d, la + q * step, bd + q * 2, lora_idesc, !fresh || q != 0 ? 1u : 0u);
+        }
+        mma_commit(&empty[stage]);
+        if (last) mma_commit(&acc_full[ab]);
+      }
+      __syncwarp();
+      fresh = last;
+      if (last) ++seg;
+      if (++j == per_tile) j = 0;
+      if (++stage == kStages) { stage = 0; phase ^= 1u; }
+    }
+  } else {
+    // ------------------------------------------------ epilogue
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // x_global and the zeroed counters
+    const int quarter = warp & 3, rl = quarter * 32 + lane, et = (warp - 2) * 32 + lane;
+    uint32_t ephase = 0;
+    auto epi_sync = [&]() -> bool {
+      mbar_arrive(epi_bar);
+      const bool ok = mbar_wait(epi_bar, ephase, a.err);
+      ephase ^= 1u;
+      return ok;
+    };
+    const int m = static_cast<int>(a.m);
+    constexpr int kChunk = kBN < 32 ? kBN : 32;
+    const int64_t slot_floats = static_cast<int64_t>(m) * 128;
+    int tile = tile0, j = step0, left = nsteps;
+    for (uint32_t seg = 0; left > 0; ++seg, ++tile, j = 0) {
+      const int steps = min(per_tile - j, left);
+      left -= steps;
+      const uint32_t ab = seg & 1u;
+      if (!mbar_wait(&acc_full[ab], (seg >> 1) & 1u, a.err)) break;
+      tc_fence_after();
+      const int64_t row = static_cast<int64_t>(tile) * 128 + rl;
+      const bool row_ok = row < a.rows;
+      float gw = 1.0f;
+      if (kFmt == kNvFp4 && row_ok) gw = __ldg(a.w_global + (a.w_per_row ? row : 0));
+      auto store = [&](int t, float v) {
+        if (!row_ok) return;
+        if (kFmt == kNvFp4) v = __fmul_rn(v, __fmul_rn(__ldg(a.x_global + t), gw));
+        const __nv_bfloat16 b = __float2bfloat16_rn(v);
+        a.out[t * a.rows + row] = *reinterpret_cast<const uint16_t*>(&b);
+      };
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ab * kBN;
+      const bool whole = steps == per_tile;
+      float* mine = a.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (tile == tile0 ? 0 : 1)) * slot_floats + rl;
+#pragma unroll 1
+      for (int cc = 0; cc * kChunk < m; ++cc) {
+        uint32_t v[kChunk];
+        if constexpr (kChunk == 32) tmem_ld32(taddr + cc * 32, v);
+        else tmem_ld16(taddr, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < kChunk; ++c) {
+          const int t = cc * kChunk + c;
+          if (t < m) {
+            if (whole) store(t, __uint_as_float(v[c]));
+            else mine[t * 128] = __uint_as_float(v[c]);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&acc_empty[ab]);
+      if (whole) continue;
+      // the runs that share the tile: c0 .. c1
+      const int64_t s0 = static_cast<int64_t>(tile) * per_tile, s1 = s0 + per_tile - 1;
+      const int64_t c0 = ((s0 + 1) * gridDim.x - 1) / total, c1 = ((s1 + 1) * gridDim.x - 1) / total;
+      __threadfence();
+      if (!epi_sync()) break;
+      if (et == 0) *last_flag = atomicAdd(a.counters + tile, 1u) == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
+      if (!epi_sync()) break;
+      if (*last_flag == 0u) continue;
+      __threadfence();
+#pragma unroll 1
+      for (int t0 = 0; t0 < m; t0 += 16) {
+        float sum[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
+        for (int64_t c = c0; c <= c1; ++c) {
+          // the tile is run c's last one, or (it began before c0 + 1's) its first
+          const int which = c == c0 && total * c / gridDim.x < s0 ? 1 : 0;
+          const float* part = a.slots + (c * 2 + which) * slot_floats + t0 * 128 + rl;
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = t0 + i < m ? __ldcg(part + i * 128) : 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[i] += v[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (t0 + i < m) store(t0 + i, sum[i]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+template <int kFmt, int kBN>
+cudaError_t launch_t(const MxGemmArgs& a, const MxMaps& m, int num_sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_done{0};
+  constexpr size_t smem = stream_smem(kFmt, kBN);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(k_mx_stream<kFmt, kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int64_t steps = static_cast<int64_t>(a.m_tiles) * (a.ksteps + a.lora_steps);
+  int grid = num_sms < kMxMaxRuns ? num_sms : kMxMaxRuns;
+  if (steps < grid) grid = static_cast<int>(steps);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_mx_stream<kFmt, kBN>, a, m.w, m.x, m.lora_w, m.lora_x);
+}
+
+template <int kFmt>
+cudaError_t launch_f(int token_tile, const MxGemmArgs& a, const MxMaps& m, int num_sms, cudaStream_t stream) {
+  switch (token_tile) {
+    case 16: return launch_t<kFmt, 16>(a, m, num_sms, stream);
+    case 32: return launch_t<kFmt, 32>(a, m, num_sms, stream);
+    default: return launch_t<kFmt, 64>(a, m, num_sms, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_mx_stream(int fmt, int token_tile, const MxGemmArgs& a, const MxMaps& m, int num_sms,
+                             cudaStream_t stream) {
+  return fmt == kMxFp4 ? launch_f<kMxFp4>(token_tile, a, m, num_sms, stream)
+                       : launch_f<kNvFp4>(token_tile, a, m, num_sms, stream);
+}
+
+}  // namespace qlora

@@ -1,0 +1,106 @@
+// mx_xa.cu -- X A^T of the LoRA branch for few tokens (sm_100a).
+//
+// XA [m, r] = X [m, k] A^T, A [r, k]: 2 r k bytes of A and 2 m k of X for 2 m r k
+// operations, so it is all latency and spread.  A cluster of eight CTAs takes 16
+// ranks x 16 tokens, an eighth of k each; every warp multiplies its share with
+// m16n8k16 (bf16 in, fp32 sums), the warps of a CTA meet in shared memory and the
+// CTAs in the first one's, both summed in a fixed order.  It runs beside the
+// quantisation of X (whose row scales it needs only at its end).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "mx.h"
+#include "mx_ptx.cuh"
+
+namespace qlora {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32, kCluster = 8;
+
+// D[16 ranks][8 tokens] += A[16][16] B[8][16]^T
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) k_mx_xa(const MxXaArgs a) {
+  __shared__ float part[kWarps][16][17];       // per warp, then (CTA 0) per CTA of the cluster
+  __shared__ float joined[kCluster][16][17];
+  asm volatile("griddepcontrol.launch_dependents;");
+  cluster_sync();                              // the first CTA runs before the others write to it
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const uint32_t rank = cluster_rank();
+  const int r0 = static_cast<int>(blockIdx.x) / kCluster * 16, m0 = static_cast<int>(blockIdx.y) * 16;
+
+  // 64 columns a step; a lane's 16 bytes of a row are columns 8t .. 8t+7 of each
+  // 32: the same order in both operands, so any order will do for the sum.
+  const int steps = static_cast<int>(a.k / 64), lanes = kCluster * kWarps;
+  float d[2][4] = {};
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const bool ra = r0 + g < a.r, rb = r0 + g + 8 < a.r, ta = m0 + g < a.m, tb = m0 + g + 8 < a.m;
+  const uint4* pa = reinterpret_cast<const uint4*>(a.a + (r0 + g) * a.k) + t;
+  const uint4* pb = reinterpret_cast<const uint4*>(a.a + (r0 + g + 8) * a.k) + t;
+  const uint4* xa = reinterpret_cast<const uint4*>(a.x + (m0 + g) * a.k) + t;
+  const uint4* xb = reinterpret_cast<const uint4*>(a.x + (m0 + g + 8) * a.k) + t;
+#pragma unroll 2
+  for (int s = static_cast<int>(rank) * kWarps + warp; s < steps; s += lanes) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int o = s * 8 + h * 4;
+      const uint4 wa = ra ? __ldg(pa + o) : zero, wb = rb ? __ldg(pb + o) : zero;
+      const uint4 va = ta ? __ldg(xa + o) : zero, vb = tb ? __ldg(xb + o) : zero;
+      // columns 8t .. 8t+7 of a row feed two products of 16
+      const uint32_t a0[4] = {wa.x, wb.x, wa.y, wb.y}, a1[4] = {wa.z, wb.z, wa.w, wb.w};
+      const uint32_t p0[2] = {va.x, va.y}, p1[2] = {va.z, va.w}, q0[2] = {vb.x, vb.y}, q1[2] = {vb.z, vb.w};
+      mma_16x8x16(d[0], a0, p0);
+      mma_16x8x16(d[0], a1, p1);
+      mma_16x8x16(d[1], a0, q0);
+      mma_16x8x16(d[1], a1, q1);
+    }
+  }
+  // d[n][i]: rank g (+8 for i >= 2), token 8n + 2t + (i & 1)
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) part[warp][g + 8 * (i >> 1)][8 * n + 2 * t + (i & 1)] = d[n][i];
+  __syncthreads();
+  const int rr = threadIdx.x >> 4, tt = threadIdx.x & 15;
+  float v = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) v += part[w][rr][tt];
+  st_cluster_f32(cluster_map(smem_u32(&joined[rank][rr][tt]), 0), v);
+  cluster_sync();
+  if (rank != 0) return;
+  v = 0.0f;
+#pragma unroll
+  for (int c = 0; c < kCluster; ++c) v += joined[c][rr][tt];
+  asm volatile("griddepcontrol.wait;" ::: "memory");         // row_div; and the buffers' readers of the call before
+  const int rank_row = r0 + rr, tok = m0 + tt;
+  if (tok >= a.m) return;
+  if (a.xa && rank_row < a.r) a.xa[static_cast<int64_t>(tok) * a.r + rank_row] = v;
+  if (rank_row < a.rpad) {
+    const float s = a.row_div ? a.s / (a.row_div[tok] * a.all_div[0]) : a.s;
+    const __nv_bfloat16 b = __float2bfloat16_rn(__fmul_rn(s, v));
+    a.sxa[static_cast<int64_t>(tok) * a.rpad + rank_row] = *reinterpret_cast<const uint16_t*>(&b);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_mx_xa(const MxXaArgs& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rpad / 16 * kCluster), static_cast<unsigned>((a.m + 15) / 16));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_mx_xa, a);
+}
+
+}  // namespace qlora
