@@ -68,7 +68,7 @@ struct MxGemmArgs {
   int m_tiles, t_tiles;      // tiles of rows (128, of a pair 256) and of tokens
   // pairs: row tiles swept across all token tiles before the next group
   int m_group;
-  // streams: partial tiles [runs][2][m][128] and the row tiles' counters (zero)
+  // streams: partial tiles [runs][2][m][128] and a counter (zero) per 32 rows
   float* slots;
   uint32_t* counters;
   uint32_t* err;

@@ -57,7 +57,7 @@ ActLayout act_layout(int format, int64_t m, int64_t k, size_t base) {
 constexpr int64_t kMxStreamTokens = 64;
 
 // What one product needs beside its operands: a streamed one's counters (one per
-// 128 weight rows) and partial tiles.
+// 32 weight rows) and partial tiles.
 struct ProductLayout {
   ActLayout act;
   size_t counters, slots, end;
@@ -69,7 +69,7 @@ ProductLayout product_layout(int format, int64_t rows, int64_t k, int64_t m, siz
   l.counters = o;
   l.slots = o;
   if (m <= kMxStreamTokens) {
-    o = round_up(o + static_cast<size_t>((rows + 127) / 128) * 4, 256);
+    o = round_up(o + static_cast<size_t>((rows + 127) / 128) * 16, 256);
     l.slots = o;
     o += size_t{kMxMaxRuns} * 2 * m * 128 * sizeof(float);
   }
@@ -135,7 +135,7 @@ cudaError_t quantize_acts(const qlora_mx_tensor* W, const uint16_t* X, int64_t M
   a.per_row = W->format == QLORA_NVFP4;
   if (M <= kMxStreamTokens) {
     a.zero = reinterpret_cast<uint32_t*>(ws + P.counters);
-    a.zero_n = static_cast<int>((W->rows + 127) / 128);
+    a.zero_n = static_cast<int>((W->rows + 127) / 128 * 4);
   }
   return counted(launch_mx_quant(W->format, false, a, d.num_sms, cs));
 }

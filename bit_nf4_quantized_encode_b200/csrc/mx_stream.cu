@@ -47,6 +47,36 @@ __host__ __device__ constexpr uint32_t stream_cols(int fmt, int bn) {
   return c;
 }
 
+// Sums n partial columns sets (the first at `part`, the second `skip` floats on,
+// then `next` apart), kT tokens and kC parts at a time, in order, and hands on
+// each token's sum.
+template <int kT, int kC, typename F>
+__device__ __forceinline__ void join(const float* part, int64_t skip, int64_t next, int n, int m, const F& store) {
+  const float* rest = part + skip - next;              // part c >= 1 is at rest + c * next
+#pragma unroll 1
+  for (int t0 = 0; t0 < m; t0 += kT) {
+    float sum[kT];
+#pragma unroll
+    for (int i = 0; i < kT; ++i) sum[i] = 0.0f;
+#pragma unroll 1
+    for (int c0 = 0; c0 < n; c0 += kC) {
+      float v[kC][kT];
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+#pragma unroll
+        for (int i = 0; i < kT; ++i)
+          v[c][i] = c0 + c < n && t0 + i < m ? __ldcg((c0 + c == 0 ? part : rest + (c0 + c) * next) + (t0 + i) * 128) : 0.0f;
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+#pragma unroll
+        for (int i = 0; i < kT; ++i) sum[i] += v[c][i];
+    }
+#pragma unroll
+    for (int i = 0; i < kT; ++i)
+      if (t0 + i < m) store(t0 + i, sum[i]);
+  }
+}
+
 template <int kFmt, int kBN>
 __global__ void __launch_bounds__(kThreads, 1)
 k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
@@ -64,9 +94,7 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;      // [2]
   uint64_t* acc_empty = acc_full + 2;        // [2]
-  uint64_t* epi_bar = acc_empty + 2;         // the 128 epilogue threads meet here (bounded waits)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
-  uint32_t* last_flag = tmem_slot + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -85,7 +113,6 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 128);
     }
-    mbar_init(epi_bar, 128);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -149,16 +176,25 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
       __syncwarp();
       if (++jx == per_tile) jx = 0;
     }
+    // two stages at a time, so that a weight row is asked for 256 bytes in a row
     uint32_t stage = early == kStages ? 0 : early, phase = early == kStages ? 1 : 0;
-    for (int i = early; i < nsteps; ++i) {
+    for (int i = early; i < nsteps; i += 2) {
+      const bool two = i + 1 < nsteps;
+      const uint32_t stage2 = stage + 1 == kStages ? 0 : stage + 1, phase2 = stage2 == 0 ? phase ^ 1u : phase;
       if (!mbar_wait_warp(&empty[stage], phase ^ 1u, a.err)) break;
+      if (two && !mbar_wait_warp(&empty[stage2], phase2 ^ 1u, a.err)) break;
+      const int j2 = j + 1 == per_tile ? 0 : j + 1, tile2 = j2 == 0 ? tile + 1 : tile;
       if (elect_one()) {
         load_w(static_cast<int>(stage), tile, j);
+        if (two) load_w(static_cast<int>(stage2), tile2, j2);
         load_x(static_cast<int>(stage), j);
+        if (two) load_x(static_cast<int>(stage2), j2);
       }
       __syncwarp();
-      if (++j == per_tile) { j = 0; ++tile; }
-      if (++stage == kStages) { stage = 0; phase ^= 1u; }
+      j = j2 + 1 == per_tile ? 0 : j2 + 1;
+      tile = j == 0 ? tile2 + 1 : tile2;
+      stage = stage2 + 1 == kStages ? 0 : stage2 + 1;
+      phase = stage == 0 ? phase2 ^ 1u : phase2;
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
@@ -218,14 +254,7 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
   } else {
     // ------------------------------------------------ epilogue
     asm volatile("griddepcontrol.wait;" ::: "memory");      // x_global and the zeroed counters
-    const int quarter = warp & 3, rl = quarter * 32 + lane, et = (warp - 2) * 32 + lane;
-    uint32_t ephase = 0;
-    auto epi_sync = [&]() -> bool {
-      mbar_arrive(epi_bar);
-      const bool ok = mbar_wait(epi_bar, ephase, a.err);
-      ephase ^= 1u;
-      return ok;
-    };
+    const int quarter = warp & 3, rl = quarter * 32 + lane;
     const int m = static_cast<int>(a.m);
     constexpr int kChunk = kBN < 32 ? kBN : 32;
     const int64_t slot_floats = static_cast<int64_t>(m) * 128;
@@ -267,33 +296,28 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
       tc_fence_before();
       mbar_arrive(&acc_empty[ab]);
       if (whole) continue;
-      // the runs that share the tile: c0 .. c1
+      // the runs that share the tile: c0 .. c1.  Each warp counts its own 32 rows,
+      // so no warp waits for another.
       const int64_t s0 = static_cast<int64_t>(tile) * per_tile, s1 = s0 + per_tile - 1;
-      const int64_t c0 = ((s0 + 1) * gridDim.x - 1) / total, c1 = ((s1 + 1) * gridDim.x - 1) / total;
+      const int c0 = static_cast<int>(((s0 + 1) * gridDim.x - 1) / total);
+      const int n = static_cast<int>(((s1 + 1) * gridDim.x - 1) / total) - c0 + 1;
       __threadfence();
-      if (!epi_sync()) break;
-      if (et == 0) *last_flag = atomicAdd(a.counters + tile, 1u) == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
-      if (!epi_sync()) break;
-      if (*last_flag == 0u) continue;
+      __syncwarp();
+      uint32_t before = 0;
+      if (lane == 0) before = atomicAdd(a.counters + tile * 4 + quarter, 1u);
+      if (__shfl_sync(0xFFFFFFFFu, before, 0) != static_cast<uint32_t>(n - 1)) continue;
       __threadfence();
-#pragma unroll 1
-      for (int t0 = 0; t0 < m; t0 += 16) {
-        float sum[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] = 0.0f;
-        for (int64_t c = c0; c <= c1; ++c) {
-          // the tile is run c's last one, or (it began before c0 + 1's) its first
-          const int which = c == c0 && total * c / gridDim.x < s0 ? 1 : 0;
-          const float* part = a.slots + (c * 2 + which) * slot_floats + t0 * 128 + rl;
-          float v[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = t0 + i < m ? __ldcg(part + i * 128) : 0.0f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sum[i] += v[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (t0 + i < m) store(t0 + i, sum[i]);
+      // run c0 may have begun in an earlier tile: this one is its last then
+      const int which0 = total * c0 / gridDim.x < s0 ? 1 : 0;
+      const float* part = a.slots + (static_cast<int64_t>(c0) * 2 + which0) * slot_floats + rl;
+      const int64_t skip = (2 - which0) * slot_floats, next = 2 * slot_floats;
+      // several parts are read at once, and added in the order of the runs
+      if (m <= 2) {
+        join<2, 16>(part, skip, next, n, m, store);
+      } else if (m <= 8) {
+        join<8, 4>(part, skip, next, n, m, store);
+      } else {
+        join<16, 2>(part, skip, next, n, m, store);
       }
     }
   }
@@ -322,7 +346,8 @@ cudaError_t launch_t(const MxGemmArgs& a, const MxMaps& m, int num_sms, cudaStre
   }
   const int64_t steps = static_cast<int64_t>(a.m_tiles) * (a.ksteps + a.lora_steps);
   int grid = num_sms < kMxMaxRuns ? num_sms : kMxMaxRuns;
-  if (steps < grid) grid = static_cast<int>(steps);
+  // a run of fewer than two steps would save less than joining one more part costs
+  if ((steps + 1) / 2 < grid) grid = static_cast<int>((steps + 1) / 2);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
