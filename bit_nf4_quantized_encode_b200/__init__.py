@@ -23,6 +23,7 @@ Microscaled 4-bit formats (MXFP4, NVFP4):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -399,6 +400,7 @@ MX_FORMATS = {"mxfp4": 0, "nvfp4": 1}
 MX_BLOCK = {"mxfp4": 32, "nvfp4": 16}
 
 
+@functools.lru_cache(maxsize=4096)
 def _mx_bytes(rows: int, cols: int, fmt: str) -> tuple:
     """(codes, scales) bytes of a microscaled matrix, as qlora_mx_sizes."""
     return rows * ((cols + 31) // 32 * 16), (rows + 127) // 128 * (-(-cols // (4 * MX_BLOCK[fmt]))) * 512
@@ -429,22 +431,24 @@ class MXTensor:
 
     def c_struct(self) -> _MxTensorC:
         """The C descriptor, after checking that the buffers hold what it describes."""
-        c, s, g = self.codes, self.scales, self.global_scale
-        if self.fmt not in MX_FORMATS:
+        c, s, g, rows, fmt = self.codes, self.scales, self.global_scale, self.rows, self.fmt
+        if fmt not in MX_FORMATS:
             raise ValueError(f"fmt must be one of {sorted(MX_FORMATS)}")
-        need_c, need_s = _mx_bytes(self.rows, self.cols, self.fmt)
-        if not (c.dtype == s.dtype == torch.uint8 and c.is_contiguous() and s.is_contiguous() and c.is_cuda
-                and c.device == s.device):
+        need_c, need_s = _mx_bytes(rows, self.cols, fmt)
+        dev = c.device
+        if not (c.dtype is torch.uint8 and s.dtype is torch.uint8 and c.is_contiguous() and s.is_contiguous()
+                and c.is_cuda and dev == s.device):
             raise ValueError("codes and scales must be contiguous uint8 tensors on one CUDA device")
         if c.numel() < need_c or s.numel() < need_s:
-            raise ValueError(f"a {self.rows}x{self.cols} {self.fmt} tensor needs {need_c} bytes of codes and {need_s} of scales")
-        if (g is None) != (self.fmt == "mxfp4"):
+            raise ValueError(f"a {rows}x{self.cols} {fmt} tensor needs {need_c} bytes of codes and {need_s} of scales")
+        if (g is None) != (fmt == "mxfp4"):
             raise ValueError("global_scale belongs to nvfp4 and only to it")
-        if g is not None and not (g.dtype == torch.float32 and g.is_contiguous() and g.device == c.device
-                                  and g.numel() in (1, self.rows)):
+        if g is None:
+            return _MxTensorC(c.data_ptr(), s.data_ptr(), 0, rows, self.cols, 0, 0)
+        n = g.numel()
+        if not (g.dtype is torch.float32 and g.is_contiguous() and g.device == dev and (n == 1 or n == rows)):
             raise ValueError("global_scale must be a float32 tensor of 1 or `rows` elements on the codes' device")
-        return _MxTensorC(c.data_ptr(), s.data_ptr(), 0 if g is None else g.data_ptr(), self.rows, self.cols,
-                          MX_FORMATS[self.fmt], 1 if self.scale_per_row else 0)
+        return _MxTensorC(c.data_ptr(), s.data_ptr(), g.data_ptr(), rows, self.cols, 1, 1 if n != 1 else 0)
 
 
 def empty_mx(rows: int, cols: int, device, fmt: str = "mxfp4", per_row: bool = False) -> MXTensor:
@@ -462,11 +466,18 @@ def empty_mx(rows: int, cols: int, device, fmt: str = "mxfp4", per_row: bool = F
 def _on(device, where: str, fn, *args):
     """Call a C entry point with the tensors' device current and its current
     stream as the last argument."""
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), where)
+    i = device.index
+    if torch.cuda.current_device() == i:
+        status = fn(*args, _raw_stream(i))
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), where)
+        with torch.cuda.device(i):
+            status = fn(*args, _raw_stream(i))
+    if status != 0:
+        raise QloraError(status, where)
+
+
+# The current stream's handle of a device, without building a Stream object (2 us a call).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def qlora_mx_sizes(rows: int, cols: int, fmt: str = "mxfp4", per_row: bool = False) -> dict:
@@ -474,6 +485,10 @@ def qlora_mx_sizes(rows: int, cols: int, fmt: str = "mxfp4", per_row: bool = Fal
     v = [ctypes.c_size_t() for _ in range(4)]
     _check(_lib.qlora_mx_sizes(rows, cols, MX_FORMATS[fmt], int(per_row), *[ctypes.byref(x) for x in v]), "qlora_mx_sizes")
     return dict(codes=v[0].value, scales=v[1].value, global_scale=v[2].value, workspace=v[3].value)
+
+
+# Work-buffer bytes of an NVFP4 quantisation with one global scale, whatever the size.
+_MX_QUANT_WORKSPACE = qlora_mx_sizes(1, 1, "nvfp4")["workspace"]
 
 
 def qlora_mx_quantize(W: torch.Tensor, fmt: str = "mxfp4", transpose: bool = False, per_row: bool = False,
@@ -494,7 +509,7 @@ def qlora_mx_quantize(W: torch.Tensor, fmt: str = "mxfp4", transpose: bool = Fal
         return out
     c = out.c_struct()
     if workspace is None and out.fmt == "nvfp4" and not out.scale_per_row:
-        workspace = torch.empty(qlora_mx_sizes(rows, cols, "nvfp4")["workspace"], dtype=torch.uint8, device=W.device)
+        workspace = torch.empty(_MX_QUANT_WORKSPACE, dtype=torch.uint8, device=W.device)
     _on(W.device, "qlora_mx_quantize", _lib.qlora_mx_quantize, W.data_ptr(), int(transpose), c, _addr(workspace),
         _size(workspace))
     return out
@@ -523,6 +538,7 @@ def _size(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+@functools.lru_cache(maxsize=4096)
 def qlora_mx_linear_workspace_size(rows: int, cols: int, fmt: str, m: int, r: int = 0) -> tuple:
     """(forward, backward) work-buffer bytes of a layer W [rows, cols]; r = 0: no adapter."""
     f, b = ctypes.c_size_t(), ctypes.c_size_t()
@@ -619,6 +635,7 @@ def qlora_mx_linear_bwd(qT: MXTensor, dY: torch.Tensor, X: torch.Tensor | None =
     return dX, dA, dB
 
 
+@functools.lru_cache(maxsize=4096)
 def qlora_mx_moe_workspace_size(experts: int, hidden: int, inner: int, m: int, top_k: int) -> int:
     b = ctypes.c_size_t()
     _check(_lib.qlora_mx_moe_workspace_size(experts, hidden, inner, m, top_k, b), "qlora_mx_moe_workspace_size")

@@ -89,6 +89,29 @@ cudaError_t launch_mx_stream(int fmt, int token_tile, const MxGemmArgs& a, const
 cudaError_t launch_mx_pair(int fmt, int token_tile, const MxGemmArgs& a, const MxMaps& m, int num_sms,
                            cudaStream_t stream);
 
+// At most 16 tokens, quantised by the product itself (mx_few.cu).
+struct MxFewArgs {
+  const uint16_t* x;         // bf16 [m, k]
+  int vec;                   // k % 8 == 0: rows start on 16 bytes
+  const uint8_t* w_scales;
+  int64_t kt;
+  const float* w_global;     // NVFP4: [1] or [rows]
+  int w_per_row;
+  int64_t rows, k;
+  int m, ksteps, lora_steps;
+  uint16_t* out;             // bf16 [m, rows]
+  int chunks, units, stage_bytes, stages;   // set by the launch
+  uint32_t* err;
+};
+// Every CTA reads the tokens (2 bytes an element, from L2) and keeps them: limits
+// of their number and of their shared memory.
+constexpr int64_t kMxFewElements = 65536;
+constexpr size_t kMxFewShared = 132 * 1024;
+// Token tile (8 or 16), or 0 where the tokens are too many.
+int mx_few_tile(int fmt, int64_t m, int64_t k, int lora_steps);
+// Maps: w codes box {128, 32}; lora_w [rows, r] box {64, 32}; lora_x box {64, token_tile}.
+cudaError_t launch_mx_few(int fmt, int token_tile, const MxFewArgs& a, const MxMaps& m, int num_sms, cudaStream_t stream);
+
 // X A^T for at most 64 tokens (mx_xa.cu), as run_rank_xa gives it for more.
 struct MxXaArgs {
   const uint16_t* x;         // bf16 [m, k]
@@ -97,9 +120,11 @@ struct MxXaArgs {
   int m, r, rpad;
   float s;
   float* xa;                 // fp32 [m, r] or null
-  uint16_t* sxa;             // bf16 [m, rpad]: s X A^T [/ (row_div all_div)], zero from column r
-  const float* row_div;      // [m] or null
-  const float* all_div;
+  uint16_t* sxa;             // bf16 [m, rpad]: s X A^T [/ (g all_div)], zero from column r
+  const float* all_div;      // [1]: divide by it and the token's NVFP4 global scale g; or null
+  // the first kernel of its call starts when all before it has ended, a later one
+  // beside the one before
+  int first;
 };
 cudaError_t launch_mx_xa(const MxXaArgs& a, cudaStream_t stream);
 

@@ -212,6 +212,40 @@ qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const
   return counted(e) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
+// The same with the tokens' quantisation in the product (see mx_few.cu).
+qlora_status run_mx_few(const qlora_mx_tensor* W, const uint16_t* X, int64_t M, int tile, const uint16_t* lora_w,
+                        const uint16_t* lora_x, int r, int lora_steps, uint16_t* out, const DeviceInfo& d,
+                        cudaStream_t cs) {
+  MxFewArgs a{};
+  a.x = X;
+  a.vec = W->cols % 8 == 0;
+  a.w_scales = W->scales;
+  a.kt = mx_tiles_k(W->format, W->cols);
+  if (W->format == QLORA_NVFP4) {
+    a.w_global = W->global_scale;
+    a.w_per_row = W->scale_per_row;
+  }
+  a.rows = W->rows;
+  a.k = W->cols;
+  a.m = static_cast<int>(M);
+  a.ksteps = static_cast<int>((W->cols + 255) / 256);
+  a.lora_steps = lora_steps;
+  a.out = out;
+  a.err = d.err;
+  MxMaps m;
+  const uint64_t up = static_cast<uint64_t>(mx_pitch(W->cols)), n = static_cast<uint64_t>(W->rows);
+  if (!make_map_u8(&m.w, W->codes, up, n, up, 128, 32, CU_TENSOR_MAP_SWIZZLE_128B)) return QLORA_ERR_CUDA;
+  if (lora_steps) {
+    const uint64_t rpad = static_cast<uint64_t>(lora_steps) * 64;
+    if (!make_map(&m.lora_w, lora_w, r, n, static_cast<uint64_t>(r) * 2, 32) ||
+        !make_map(&m.lora_x, lora_x, rpad, static_cast<uint64_t>(M), rpad * 2, static_cast<uint32_t>(tile)))
+      return QLORA_ERR_CUDA;
+  } else {
+    m.lora_w = m.lora_x = m.w;
+  }
+  return counted(launch_mx_few(W->format, tile, a, m, d.num_sms, cs)) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
 // ------------------------------------------------------------------ mixture of experts
 struct MoeLayout {
   size_t x_codes, x_scales, h_codes, h_scales, part, list, n_used, counters, total;
@@ -342,16 +376,18 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, in
   if ((st = device_info(&d)) != QLORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (quantize_acts(W, X, M, ws, L.product, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
+  const int few = mx_few_tile(W->format, M, W->cols, r ? sh.lora_steps : 0);
+  if (!few && quantize_acts(W, X, M, ws, L.product, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
   const uint16_t* sxa = nullptr;
   if (r) {
-    RankDivide div;
-    if (W->format == QLORA_NVFP4) {
-      div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
-      div.all = W->global_scale;
-    }
     sxa = reinterpret_cast<const uint16_t*>(ws + L.xa.sxa);
+    const float* all_div = W->format == QLORA_NVFP4 ? W->global_scale : nullptr;
     if (M > kMxStreamTokens) {
+      RankDivide div;
+      if (all_div) {
+        div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
+        div.all = all_div;
+      }
       if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, div, d, cs)) != QLORA_OK) return st;
     } else {
       MxXaArgs xa{};
@@ -364,11 +400,12 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, in
       xa.s = s;
       xa.xa = XA_out;
       xa.sxa = reinterpret_cast<uint16_t*>(ws + L.xa.sxa);
-      xa.row_div = div.row;
-      xa.all_div = div.all;
+      xa.all_div = all_div;
+      xa.first = few != 0;
       if (counted(launch_mx_xa(xa, cs)) != cudaSuccess) return QLORA_ERR_CUDA;
     }
   }
+  if (few) return run_mx_few(W, X, M, few, B, sxa, r, r ? sh.lora_steps : 0, Y, d, cs);
   return run_mx_gemm(W, M, ws, L.product, B, false, sxa, r, r ? sh.lora_steps : 0, Y, d, cs);
 }
 

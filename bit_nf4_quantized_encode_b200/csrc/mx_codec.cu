@@ -22,6 +22,7 @@
 #include <cstdint>
 
 #include "mx.h"
+#include "mx_encode.cuh"
 #include "mx_format.cuh"
 #include "nf4_device.cuh"
 
@@ -30,148 +31,20 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Eight consecutive elements of a row, from column c (zero past cols).
-template <bool kVec>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t cols) {
-  if (c >= cols) return make_uint4(0, 0, 0, 0);
-  if constexpr (kVec) return __ldg(reinterpret_cast<const uint4*>(row + c));   // cols % 8 == 0
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < cols) w[i >> 1] |= static_cast<uint32_t>(__ldg(row + c + i)) << (16 * (i & 1));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Thirty-two consecutive elements: what one thread encodes, one MXFP4 block or
-// two NVFP4 blocks, so that no block is shared between threads.
-struct Elems32 {
-  uint4 q[4];
-};
-template <bool kVec>
-__device__ __forceinline__ Elems32 load32(const uint16_t* row, int64_t c, int64_t cols) {
-  Elems32 e;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) e.q[i] = load8<kVec>(row, c + 8 * i, cols);
-  return e;
-}
-
-// Per 16-bit half: the larger magnitude.
-__device__ __forceinline__ uint32_t mag_max2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
-__device__ __forceinline__ uint32_t mag16(const uint4& a, const uint4& b) {
-  uint32_t m = a.x & 0x7FFF7FFFu;
-  m = mag_max2(m, a.y); m = mag_max2(m, a.z); m = mag_max2(m, a.w);
-  m = mag_max2(m, b.x); m = mag_max2(m, b.y); m = mag_max2(m, b.z); m = mag_max2(m, b.w);
-  return m;
-}
-__device__ __forceinline__ uint32_t wider_half(uint32_t m) { return max(m & 0xFFFFu, m >> 16); }
-
-// Largest finite magnitude (bf16 bits) of what mag16 saw or, where that holds
-// values that are not finite, of the elements again without them.
-__device__ __forceinline__ uint32_t finite_mag(uint32_t m, const uint4& q) {
-  uint32_t top = wider_half(m);
-  if (top >= 0x7F80u) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    bool bad = false;
-    top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, max(mx_finite_mag(w[i], bad), mx_finite_mag(w[i] >> 16, bad)));
-  }
-  return top;
-}
-__device__ __forceinline__ uint32_t finite_mag8(const uint4& q) {
-  uint32_t m = q.x & 0x7FFF7FFFu;
-  m = mag_max2(m, q.y); m = mag_max2(m, q.z); m = mag_max2(m, q.w);
-  return finite_mag(m, q);
-}
-
-// Scale byte of a block with the largest magnitude `mag` (bf16 bits).
-template <int kFmt>
-__device__ __forceinline__ uint32_t scale_byte(uint32_t mag, float inv_g) {
-  if (kFmt == kMxFp4) return mag >= 0x7F80u ? 255u : mx_e8m0(mag << 16);
-  return mag >= 0x7F80u ? 0x7Fu : mx_e4m3(__fdiv_rn(__fmul_rn(__uint_as_float(mag << 16), inv_g), 6.0f));
-}
-
-// Multiplier (MXFP4), or scale and its reciprocal (NVFP4), of a block's elements.
-struct BlockScale {
-  float s, r;
-  bool zero;                 // every code is 0: NaN scale or (NVFP4) scale 0
-};
-template <int kFmt>
-__device__ __forceinline__ BlockScale block_scale(uint32_t sb) {
-  BlockScale b;
-  if (kFmt == kMxFp4) {
-    b.zero = sb == 255u;
-    b.s = b.r = mx_e8m0_inverse(b.zero ? 127u : sb);
-  } else {
-    b.zero = sb == 0x7Fu || sb == 0u;
-    b.s = e4m3_to_f32(b.zero ? 0x38u : sb);
-    b.r = __frcp_rn(b.s);
-  }
-  return b;
-}
-template <int kFmt>
-__device__ __forceinline__ uint32_t encode8(float (&v)[8], const BlockScale& b, float inv_g) {
-  const uint64_t s = f32x2(kFmt == kMxFp4 ? b.s : -b.s, kFmt == kMxFp4 ? b.s : -b.s), r = f32x2(b.r, b.r);
-  const uint64_t ig = f32x2(inv_g, inv_g);
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const uint64_t x = f32x2(v[i], v[i + 1]);
-    float lo, hi;
-    if (kFmt == kMxFp4) {
-      f32x2_split(f32x2_mul(x, s), lo, hi);
-      v[i] = lo;
-      v[i + 1] = hi;
-    } else {
-      f32x2_split(mx_quotient2(f32x2_mul(x, ig), s, r), lo, hi);
-      v[i] = copysignf(lo, v[i]);
-      v[i + 1] = copysignf(hi, v[i + 1]);
-    }
-  }
-  const uint32_t c = mx_codes8(v);
-  return b.zero ? 0u : c;
-}
-__device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-
 // A warp's 1024 consecutive elements (32 per lane, from column c): codes and
 // scales to memory.  The four bytes of a scale tile's row leave as one word.
 template <int kFmt>
 __device__ __forceinline__ void emit1024(const MxQuantArgs& a, int64_t row, int64_t c, const Elems32& e, float inv_g) {
   const int lane = threadIdx.x & 31;
-  uint4 out;
-  uint32_t* o = &out.x;
-  float v[8];
+  uint32_t scales;
+  const uint4 out = encode32<kFmt>(e, inv_g, scales);
   uint32_t word;
   if (kFmt == kMxFp4) {
-    const uint32_t sb = scale_byte<kFmt>(wider_half(__vmaxu2(mag16(e.q[0], e.q[1]), mag16(e.q[2], e.q[3]))), inv_g);
-    const BlockScale b = block_scale<kFmt>(sb);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      unpack8(e.q[i], v);
-      o[i] = encode8<kFmt>(v, b, inv_g);
-    }
-    word = sb << (8 * (lane & 3));
+    word = scales << (8 * (lane & 3));
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
   } else {
-    word = 0;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t sb = scale_byte<kFmt>(wider_half(mag16(e.q[2 * h], e.q[2 * h + 1])), inv_g);
-      const BlockScale b = block_scale<kFmt>(sb);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        unpack8(e.q[2 * h + i], v);
-        o[2 * h + i] = encode8<kFmt>(v, b, inv_g);
-      }
-      word |= sb << (16 * (lane & 1) + 8 * h);
-    }
+    word = scales << (16 * (lane & 1));
     word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
   }
   if (row < a.rows && c < a.pitch * 2) *reinterpret_cast<uint4*>(a.codes + row * a.pitch + (c >> 1)) = out;

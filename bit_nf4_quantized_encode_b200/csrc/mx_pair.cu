@@ -71,7 +71,7 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
   uint64_t* acc_free = acc_full + 1;         // the leader's: one arrival per epilogue warp of the pair
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_free + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = warp_index();
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int ntiles = a.m_tiles * a.t_tiles;

@@ -5,13 +5,14 @@
 // ranks x 16 tokens, an eighth of k each; every warp multiplies its share with
 // m16n8k16 (bf16 in, fp32 sums), the warps of a CTA meet in shared memory and the
 // CTAs in the first one's, both summed in a fixed order.  It runs beside the
-// quantisation of X (whose row scales it needs only at its end).
+// quantisation of X, and finds NVFP4's global scale of a token by itself.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "mx.h"
+#include "mx_encode.cuh"
 #include "mx_ptx.cuh"
 
 namespace qlora {
@@ -29,7 +30,10 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4
 __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) k_mx_xa(const MxXaArgs a) {
   __shared__ float part[kWarps][16][17];       // per warp, then (CTA 0) per CTA of the cluster
   __shared__ float joined[kCluster][16][17];
+  __shared__ uint32_t s_amax[16];              // the first CTA's: largest finite magnitude of each token
   asm volatile("griddepcontrol.launch_dependents;");
+  if (threadIdx.x < 16) s_amax[threadIdx.x] = 0u;
+  __syncthreads();
   cluster_sync();                              // the first CTA runs before the others write to it
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t rank = cluster_rank();
@@ -40,6 +44,7 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) k_m
   const int steps = static_cast<int>(a.k / 64), lanes = kCluster * kWarps;
   float d[2][4] = {};
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  uint32_t mag_a = 0, mag_b = 0;               // of tokens g and g + 8
   const bool ra = r0 + g < a.r, rb = r0 + g + 8 < a.r, ta = m0 + g < a.m, tb = m0 + g + 8 < a.m;
   const uint4* pa = reinterpret_cast<const uint4*>(a.a + (r0 + g) * a.k) + t;
   const uint4* pb = reinterpret_cast<const uint4*>(a.a + (r0 + g + 8) * a.k) + t;
@@ -52,6 +57,10 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) k_m
       const int o = s * 8 + h * 4;
       const uint4 wa = ra ? __ldg(pa + o) : zero, wb = rb ? __ldg(pb + o) : zero;
       const uint4 va = ta ? __ldg(xa + o) : zero, vb = tb ? __ldg(xb + o) : zero;
+      if (a.all_div) {
+        mag_a = max(mag_a, finite_mag8(va));
+        mag_b = max(mag_b, finite_mag8(vb));
+      }
       // columns 8t .. 8t+7 of a row feed two products of 16
       const uint32_t a0[4] = {wa.x, wb.x, wa.y, wb.y}, a1[4] = {wa.z, wb.z, wa.w, wb.w};
       const uint32_t p0[2] = {va.x, va.y}, p1[2] = {va.z, va.w}, q0[2] = {vb.x, vb.y}, q1[2] = {vb.z, vb.w};
@@ -66,6 +75,17 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) k_m
   for (int n = 0; n < 2; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) part[warp][g + 8 * (i >> 1)][8 * n + 2 * t + (i & 1)] = d[n][i];
+  if (a.all_div) {
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      mag_a = max(mag_a, __shfl_xor_sync(0xFFFFFFFFu, mag_a, o));
+      mag_b = max(mag_b, __shfl_xor_sync(0xFFFFFFFFu, mag_b, o));
+    }
+    if (t == 0) {
+      atomic_max_cluster(cluster_map(smem_u32(&s_amax[g]), 0), mag_a);
+      atomic_max_cluster(cluster_map(smem_u32(&s_amax[g + 8]), 0), mag_b);
+    }
+  }
   __syncthreads();
   const int rr = threadIdx.x >> 4, tt = threadIdx.x & 15;
   float v = 0.0f;
@@ -77,12 +97,12 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) k_m
   v = 0.0f;
 #pragma unroll
   for (int c = 0; c < kCluster; ++c) v += joined[c][rr][tt];
-  asm volatile("griddepcontrol.wait;" ::: "memory");         // row_div; and the buffers' readers of the call before
+  asm volatile("griddepcontrol.wait;" ::: "memory");         // a reader of this kernel's end may rely on the one before
   const int rank_row = r0 + rr, tok = m0 + tt;
   if (tok >= a.m) return;
   if (a.xa && rank_row < a.r) a.xa[static_cast<int64_t>(tok) * a.r + rank_row] = v;
   if (rank_row < a.rpad) {
-    const float s = a.row_div ? a.s / (a.row_div[tok] * a.all_div[0]) : a.s;
+    const float s = a.all_div ? a.s / (mx_global_scale(s_amax[tt] << 16) * a.all_div[0]) : a.s;
     const __nv_bfloat16 b = __float2bfloat16_rn(__fmul_rn(s, v));
     a.sxa[static_cast<int64_t>(tok) * a.rpad + rank_row] = *reinterpret_cast<const uint16_t*>(&b);
   }
@@ -99,7 +119,7 @@ cudaError_t launch_mx_xa(const MxXaArgs& a, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = a.first ? 0 : 1;
   return cudaLaunchKernelEx(&cfg, k_mx_xa, a);
 }
 

@@ -170,7 +170,8 @@ def lora_terms(x, a, b, s):
 LAYERS = [(1, 1, 1), (8, 64, 1), (128, 256, 1), (64, 64, 16), (300, 520, 17), (392, 640, 33), (256, 4096, 65),
           (130, 130, 129), (2048, 8192, 3), (1001, 1999, 77), (512, 1024, 300), (136, 90, 257), (4096, 96, 5),
           (129, 7000, 64), (300, 72, 129), (1030, 2100, 520), (520, 4096, 1030), (20000, 300, 2),
-          (300, 20000, 9), (5000, 3000, 40)]
+          (300, 20000, 9), (5000, 3000, 40), (45000, 96, 3), (70000, 40, 1), (1000, 9000, 7),
+          (9472, 512, 12)]
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
@@ -185,7 +186,7 @@ def test_linear_fwd(qb, rows, cols, m, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
-@pytest.mark.parametrize("rows,cols,m,r", [(8, 64, 1, 8), (256, 256, 16, 8), (392, 640, 33, 64), (3000, 8192, 5, 64), (1000, 4096, 129, 136), (4096, 256, 64, 136),
+@pytest.mark.parametrize("rows,cols,m,r", [(8, 64, 1, 8), (256, 256, 16, 8), (392, 640, 33, 64), (3000, 8192, 5, 64), (3000, 8192, 16, 64), (5000, 2048, 16, 256), (1000, 4096, 129, 136), (4096, 256, 64, 136),
                                            (2048, 704, 300, 256)])
 def test_linear_fwd_with_an_adapter(qb, rows, cols, m, r, fmt):
     w, x = f64(normal((rows, cols), 0.02, 1)), normal((m, cols), 1.0, 2)
