@@ -22,6 +22,7 @@
 #include <cstdint>
 
 #include "mx.h"
+#include "mx_encode.cuh"
 #include "mx_format.cuh"
 #include "mx_ptx.cuh"
 #include "nf4_device.cuh"
@@ -30,20 +31,14 @@ namespace qlora {
 namespace {
 
 // ------------------------------------------------------------------ routing
-// One cluster of CTAs: each takes a part of the experts' logits and of the
-// tokens' quantisation; the logits meet in the first CTA's shared memory.
+// One cluster of eight CTAs.  The logits are an [experts, 16] product over hidden:
+// a CTA takes an eighth of hidden, its warps groups of 16 experts (several warps a
+// group where there are few), with m16n8k16 (bf16 in, fp32 sums).  The parts of
+// an expert meet in the CTA that owns it (expert mod 8), summed in a fixed order,
+// and the logits in the first CTA, which chooses.  Latency is all there is: every
+// load of a warp is issued at once.
 constexpr int kRouteCtas = 8;
-constexpr int kRouteThreads = 512;
-
-__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
-  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    acc = __fmaf_rn(bf16_lo(x[i]), bf16_lo(y[i]), acc);
-    acc = __fmaf_rn(bf16_hi(x[i]), bf16_hi(y[i]), acc);
-  }
-  return acc;
-}
+constexpr int kRouteThreads = 512, kRouteWarps = kRouteThreads / 32;
 
 // Order-preserving key of a logit, above 0 (0 marks a taken one); NaN lowest.
 __device__ __forceinline__ uint32_t logit_key(float v) {
@@ -52,91 +47,126 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
   return (b >> 31) ? ~b : (b | 0x80000000u);
 }
 
+// Shared memory: the logits [16][experts] (the first CTA's), the owner's parts
+// [8][ceil(experts / 8)][16] and the warps' tiles [16][16][16].
+__host__ __device__ constexpr size_t route_smem(int experts) {
+  return sizeof(float) * (static_cast<size_t>(16) * experts + static_cast<size_t>(128) * ((experts + 7) / 8) + 16 * 256);
+}
+
 __global__ void __launch_bounds__(kRouteThreads) __cluster_dims__(kRouteCtas, 1, 1)
 k_moe_route(const MxMoeArgs a) {
-  extern __shared__ float s_logit[];                             // [m][experts], the first CTA's is used
+  extern __shared__ float smem[];
   __shared__ int s_id[16][16];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  __shared__ uint32_t s_used[kMoeMaxExperts / 32];
+  const int per_owner = (a.experts + 7) / 8;
+  float* s_logit = smem;
+  float* s_in = s_logit + 16 * a.experts;
+  float* s_tile = s_in + 128 * per_owner;
+  const int warp = warp_index(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rank = static_cast<int>(cluster_rank());
   asm volatile("griddepcontrol.launch_dependents;");
-  cluster_sync();                          // the first CTA runs before the others write to it
 
-  // logits: one warp per expert, the router's row once for all tokens
-  const int nvec = static_cast<int>(a.hidden / 8);
-  for (int e = static_cast<int>(rank) * (kRouteThreads / 32) + warp; e < a.experts; e += kRouteCtas * (kRouteThreads / 32)) {
-    const uint4* rr = reinterpret_cast<const uint4*>(a.router + static_cast<int64_t>(e) * a.hidden);
-    float acc[16];
-#pragma unroll
-    for (int t = 0; t < 16; ++t) acc[t] = 0.0f;
-    for (int i = lane; i < nvec; i += 32) {
-      const uint4 w = __ldg(rr + i);
-#pragma unroll
-      for (int t = 0; t < 16; ++t)
-        if (t < a.m) acc[t] = dot8(w, __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(t) * a.hidden) + i), acc[t]);
+  // q(x): one warp per 1024 elements
+  const int segs = static_cast<int>((a.hidden + 1023) / 1024), kt = static_cast<int>(a.hidden / 128);
+  for (int u = rank * kRouteWarps + warp; u < a.m * segs; u += kRouteCtas * kRouteWarps) {
+    const int tok = u / segs, c = (u - tok * segs) * 1024 + lane * 32;
+    const Elems32 e = load32<true>(a.x + static_cast<int64_t>(tok) * a.hidden, c, a.hidden);
+    uint32_t sb;
+    const uint4 codes = encode32<kMxFp4>(e, 1.0f, sb);
+    uint32_t word = sb << (8 * (lane & 3));
+    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
+    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
+    if (c < a.hidden) {                                           // whole tiles of four lanes: hidden % 128 == 0
+      *reinterpret_cast<uint4*>(a.x_codes + static_cast<int64_t>(tok) * (a.hidden / 2) + (c >> 1)) = codes;
+      if ((lane & 3) == 0) *reinterpret_cast<uint32_t*>(a.x_scales + mx_scale_offset(tok, c / 32, kt)) = word;
     }
-#pragma unroll
-    for (int t = 0; t < 16; ++t)
-      if (t < a.m) {
-        float v = acc[t];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        if (lane == 0) st_cluster_f32(cluster_map(smem_u32(s_logit + t * a.experts + e), 0), v);
-      }
   }
-  // q(x): one warp per 256 elements
-  const int chunks = static_cast<int>((a.hidden + 255) / 256);
-  for (int u = static_cast<int>(rank) * (kRouteThreads / 32) + warp; u < a.m * chunks; u += kRouteCtas * (kRouteThreads / 32)) {
-    const int t = u / chunks;
-    const int64_t c = static_cast<int64_t>(u - t * chunks) * 256 + lane * 8;
-    const bool in = c < a.hidden;
-    uint4 q = make_uint4(0, 0, 0, 0);
-    if (in) q = __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(t) * a.hidden + c));
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    uint32_t mag = 0;
-    float v[8];
+
+  cluster_sync();                          // every CTA runs before the others write to it
+
+  // logits
+  const int groups = (a.experts + 15) / 16;
+  const int share = groups >= kRouteWarps ? 1 : kRouteWarps / groups;          // warps of a group
+  const int steps = static_cast<int>(a.hidden / 64);
+  const int s0 = steps * rank / kRouteCtas, s1 = steps * (rank + 1) / kRouteCtas;
+  const int64_t row = a.hidden / 8;                                            // of 16-byte pieces
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int round = 0; round * kRouteWarps < groups * share; ++round) {
+    const int slot = round * kRouteWarps + warp, grp = slot / share, sub = slot - grp * share;
+    if (grp < groups) {
+      const int e0 = grp * 16;
+      const bool ra = e0 + g < a.experts, rb = e0 + g + 8 < a.experts, ta = g < a.m, tb = g + 8 < a.m;
+      const uint4* pa = reinterpret_cast<const uint4*>(a.router) + (e0 + g) * row + t;
+      const uint4* xa = reinterpret_cast<const uint4*>(a.x) + g * row + t;
+      float d[2][4] = {};
+#pragma unroll 2
+      for (int s = s0 + sub; s < s1; s += share) {
+        uint4 w[2][2], x[2][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      mag = max(mag, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
-      v[2 * i] = bf16_lo(w[i]);
-      v[2 * i + 1] = bf16_hi(w[i]);
-    }
-    mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
-    mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
-    const bool bad = mag >= 0x7F80u;
-    const uint32_t sb = bad ? 255u : mx_e8m0(mag << 16);
-    const float inv = bad ? 0.0f : mx_e8m0_inverse(sb);
+        for (int h = 0; h < 2; ++h) {
+          const int o = s * 8 + h * 4;
+          w[h][0] = ra ? __ldg(pa + o) : zero;
+          w[h][1] = rb ? __ldg(pa + 8 * row + o) : zero;
+          x[h][0] = ta ? __ldg(xa + o) : zero;
+          x[h][1] = tb ? __ldg(xa + 8 * row + o) : zero;
+        }
+        // a lane's eight columns feed two products of 16, in the same order on both sides
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], inv);
-    const uint32_t codes = bad ? 0u : mx_codes8(v);
-    uint32_t word = sb << (8 * ((lane >> 2) & 3));
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
-    if (in) {
-      *reinterpret_cast<uint32_t*>(a.x_codes + static_cast<int64_t>(t) * (a.hidden / 2) + (c >> 1)) = codes;
-      if ((lane & 15) == 0)
-        *reinterpret_cast<uint32_t*>(a.x_scales + mx_scale_offset(t, c / 32, a.hidden / 128)) = word;
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a0[4] = {w[h][0].x, w[h][1].x, w[h][0].y, w[h][1].y};
+          const uint32_t a1[4] = {w[h][0].z, w[h][1].z, w[h][0].w, w[h][1].w};
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t b0[2] = {x[h][n].x, x[h][n].y}, b1[2] = {x[h][n].z, x[h][n].w};
+            mma_16x8x16(d[n], a0, b0);
+            mma_16x8x16(d[n], a1, b1);
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s_tile[warp * 256 + (g + 8 * (i >> 1)) * 16 + 8 * n + 2 * t + (i & 1)] = d[n][i];
     }
+    __syncthreads();
+    // this round's experts: the warps of a group in order, to the owner
+    const int here = min(groups - round * kRouteWarps / share, kRouteWarps / share);
+    for (int i = threadIdx.x; i < here * 256; i += kRouteThreads) {
+      const int lg = i >> 8, e = (round * kRouteWarps / share + lg) * 16 + ((i >> 4) & 15), tok = i & 15;
+      float v = 0.0f;
+      for (int q = 0; q < share; ++q) v += s_tile[(lg * share + q) * 256 + (i & 255)];
+      if (e < a.experts)
+        st_cluster_f32(cluster_map(smem_u32(s_in + (rank * per_owner + (e >> 3)) * 16 + tok), static_cast<uint32_t>(e & 7)), v);
+    }
+    __syncthreads();
+  }
+  cluster_sync();
+  for (int i = threadIdx.x; i < per_owner * 16; i += kRouteThreads) {
+    const int e = (i >> 4) * 8 + rank, tok = i & 15;
+    float v = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kRouteCtas; ++q) v += s_in[(q * per_owner) * 16 + i];
+    if (e < a.experts) st_cluster_f32(cluster_map(smem_u32(s_logit + tok * a.experts + e), 0), v);
   }
   cluster_sync();
   if (rank != 0) return;
 
   // top-k: one warp per token, top_k rounds of "largest key, lowest index"
   if (warp < a.m) {
-    uint32_t* key = reinterpret_cast<uint32_t*>(s_logit + warp * a.experts);
+    const float* logit = s_logit + warp * a.experts;
     float first = 0.0f, mine = 0.0f;
     for (int j = 0; j < a.top_k; ++j) {
       uint32_t best = 0;
       int at = 0;
       for (int e = lane; e < a.experts; e += 32) {
-        // a taken logit is remembered by its index, the logits stay as they are
         bool taken = false;
         for (int i = 0; i < j; ++i) taken |= s_id[warp][i] == e;
-        const uint32_t k = taken ? 0u : logit_key(__uint_as_float(key[e]));
+        const uint32_t k = taken ? 0u : logit_key(logit[e]);
         if (k > best) { best = k; at = e; }
       }
       const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
       const int id = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, best == top ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
-      const float v = __uint_as_float(key[id]);
+      const float v = logit[id];
       if (j == 0) first = v;
       if (lane == j) mine = expf(v - first);
       if (lane == 0) s_id[warp][j] = id;
@@ -150,34 +180,39 @@ k_moe_route(const MxMoeArgs a) {
       a.probs[warp * a.top_k + lane] = __fdiv_rn(mine, sum);
     }
   }
+  for (int i = threadIdx.x; i < static_cast<int>(a.hidden / 128); i += kRouteThreads) a.counters[i] = 0u;
+  for (int i = threadIdx.x; i < kMoeMaxExperts / 32; i += kRouteThreads) s_used[i] = 0u;
   __syncthreads();
   // the experts in use, in ascending order: id, tokens (bits), and per token its j
-  if (warp == 0) {
-    int n = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += 32) {
-      const int e = e0 + lane;
-      uint32_t mask = 0;
-      uint64_t slot = 0;                                         // four bits per token
-      if (e < a.experts)
-        for (int t = 0; t < a.m; ++t)
-          for (int j = 0; j < a.top_k; ++j)
-            if (s_id[t][j] == e) {
-              mask |= 1u << t;
-              slot |= static_cast<uint64_t>(j) << (4 * t);
-            }
-      const uint32_t used = __ballot_sync(0xFFFFFFFFu, mask != 0);
-      if (mask != 0) {
-        MoeExpert x;
-        x.id = e;
-        x.tokens = mask;
-        x.slots = slot;
-        a.list[n + __popc(used & ((1u << lane) - 1u))] = x;
-      }
-      n += __popc(used);
-    }
-    if (lane == 0) *a.n_used = n;
+  for (int i = threadIdx.x; i < a.m * a.top_k; i += kRouteThreads) {
+    const int e = s_id[i / a.top_k][i % a.top_k];
+    atomicOr(&s_used[e >> 5], 1u << (e & 31));
   }
-  for (int i = threadIdx.x; i < static_cast<int>(a.hidden / 128); i += kRouteThreads) a.counters[i] = 0u;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.m * a.top_k; i += kRouteThreads) {
+    const int tok = i / a.top_k, e = s_id[tok][i % a.top_k];
+    MoeExpert x;
+    x.id = e;
+    x.tokens = 0;
+    x.slots = 0;
+    bool lowest = true;                                           // the expert's first token writes its entry
+    for (int q = 0; q < a.m; ++q)
+      for (int j = 0; j < a.top_k; ++j)
+        if (s_id[q][j] == e) {
+          lowest &= q >= tok;
+          x.tokens |= 1u << q;
+          x.slots |= static_cast<uint64_t>(j) << (4 * q);
+        }
+    if (!lowest) continue;
+    int at = __popc(s_used[e >> 5] & ((1u << (e & 31)) - 1u));
+    for (int w = 0; w < (e >> 5); ++w) at += __popc(s_used[w]);
+    a.list[at] = x;
+  }
+  if (threadIdx.x == 0) {
+    int n = 0;
+    for (int w = 0; w < (a.experts + 31) / 32; ++w) n += __popc(s_used[w]);
+    *a.n_used = n;
+  }
 }
 
 // ------------------------------------------------------------------ the two products
@@ -191,7 +226,7 @@ __host__ __device__ constexpr int moe_tiles(bool up) { return up ? 2 : 1; }
 __host__ __device__ constexpr int moe_stage(bool up) {
   return moe_tiles(up) * (kTile + kAtoms * 512) + kSlots * 128 + kAtoms * 512;
 }
-__host__ __device__ constexpr int moe_stages(bool up) { return up ? 5 : 5; }
+__host__ __device__ constexpr int moe_stages(bool up) { return up ? 5 : 10; }
 __host__ __device__ constexpr size_t moe_smem(bool up) {
   return 1024 + static_cast<size_t>(moe_stages(up)) * moe_stage(up) + 256;
 }
@@ -217,7 +252,7 @@ k_moe_product(const MxMoeArgs a, const __grid_constant__ CUtensorMap wmap, const
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
   uint32_t* last_flag = tmem_slot + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int splits = kUp ? a.splits : 1;
   const int sp = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int64_t k = kUp ? a.hidden : a.inner;                     // contraction
@@ -242,10 +277,11 @@ k_moe_product(const MxMoeArgs a, const __grid_constant__ CUtensorMap wmap, const
     tmem_alloc(tmem_slot, kMoeCols);
     tmem_relinquish();
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && elect_one()) {
     tma_prefetch_desc(&wmap);
     tma_prefetch_desc(&xmap);
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -257,66 +293,74 @@ k_moe_product(const MxMoeArgs a, const __grid_constant__ CUtensorMap wmap, const
   const uint8_t* w_scales = kUp ? a.w13_scales : a.w2_scales;
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool alive = true;
-      for (int u = first; u < units && alive; u += stride) {
-        const int ex = u / row_tiles, rt = u - ex * row_tiles;
-        const int64_t id = a.list[ex].id;
-        // first row of the tile in the stacked weight, and of the up half
-        const int64_t row0 = (kUp ? id * 2 * a.inner : id * a.hidden) + static_cast<int64_t>(rt) * 128;
-        const uint8_t* xs = kUp ? a.x_scales : a.h_scales + static_cast<int64_t>(ex) * kt * 512;
-        for (int ks = kbeg; ks < kend; ++ks, ++it) {
-          const uint32_t stage = it % kStages, phase = (it / kStages) & 1u;
-          if (!mbar_wait(&empty[stage], phase ^ 1u, a.err)) { alive = false; break; }
-          uint8_t* sW = smem_gen + stage * kStageBytes;
-          uint8_t* sX = sW + kW * kTile;
-          uint8_t* sSw = sX + kSlots * 128;
-          const int atoms = min(kAtoms, kt - ks * kAtoms);
-          const uint32_t sbytes = static_cast<uint32_t>(atoms * 512);
+    uint32_t stage = 0, phase = 0;
+    bool alive = true;
+    for (int u = first; u < units && alive; u += stride) {
+      const int ex = u / row_tiles, rt = u - ex * row_tiles;
+      const int id = a.list[ex].id;
+      // row tile of the stacked weight, and of the up half
+      const int tile0 = (kUp ? id * 2 * row_tiles : id * row_tiles) + rt;
+      const uint8_t* xs = kUp ? a.x_scales : a.h_scales + static_cast<int64_t>(ex) * kt * 512;
+      for (int ks = kbeg; ks < kend; ++ks) {
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1u, a.err)) { alive = false; break; }
+        uint8_t* sW = smem_gen + stage * kStageBytes;
+        uint8_t* sX = sW + kW * kTile;
+        uint8_t* sSw = sX + kSlots * 128;
+        const uint32_t sbytes = static_cast<uint32_t>(min(kAtoms, kt - ks * kAtoms) * 512);
+        if (elect_one()) {
           mbar_arrive_expect_tx(&full[stage], kW * kTile + kSlots * 128 + (kW + 1) * sbytes);
 #pragma unroll
           for (int i = 0; i < kW; ++i) {
-            const int64_t r = row0 + i * a.inner;
-            tma_load_2d(sW + i * kTile, &wmap, ks * 128, static_cast<int32_t>(r), &full[stage]);
-            bulk_load(sSw + i * (kAtoms * 512), w_scales + (r / 128 * kt + ks * kAtoms) * 512, sbytes, &full[stage]);
+            tma_load_2d(sW + i * kTile, &wmap, ks * 128, (tile0 + i * row_tiles) * 128, &full[stage]);
+            bulk_load(sSw + i * (kAtoms * 512), w_scales + (static_cast<int64_t>(tile0 + i * row_tiles) * kt + ks * kAtoms) * 512,
+                      sbytes, &full[stage]);
           }
           tma_load_2d(sX, &xmap, ks * 128, kUp ? 0 : ex * kSlots, &full[stage]);
           bulk_load(sSw + kW * (kAtoms * 512), xs + ks * (kAtoms * 512), sbytes, &full[stage]);
         }
+        __syncwarp();
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t it = 0, uctr = 0;
-      bool alive = true;
-      for (int u = first; u < units && alive; u += stride, ++uctr) {
-        const uint32_t ab = uctr & 1u;
-        if (!mbar_wait(&acc_empty[ab], ((uctr >> 1) & 1u) ^ 1u, a.err)) break;
+    uint32_t stage = 0, phase = 0, uctr = 0;
+    bool alive = true;
+    const uint64_t desc0 = smem_desc_sw128(smem0, 16, 1024);         // + (byte offset >> 4)
+    const uint64_t sdesc0 = smem_desc_scales(smem0);
+    for (int u = first; u < units && alive; u += stride, ++uctr) {
+      const uint32_t ab = uctr & 1u;
+      if (!mbar_wait_warp(&acc_empty[ab], ((uctr >> 1) & 1u) ^ 1u, a.err)) break;
+      for (int ks = kbeg; ks < kend; ++ks) {
+        if (!mbar_wait_warp(&full[stage], phase, a.err)) { alive = false; break; }
         tc_fence_after();
-        for (int ks = kbeg; ks < kend; ++ks, ++it) {
-          const uint32_t stage = it % kStages, phase = (it / kStages) & 1u;
-          if (!mbar_wait(&full[stage], phase, a.err)) { alive = false; break; }
-          tc_fence_after();
-          const uint32_t sW = smem0 + stage * kStageBytes, sX = sW + kW * kTile, sSw = sX + kSlots * 128;
-          const int atoms = min(kAtoms, kt - ks * kAtoms);
-          for (int t = 0; t < atoms; ++t) {
+        const uint32_t off = stage * (kStageBytes >> 4);
+        const uint64_t wd = desc0 + off, xd = wd + (kW * kTile >> 4);
+        const uint64_t sw = sdesc0 + off + ((kW * kTile + kSlots * 128) >> 4);
+        const int atoms = min(kAtoms, kt - ks * kAtoms);
+        const uint32_t d = tmem + ab * kAcc;
+        if (elect_one()) {
 #pragma unroll
-            for (int i = 0; i < kW; ++i)
-              tmem_cp_scales(tmem + kSfw + 4 * (i * kAtoms + t), smem_desc_scales(sSw + (i * kAtoms + t) * 512));
-            tmem_cp_scales(tmem + kSfx + 4 * t, smem_desc_scales(sSw + (kW * kAtoms + t) * 512));
-          }
-          for (int q = 0; q < 2 * atoms; ++q) {
-            const uint64_t xd = smem_desc_sw128(sX + q * 32, 16, 1024);
+          for (int t = 0; t < kAtoms; ++t)
+            if (t < atoms) {
 #pragma unroll
-            for (int i = 0; i < kW; ++i)
-              mma_mxf4_ss(tmem + ab * kAcc + i * kSlots, smem_desc_sw128(sW + i * kTile + q * 32, 16, 1024), xd,
-                          idesc_mxf4(128, kSlots, true, 2u * (q & 1)), tmem + kSfw + 4 * (i * kAtoms + (q >> 1)),
-                          tmem + kSfx + 4 * (q >> 1), ks != kbeg || q != 0 ? 1u : 0u);
-          }
+              for (int i = 0; i < kW; ++i)
+                tmem_cp_scales(tmem + kSfw + 4 * (i * kAtoms + t), sw + (i * kAtoms + t) * 32);
+              tmem_cp_scales(tmem + kSfx + 4 * t, sw + (kW * kAtoms + t) * 32);
+            }
+#pragma unroll
+          for (int q = 0; q < 2 * kAtoms; ++q)
+            if (q < 2 * atoms) {
+#pragma unroll
+              for (int i = 0; i < kW; ++i)
+                mma_mxf4_ss(d + i * kSlots, wd + i * (kTile >> 4) + q * 2, xd + q * 2,
+                            idesc_mxf4(128, kSlots, true, 2u * (q & 1)), tmem + kSfw + 4 * (i * kAtoms + (q >> 1)),
+                            tmem + kSfx + 4 * (q >> 1), ks != kbeg || q != 0 ? 1u : 0u);
+            }
           mma_commit(&empty[stage]);
+          if (ks == kend - 1) mma_commit(&acc_full[ab]);
         }
-        if (alive) mma_commit(&acc_full[ab]);
+        __syncwarp();
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
     }
   }
@@ -491,8 +535,8 @@ int mx_moe_splits(int64_t units, int ksteps, int num_sms) {
 cudaError_t launch_mx_moe(const MxMoeArgs& a, const CUtensorMap& w13, const CUtensorMap& x, const CUtensorMap& w2,
                           const CUtensorMap& h, int max_used, int num_sms, cudaStream_t stream) {
   static std::atomic<uint64_t> done{0};
-  const size_t smem = static_cast<size_t>(a.m) * a.experts * sizeof(float);
-  cudaError_t e = smem_limit(k_moe_route, 16 * kMoeMaxExperts * sizeof(float), done);
+  const size_t smem = route_smem(a.experts);
+  cudaError_t e = smem_limit(k_moe_route, route_smem(kMoeMaxExperts), done);
   if (e != cudaSuccess) return e;
   k_moe_route<<<kRouteCtas, kRouteThreads, smem, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

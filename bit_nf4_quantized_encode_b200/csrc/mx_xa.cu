@@ -20,13 +20,6 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32, kCluster = 8;
 
-// D[16 ranks][8 tokens] += A[16][16] B[8][16]^T
-__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
-
 __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) k_mx_xa(const MxXaArgs a) {
   __shared__ float part[kWarps][16][17];       // per warp, then (CTA 0) per CTA of the cluster
   __shared__ float joined[kCluster][16][17];
