@@ -129,7 +129,7 @@ struct MxXaArgs {
 cudaError_t launch_mx_xa(const MxXaArgs& a, cudaStream_t stream);
 
 // Mixture-of-experts layer for at most 16 tokens (mx_moe.cu).
-constexpr int kMoeMaxExperts = 1024, kMoeMaxTopK = 16, kMoeMaxTokens = 16;
+constexpr int kMoeMaxExperts = 256, kMoeMaxTopK = 16, kMoeMaxTokens = 16;
 
 // An expert in use: its tokens (bit t) and, four bits per token, which of the
 // token's choices it is.
@@ -146,7 +146,6 @@ struct MxMoeArgs {
   const uint8_t* w2_scales;   // of [experts * hidden, inner]
   int64_t hidden, inner;      // multiples of 128
   int m, experts, top_k;
-  int splits;                 // CTAs (one cluster) that share an up tile's contraction
   uint16_t* y;                // bf16 [m, hidden]
   int32_t* ids;               // [m, top_k]
   float* probs;               // [m, top_k]
@@ -155,13 +154,14 @@ struct MxMoeArgs {
   uint8_t* x_scales;          // one row tile
   uint8_t* h_codes;           // [used][16][inner / 2]
   uint8_t* h_scales;          // [used] row tiles
-  float* part;                // [m, top_k, hidden]
+  float* slots;               // [runs][2][2 m][128]
   MoeExpert* list;            // [used]
   int* n_used;
-  uint32_t* counters;         // [hidden / 128]
+  uint32_t* counters;         // the down tiles' [hidden / 32], the up tiles' [used * inner / 32]
+  uint32_t* up_counters;
+  int n_counters;
   uint32_t* err;
 };
-int mx_moe_splits(int64_t units, int ksteps, int num_sms);
 // Maps: w13 / w2 / x / h codes as uint8, 128B swizzle, box {128, 128} for the
 // weights and {128, 16} for x [m rows] and h [16 * max_used rows].
 cudaError_t launch_mx_moe(const MxMoeArgs& a, const CUtensorMap& w13, const CUtensorMap& x, const CUtensorMap& w2,

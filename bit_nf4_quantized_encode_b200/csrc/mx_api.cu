@@ -248,7 +248,8 @@ qlora_status run_mx_few(const qlora_mx_tensor* W, const uint16_t* X, int64_t M, 
 
 // ------------------------------------------------------------------ mixture of experts
 struct MoeLayout {
-  size_t x_codes, x_scales, h_codes, h_scales, part, list, n_used, counters, total;
+  size_t x_codes, x_scales, h_codes, h_scales, slots, list, n_used, counters, total;
+  int64_t n_counters;
   int max_used;
 };
 qlora_status moe_layout(int32_t experts, int64_t hidden, int64_t inner, int64_t M, int32_t top_k, MoeLayout* l) {
@@ -266,10 +267,11 @@ qlora_status moe_layout(int32_t experts, int64_t hidden, int64_t inner, int64_t 
   l->x_scales = take(static_cast<size_t>(hidden) / 128 * 512);
   l->h_codes = take(static_cast<size_t>(l->max_used) * 16 * inner / 2);
   l->h_scales = take(static_cast<size_t>(l->max_used) * inner / 128 * 512);
-  l->part = take(static_cast<size_t>(pairs) * hidden * 4);
+  l->slots = take(size_t{kMxMaxRuns} * 2 * 2 * M * 128 * sizeof(float));
   l->list = take(static_cast<size_t>(l->max_used) * sizeof(MoeExpert));
   l->n_used = take(4);
-  l->counters = take(static_cast<size_t>(hidden) / 128 * 4);
+  l->n_counters = hidden / 32 + l->max_used * (inner / 32);
+  l->counters = take(static_cast<size_t>(l->n_counters) * 4);
   l->total = o;
   return QLORA_OK;
 }
@@ -486,7 +488,6 @@ qlora_status qlora_mx_moe_fwd(const qlora_mx_tensor* W13, const qlora_mx_tensor*
   a.m = static_cast<int>(M);
   a.experts = experts;
   a.top_k = top_k;
-  a.splits = mx_moe_splits(static_cast<int64_t>(l.max_used) * (inner / 128), static_cast<int>((hidden + 255) / 256), d.num_sms);
   a.y = Y;
   a.ids = ids;
   a.probs = probs;
@@ -494,10 +495,12 @@ qlora_status qlora_mx_moe_fwd(const qlora_mx_tensor* W13, const qlora_mx_tensor*
   a.x_scales = ws + l.x_scales;
   a.h_codes = ws + l.h_codes;
   a.h_scales = ws + l.h_scales;
-  a.part = reinterpret_cast<float*>(ws + l.part);
+  a.slots = reinterpret_cast<float*>(ws + l.slots);
   a.list = reinterpret_cast<MoeExpert*>(ws + l.list);
   a.n_used = reinterpret_cast<int*>(ws + l.n_used);
   a.counters = reinterpret_cast<uint32_t*>(ws + l.counters);
+  a.up_counters = a.counters + hidden / 32;
+  a.n_counters = static_cast<int>(l.n_counters);
   a.err = d.err;
   const uint64_t hp = static_cast<uint64_t>(hidden) / 2, ip = static_cast<uint64_t>(inner) / 2;
   CUtensorMap w13, w2, x, h;

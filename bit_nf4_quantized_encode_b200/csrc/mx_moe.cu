@@ -5,8 +5,7 @@
 //                index first among equal ones) and p = softmax over them; the
 //                list of experts in use with their tokens; q(x).
 //   k_moe_up     per expert in use: [g; u] = W13 q(x), h = g / (1 + e^-g) * u, q(h).
-//   k_moe_down   per expert in use: o = W2 q(h); y[t] = sum_j p[t, j] o_j[t],
-//                summed in the order of j by the CTA that completes a row tile.
+//   k_moe_down   y[t] = sum over its experts, in ascending order, of p W2 q(h).
 //
 // Both products are those of mx_stream.cu: the weight is the 128-row operand of
 // tcgen05's block-scaled kind, the 16 token slots the other one, whichever of
@@ -25,6 +24,7 @@
 #include "mx_encode.cuh"
 #include "mx_format.cuh"
 #include "mx_ptx.cuh"
+#include "mx_runs.cuh"
 #include "nf4_device.cuh"
 
 namespace qlora {
@@ -33,10 +33,9 @@ namespace {
 // ------------------------------------------------------------------ routing
 // One cluster of eight CTAs.  The logits are an [experts, 16] product over hidden:
 // a CTA takes an eighth of hidden, its warps groups of 16 experts (several warps a
-// group where there are few), with m16n8k16 (bf16 in, fp32 sums).  The parts of
-// an expert meet in the CTA that owns it (expert mod 8), summed in a fixed order,
-// and the logits in the first CTA, which chooses.  Latency is all there is: every
-// load of a warp is issued at once.
+// group where there are few), with m16n8k16 (bf16 in, fp32 sums).  The parts meet
+// in the first CTA, which sums them in a fixed order and chooses: a warp per token
+// keeps the token's logits in registers.  Latency is all there is.
 constexpr int kRouteCtas = 8;
 constexpr int kRouteThreads = 512, kRouteWarps = kRouteThreads / 32;
 
@@ -47,24 +46,30 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
   return (b >> 31) ? ~b : (b | 0x80000000u);
 }
 
-// Shared memory: the logits [16][experts] (the first CTA's), the owner's parts
-// [8][ceil(experts / 8)][16] and the warps' tiles [16][16][16].
-__host__ __device__ constexpr size_t route_smem(int experts) {
-  return sizeof(float) * (static_cast<size_t>(16) * experts + static_cast<size_t>(128) * ((experts + 7) / 8) + 16 * 256);
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float((k >> 31) ? k ^ 0x80000000u : ~k);
 }
+
+// Shared memory: the CTAs' parts of the logits [8][16][experts] (the first CTA's),
+// the warps' tiles [16][16][16].
+__host__ __device__ constexpr size_t route_smem(int experts) {
+  return sizeof(float) * (static_cast<size_t>(kRouteCtas) * 16 * experts + kRouteWarps * 256);
+}
+constexpr int kKeys = kMoeMaxExperts / 32;          // logits of a lane
 
 __global__ void __launch_bounds__(kRouteThreads) __cluster_dims__(kRouteCtas, 1, 1)
 k_moe_route(const MxMoeArgs a) {
   extern __shared__ float smem[];
-  __shared__ int s_id[16][16];
-  __shared__ uint32_t s_used[kMoeMaxExperts / 32];
-  const int per_owner = (a.experts + 7) / 8;
-  float* s_logit = smem;
-  float* s_in = s_logit + 16 * a.experts;
-  float* s_tile = s_in + 128 * per_owner;
+  __shared__ uint32_t s_mask[kMoeMaxExperts];        // an expert's tokens
+  __shared__ unsigned long long s_slot[kMoeMaxExperts];
+  __shared__ int s_count[kMoeMaxExperts / 32];
+  float* s_in = smem;
+  float* s_tile = s_in + kRouteCtas * 16 * a.experts;
   const int warp = warp_index(), lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(cluster_rank());
   asm volatile("griddepcontrol.launch_dependents;");
+  for (int i = rank * kRouteThreads + threadIdx.x; i < a.n_counters; i += kRouteCtas * kRouteThreads) a.counters[i] = 0u;
+  cluster_arrive();                        // every CTA runs before the others write to it: waited for below
 
   // q(x): one warp per 1024 elements
   const int segs = static_cast<int>((a.hidden + 1023) / 1024), kt = static_cast<int>(a.hidden / 128);
@@ -81,8 +86,6 @@ k_moe_route(const MxMoeArgs a) {
       if ((lane & 3) == 0) *reinterpret_cast<uint32_t*>(a.x_scales + mx_scale_offset(tok, c / 32, kt)) = word;
     }
   }
-
-  cluster_sync();                          // every CTA runs before the others write to it
 
   // logits
   const int groups = (a.experts + 15) / 16;
@@ -129,88 +132,88 @@ k_moe_route(const MxMoeArgs a) {
         for (int i = 0; i < 4; ++i) s_tile[warp * 256 + (g + 8 * (i >> 1)) * 16 + 8 * n + 2 * t + (i & 1)] = d[n][i];
     }
     __syncthreads();
-    // this round's experts: the warps of a group in order, to the owner
-    const int here = min(groups - round * kRouteWarps / share, kRouteWarps / share);
-    for (int i = threadIdx.x; i < here * 256; i += kRouteThreads) {
-      const int lg = i >> 8, e = (round * kRouteWarps / share + lg) * 16 + ((i >> 4) & 15), tok = i & 15;
+    if (round == 0) cluster_wait();
+    // this round's experts: the warps of a group in order
+    const int e0 = round * kRouteWarps / share * 16, here = min(a.experts - e0, kRouteWarps / share * 16);
+    for (int i = threadIdx.x; i < here * 16; i += kRouteThreads) {
+      const int e = i >> 4, tok = i & 15;
       float v = 0.0f;
-      for (int q = 0; q < share; ++q) v += s_tile[(lg * share + q) * 256 + (i & 255)];
-      if (e < a.experts)
-        st_cluster_f32(cluster_map(smem_u32(s_in + (rank * per_owner + (e >> 3)) * 16 + tok), static_cast<uint32_t>(e & 7)), v);
+      for (int q = 0; q < share; ++q) v += s_tile[((e >> 4) * share + q) * 256 + (i & 255)];
+      st_cluster_f32(cluster_map(smem_u32(s_in + (rank * 16 + tok) * a.experts + e0 + e), 0), v);
     }
     __syncthreads();
   }
   cluster_sync();
-  for (int i = threadIdx.x; i < per_owner * 16; i += kRouteThreads) {
-    const int e = (i >> 4) * 8 + rank, tok = i & 15;
-    float v = 0.0f;
-#pragma unroll
-    for (int q = 0; q < kRouteCtas; ++q) v += s_in[(q * per_owner) * 16 + i];
-    if (e < a.experts) st_cluster_f32(cluster_map(smem_u32(s_logit + tok * a.experts + e), 0), v);
-  }
-  cluster_sync();
   if (rank != 0) return;
+  for (int e = threadIdx.x; e < kMoeMaxExperts; e += kRouteThreads) {
+    s_mask[e] = 0u;
+    s_slot[e] = 0ull;
+  }
+  __syncthreads();
 
   // top-k: one warp per token, top_k rounds of "largest key, lowest index"
   if (warp < a.m) {
-    const float* logit = s_logit + warp * a.experts;
+    uint32_t key[kKeys];
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const int e = i * 32 + lane;
+      key[i] = 0u;
+      if (e < a.experts) {
+        float v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kRouteCtas; ++q) v += s_in[(q * 16 + warp) * a.experts + e];
+        key[i] = logit_key(v);
+      }
+    }
     float first = 0.0f, mine = 0.0f;
+    int my_id = 0;
     for (int j = 0; j < a.top_k; ++j) {
       uint32_t best = 0;
       int at = 0;
-      for (int e = lane; e < a.experts; e += 32) {
-        bool taken = false;
-        for (int i = 0; i < j; ++i) taken |= s_id[warp][i] == e;
-        const uint32_t k = taken ? 0u : logit_key(logit[e]);
-        if (k > best) { best = k; at = e; }
-      }
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i)
+        if (key[i] > best) { best = key[i]; at = i; }
       const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-      const int id = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, best == top ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
-      const float v = logit[id];
-      if (j == 0) first = v;
-      if (lane == j) mine = expf(v - first);
-      if (lane == 0) s_id[warp][j] = id;
-      __syncwarp();
+      const uint32_t id = __reduce_min_sync(0xFFFFFFFFu, best == top ? static_cast<uint32_t>(at * 32 + lane) : 0xFFFFFFFFu);
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i)
+        if (static_cast<uint32_t>(i * 32 + lane) == id) key[i] = 0u;
+      if (j == 0) first = key_logit(top);
+      if (lane == j) {
+        mine = expf(key_logit(top) - first);
+        my_id = static_cast<int>(id);
+      }
     }
     float sum = lane < a.top_k ? mine : 0.0f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane < a.top_k) {
-      a.ids[warp * a.top_k + lane] = s_id[warp][lane];
+      a.ids[warp * a.top_k + lane] = my_id;
       a.probs[warp * a.top_k + lane] = __fdiv_rn(mine, sum);
+      atomicOr(&s_mask[my_id], 1u << warp);
+      atomicOr(&s_slot[my_id], static_cast<unsigned long long>(lane) << (4 * warp));
     }
   }
-  for (int i = threadIdx.x; i < static_cast<int>(a.hidden / 128); i += kRouteThreads) a.counters[i] = 0u;
-  for (int i = threadIdx.x; i < kMoeMaxExperts / 32; i += kRouteThreads) s_used[i] = 0u;
   __syncthreads();
   // the experts in use, in ascending order: id, tokens (bits), and per token its j
-  for (int i = threadIdx.x; i < a.m * a.top_k; i += kRouteThreads) {
-    const int e = s_id[i / a.top_k][i % a.top_k];
-    atomicOr(&s_used[e >> 5], 1u << (e & 31));
-  }
+  static_assert(kMoeMaxExperts <= kRouteThreads);
+  const int e = threadIdx.x;
+  const uint32_t mask = e < kMoeMaxExperts ? s_mask[e] : 0u;
+  const uint32_t used = __ballot_sync(0xFFFFFFFFu, mask != 0u);
+  if (e < kMoeMaxExperts && lane == 0) s_count[warp] = __popc(used);
   __syncthreads();
-  for (int i = threadIdx.x; i < a.m * a.top_k; i += kRouteThreads) {
-    const int tok = i / a.top_k, e = s_id[tok][i % a.top_k];
+  if (mask != 0u) {
+    int at = __popc(used & ((1u << lane) - 1u));
+    for (int w = 0; w < warp; ++w) at += s_count[w];
     MoeExpert x;
     x.id = e;
-    x.tokens = 0;
-    x.slots = 0;
-    bool lowest = true;                                           // the expert's first token writes its entry
-    for (int q = 0; q < a.m; ++q)
-      for (int j = 0; j < a.top_k; ++j)
-        if (s_id[q][j] == e) {
-          lowest &= q >= tok;
-          x.tokens |= 1u << q;
-          x.slots |= static_cast<uint64_t>(j) << (4 * q);
-        }
-    if (!lowest) continue;
-    int at = __popc(s_used[e >> 5] & ((1u << (e & 31)) - 1u));
-    for (int w = 0; w < (e >> 5); ++w) at += __popc(s_used[w]);
+    x.tokens = mask;
+    x.slots = s_slot[e];
     a.list[at] = x;
   }
   if (threadIdx.x == 0) {
     int n = 0;
-    for (int w = 0; w < (a.experts + 31) / 32; ++w) n += __popc(s_used[w]);
+    for (int w = 0; w < kMoeMaxExperts / 32; ++w) n += s_count[w];
     *a.n_used = n;
   }
 }
@@ -232,6 +235,30 @@ __host__ __device__ constexpr size_t moe_smem(bool up) {
 }
 constexpr uint32_t kMoeCols = 128;          // TMEM columns
 
+// h of token t at a lane's row -> q(h): a block is the warp's 32 rows.
+__device__ __forceinline__ void emit_h(const MxMoeArgs& a, int ex, int rt, int row_tiles, int t, int quarter, int lane,
+                                       float g, float up) {
+  const float h = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), up);
+  const uint32_t mag = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu);
+  const bool bad = mag >= 0x7F800000u;
+  const uint32_t sb = bad ? 255u : min(mx_e8m0(mag), 253u);
+  float v[8] = {bad ? 0.0f : __fmul_rn(h, mx_e8m0_inverse(bad ? 127u : sb)), 0, 0, 0, 0, 0, 0, 0};
+  uint32_t word = (mx_codes8(v) & 15u) << (4 * (lane & 7));
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
+  const int64_t row = static_cast<int64_t>(ex) * kSlots + t;
+  if ((lane & 7) == 0)
+    *reinterpret_cast<uint32_t*>(a.h_codes + row * (a.inner / 2) + rt * 64 + quarter * 16 + (lane >> 3) * 4) = word;
+  if (lane == 0)
+    a.h_scales[(static_cast<int64_t>(ex) * row_tiles + rt) * 512 + t * 16 + quarter] = static_cast<uint8_t>(sb);
+}
+
+// The steps (256 of the contraction) are dealt in equal runs (mx_runs.cuh).
+// k_moe_up: a tile is 128 gate rows and the 128 up rows beside them of an expert
+// in use.  k_moe_down: a tile is 128 rows of y, its steps run over all experts in
+// use; an expert's product leaves the accumulator at its last step (or the run's)
+// and is added to the rows' y in registers, times its tokens' p.
 template <bool kUp>
 __global__ void __launch_bounds__(kThreads, 1)
 k_moe_product(const MxMoeArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap) {
@@ -248,18 +275,13 @@ k_moe_product(const MxMoeArgs a, const __grid_constant__ CUtensorMap wmap, const
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;      // [2]
   uint64_t* acc_empty = acc_full + 2;        // [2]
-  uint64_t* epi_bar = acc_empty + 2;         // the 128 epilogue threads meet here (bounded waits)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
-  uint32_t* last_flag = tmem_slot + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
 
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  const int splits = kUp ? a.splits : 1;
-  const int sp = splits > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int64_t k = kUp ? a.hidden : a.inner;                     // contraction
+  const int k = static_cast<int>(kUp ? a.hidden : a.inner);       // contraction
   const int row_tiles = static_cast<int>((kUp ? a.inner : a.hidden) / 128);
-  const int kt = static_cast<int>(k / 128);                       // scale tiles along k
-  const int ksteps = static_cast<int>((k + 255) / 256);
-  const int kbeg = ksteps * sp / splits, kend = ksteps * (sp + 1) / splits;
+  const int kt = k / 128;                                         // scale tiles along k
+  const int ksteps = (k + 255) / 256;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -270,7 +292,6 @@ k_moe_product(const MxMoeArgs a, const __grid_constant__ CUtensorMap wmap, const
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], 128);
     }
-    mbar_init(epi_bar, 128);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -288,116 +309,119 @@ k_moe_product(const MxMoeArgs a, const __grid_constant__ CUtensorMap wmap, const
   const uint32_t tmem = *tmem_slot;
   if (kUp) asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int units = *a.n_used * row_tiles;
-  const int first = static_cast<int>(blockIdx.x) / splits, stride = static_cast<int>(gridDim.x) / splits;
-  const uint8_t* w_scales = kUp ? a.w13_scales : a.w2_scales;
+  const int n_used = *a.n_used;
+  const int per_tile = kUp ? ksteps : ksteps * n_used;
+  const int64_t total = static_cast<int64_t>(kUp ? n_used * row_tiles : row_tiles) * per_tile;
+  // the grid is for the most experts that can be in use; no run is empty
+  const int runs = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + 1) / 2));
+  const int run = static_cast<int>(blockIdx.x);
+  const int64_t begin = run_begin(total, min(run, runs), runs);
+  const int nsteps = run < runs ? static_cast<int>(run_begin(total, run + 1, runs) - begin) : 0;
+  const int tile0 = static_cast<int>(begin / per_tile), step0 = static_cast<int>(begin - static_cast<int64_t>(tile0) * per_tile);
 
   if (warp == 0) {
+    // ------------------------------------------------ TMA producer
+    const uint8_t* w_scales = kUp ? a.w13_scales : a.w2_scales;
     uint32_t stage = 0, phase = 0;
-    bool alive = true;
-    for (int u = first; u < units && alive; u += stride) {
-      const int ex = u / row_tiles, rt = u - ex * row_tiles;
-      const int id = a.list[ex].id;
-      // row tile of the stacked weight, and of the up half
-      const int tile0 = (kUp ? id * 2 * row_tiles : id * row_tiles) + rt;
-      const uint8_t* xs = kUp ? a.x_scales : a.h_scales + static_cast<int64_t>(ex) * kt * 512;
-      for (int ks = kbeg; ks < kend; ++ks) {
-        if (!mbar_wait_warp(&empty[stage], phase ^ 1u, a.err)) { alive = false; break; }
-        uint8_t* sW = smem_gen + stage * kStageBytes;
-        uint8_t* sX = sW + kW * kTile;
-        uint8_t* sSw = sX + kSlots * 128;
-        const uint32_t sbytes = static_cast<uint32_t>(min(kAtoms, kt - ks * kAtoms) * 512);
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&full[stage], kW * kTile + kSlots * 128 + (kW + 1) * sbytes);
+    int ex = kUp ? tile0 / row_tiles : step0 / ksteps;            // place in the list of experts in use
+    int rt = kUp ? tile0 - ex * row_tiles : tile0, ks = kUp ? step0 : step0 - ex * ksteps;
+    bool fresh = true;
+    int wt = 0;                                                   // row tile of the stacked weight
+    for (int i = 0; i < nsteps; ++i) {
+      if (fresh) wt = a.list[ex].id * (kUp ? 2 * row_tiles : row_tiles) + rt;
+      if (!mbar_wait_warp(&empty[stage], phase ^ 1u, a.err)) break;
+      uint8_t* sW = smem_gen + stage * kStageBytes;
+      uint8_t* sX = sW + kW * kTile;
+      uint8_t* sSw = sX + kSlots * 128;
+      const uint32_t sbytes = static_cast<uint32_t>(min(kAtoms, kt - ks * kAtoms) * 512);
+      const uint8_t* xs = (kUp ? a.x_scales : a.h_scales + static_cast<int64_t>(ex) * kt * 512) + ks * (kAtoms * 512);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&full[stage], kW * kTile + kSlots * 128 + (kW + 1) * sbytes);
 #pragma unroll
-          for (int i = 0; i < kW; ++i) {
-            tma_load_2d(sW + i * kTile, &wmap, ks * 128, (tile0 + i * row_tiles) * 128, &full[stage]);
-            bulk_load(sSw + i * (kAtoms * 512), w_scales + (static_cast<int64_t>(tile0 + i * row_tiles) * kt + ks * kAtoms) * 512,
-                      sbytes, &full[stage]);
-          }
-          tma_load_2d(sX, &xmap, ks * 128, kUp ? 0 : ex * kSlots, &full[stage]);
-          bulk_load(sSw + kW * (kAtoms * 512), xs + ks * (kAtoms * 512), sbytes, &full[stage]);
+        for (int w = 0; w < kW; ++w) {
+          tma_load_2d(sW + w * kTile, &wmap, ks * 128, (wt + w * row_tiles) * 128, &full[stage]);
+          bulk_load(sSw + w * (kAtoms * 512), w_scales + (static_cast<int64_t>(wt + w * row_tiles) * kt + ks * kAtoms) * 512,
+                    sbytes, &full[stage]);
         }
-        __syncwarp();
-        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+        tma_load_2d(sX, &xmap, ks * 128, kUp ? 0 : ex * kSlots, &full[stage]);
+        bulk_load(sSw + kW * (kAtoms * 512), xs, sbytes, &full[stage]);
       }
+      __syncwarp();
+      fresh = ++ks == ksteps;
+      if (fresh) {                                                // the next expert's rows (down) or row tile (up)
+        ks = 0;
+        if (kUp) {
+          if (++rt == row_tiles) { rt = 0; ++ex; }
+        } else if (++ex == n_used) {
+          ex = 0;
+          ++rt;
+        }
+      }
+      if (++stage == kStages) { stage = 0; phase ^= 1u; }
     }
   } else if (warp == 1) {
-    uint32_t stage = 0, phase = 0, uctr = 0;
-    bool alive = true;
+    // ------------------------------------------------ MMA issuer
+    uint32_t stage = 0, phase = 0, seg = 0;
     const uint64_t desc0 = smem_desc_sw128(smem0, 16, 1024);         // + (byte offset >> 4)
     const uint64_t sdesc0 = smem_desc_scales(smem0);
-    for (int u = first; u < units && alive; u += stride, ++uctr) {
-      const uint32_t ab = uctr & 1u;
-      if (!mbar_wait_warp(&acc_empty[ab], ((uctr >> 1) & 1u) ^ 1u, a.err)) break;
-      for (int ks = kbeg; ks < kend; ++ks) {
-        if (!mbar_wait_warp(&full[stage], phase, a.err)) { alive = false; break; }
-        tc_fence_after();
-        const uint32_t off = stage * (kStageBytes >> 4);
-        const uint64_t wd = desc0 + off, xd = wd + (kW * kTile >> 4);
-        const uint64_t sw = sdesc0 + off + ((kW * kTile + kSlots * 128) >> 4);
-        const int atoms = min(kAtoms, kt - ks * kAtoms);
-        const uint32_t d = tmem + ab * kAcc;
-        if (elect_one()) {
+    int ks = kUp ? step0 : step0 % ksteps;
+    bool fresh = true;
+    for (int i = 0; i < nsteps; ++i) {
+      const uint32_t ab = seg & 1u;
+      if (fresh && !mbar_wait_warp(&acc_empty[ab], ((seg >> 1) & 1u) ^ 1u, a.err)) break;
+      if (!mbar_wait_warp(&full[stage], phase, a.err)) break;
+      tc_fence_after();
+      const uint32_t off = stage * (kStageBytes >> 4);
+      const uint64_t wd = desc0 + off, xd = wd + (kW * kTile >> 4);
+      const uint64_t sw = sdesc0 + off + ((kW * kTile + kSlots * 128) >> 4);
+      const int atoms = min(kAtoms, kt - ks * kAtoms);
+      const uint32_t d = tmem + ab * kAcc;
+      const bool last = ks == ksteps - 1 || i == nsteps - 1;
+      if (elect_one()) {
 #pragma unroll
-          for (int t = 0; t < kAtoms; ++t)
-            if (t < atoms) {
+        for (int t = 0; t < kAtoms; ++t)
+          if (t < atoms) {
 #pragma unroll
-              for (int i = 0; i < kW; ++i)
-                tmem_cp_scales(tmem + kSfw + 4 * (i * kAtoms + t), sw + (i * kAtoms + t) * 32);
-              tmem_cp_scales(tmem + kSfx + 4 * t, sw + (kW * kAtoms + t) * 32);
-            }
+            for (int w = 0; w < kW; ++w)
+              tmem_cp_scales(tmem + kSfw + 4 * (w * kAtoms + t), sw + (w * kAtoms + t) * 32);
+            tmem_cp_scales(tmem + kSfx + 4 * t, sw + (kW * kAtoms + t) * 32);
+          }
 #pragma unroll
-          for (int q = 0; q < 2 * kAtoms; ++q)
-            if (q < 2 * atoms) {
+        for (int q = 0; q < 2 * kAtoms; ++q)
+          if (q < 2 * atoms) {
 #pragma unroll
-              for (int i = 0; i < kW; ++i)
-                mma_mxf4_ss(d + i * kSlots, wd + i * (kTile >> 4) + q * 2, xd + q * 2,
-                            idesc_mxf4(128, kSlots, true, 2u * (q & 1)), tmem + kSfw + 4 * (i * kAtoms + (q >> 1)),
-                            tmem + kSfx + 4 * (q >> 1), ks != kbeg || q != 0 ? 1u : 0u);
-            }
-          mma_commit(&empty[stage]);
-          if (ks == kend - 1) mma_commit(&acc_full[ab]);
-        }
-        __syncwarp();
-        if (++stage == kStages) { stage = 0; phase ^= 1u; }
+            for (int w = 0; w < kW; ++w)
+              mma_mxf4_ss(d + w * kSlots, wd + w * (kTile >> 4) + q * 2, xd + q * 2,
+                          idesc_mxf4(128, kSlots, true, 2u * (q & 1)), tmem + kSfw + 4 * (w * kAtoms + (q >> 1)),
+                          tmem + kSfx + 4 * (q >> 1), !fresh || q != 0 ? 1u : 0u);
+          }
+        mma_commit(&empty[stage]);
+        if (last) mma_commit(&acc_full[ab]);
       }
+      __syncwarp();
+      fresh = last;
+      if (last) ++seg;
+      if (++ks == ksteps) ks = 0;
+      if (++stage == kStages) { stage = 0; phase ^= 1u; }
     }
-  }
-
-  const int quarter = warp & 3, rl = quarter * 32 + lane;
-  // h of token t at row rl of the tile -> q(h): a block is the warp's 32 rows
-  auto emit_h = [&](int ex, int rt, int t, float g, float up) {
-    const float h = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), up);
-    const uint32_t mag = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu);
-    const bool bad = mag >= 0x7F800000u;
-    const uint32_t sb = bad ? 255u : min(mx_e8m0(mag), 253u);
-    float v[8] = {bad ? 0.0f : __fmul_rn(h, mx_e8m0_inverse(bad ? 127u : sb)), 0, 0, 0, 0, 0, 0, 0};
-    uint32_t word = (mx_codes8(v) & 15u) << (4 * (lane & 7));
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 1);
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2);
-    word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-    const int64_t row = static_cast<int64_t>(ex) * kSlots + t;
-    if ((lane & 7) == 0)
-      *reinterpret_cast<uint32_t*>(a.h_codes + row * (a.inner / 2) + rt * 64 + quarter * 16 + (lane >> 3) * 4) = word;
-    if (lane == 0)
-      a.h_scales[(static_cast<int64_t>(ex) * row_tiles + rt) * 512 + t * 16 + quarter] = static_cast<uint8_t>(sb);
-  };
-
-  if (splits == 1 && warp >= 2) {
-    const int et = (warp - 2) * 32 + lane;
-    uint32_t uctr = 0, ephase = 0;
-    auto epi_sync = [&]() -> bool {
-      mbar_arrive(epi_bar);
-      const bool ok = mbar_wait(epi_bar, ephase, a.err);
-      ephase ^= 1u;
-      return ok;
-    };
-    for (int u = first; u < units; u += stride, ++uctr) {
-      const int ex = u / row_tiles, rt = u - ex * row_tiles;
+  } else {
+    // ------------------------------------------------ epilogue
+    const int quarter = warp & 3, rl = quarter * 32 + lane;
+    const int64_t slot_floats = static_cast<int64_t>(kW) * a.m * 128;
+    int tile = tile0, s = step0, left = nsteps;
+    float y[kSlots];
+#pragma unroll
+    for (int t = 0; t < kSlots; ++t) y[t] = 0.0f;
+    int from = step0;                                             // first step of this run's part of the tile
+    for (uint32_t seg = 0; left > 0; ++seg) {
+      const int ex = kUp ? tile / row_tiles : s / ksteps;
+      const int ks = kUp ? s : s - ex * ksteps;
+      const int steps = min(ksteps - ks, left);
+      left -= steps;
+      s += steps;
       const MoeExpert info = a.list[ex];
-      const uint32_t ab = uctr & 1u;
-      if (!mbar_wait(&acc_full[ab], (uctr >> 1) & 1u, a.err)) break;
+      const uint32_t ab = seg & 1u;
+      if (!mbar_wait(&acc_full[ab], (seg >> 1) & 1u, a.err)) break;
       tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ab * kAcc;
       uint32_t v0[16], v1[16];
@@ -406,79 +430,65 @@ k_moe_product(const MxMoeArgs a, const __grid_constant__ CUtensorMap wmap, const
       tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(&acc_empty[ab]);
-      if (kUp) {
+      const bool whole = from == 0 && s == per_tile;
+      float* mine = my_slot(a.slots, slot_floats, tile == tile0) + rl;
+      if constexpr (kUp) {
+        const int rt = tile - ex * row_tiles;
+        auto emit = [&](int t, float g, float up) { emit_h(a, ex, rt, row_tiles, t, quarter, lane, g, up); };
 #pragma unroll
         for (int t = 0; t < kSlots; ++t)
-          if ((info.tokens >> t) & 1u) emit_h(ex, rt, t, __uint_as_float(v0[t]), __uint_as_float(v1[t]));
+          if ((info.tokens >> t) & 1u) {
+            if (whole) {
+              emit(t, __uint_as_float(v0[t]), __uint_as_float(v1[t]));
+            } else {
+              mine[(2 * t) * 128] = __uint_as_float(v0[t]);
+              mine[(2 * t + 1) * 128] = __uint_as_float(v1[t]);
+            }
+          }
+        if (!whole) {
+          const Parts p = parts_of(a.slots + rl, slot_floats, total, static_cast<int64_t>(tile) * per_tile, per_tile, runs);
+          if (count_part(a.up_counters + tile * 4 + quarter, p.n))
+            for (uint32_t left_t = info.tokens; left_t != 0u; left_t &= left_t - 1u) {
+              const int t = __ffs(static_cast<int>(left_t)) - 1;
+              Parts pt = p;
+              pt.first += (2 * t) * 128;
+              float gu[2];
+              join_parts<2, 8>(pt, 2, [&](int i, float v) { gu[i] = v; });
+              emit(t, gu[0], gu[1]);
+            }
+        }
       } else {
-        const int64_t row = static_cast<int64_t>(rt) * 128 + rl;
 #pragma unroll
         for (int t = 0; t < kSlots; ++t)
           if ((info.tokens >> t) & 1u) {
             const int j = static_cast<int>((info.slots >> (4 * t)) & 15u);
-            a.part[(static_cast<int64_t>(t) * a.top_k + j) * a.hidden + row] = __uint_as_float(v0[t]);
+            y[t] = __fmaf_rn(__ldg(a.probs + t * a.top_k + j), __uint_as_float(v0[t]), y[t]);
           }
-        __threadfence();
-        if (!epi_sync()) break;
-        if (et == 0) *last_flag = atomicAdd(a.counters + rt, 1u) == static_cast<uint32_t>(units / row_tiles - 1) ? 1u : 0u;
-        if (!epi_sync()) break;
-        if (*last_flag == 0u) continue;
-        __threadfence();
-        for (int t = 0; t < a.m; ++t) {
-          float y = 0.0f;
-          for (int j = 0; j < a.top_k; ++j)
-            y = __fmaf_rn(a.probs[t * a.top_k + j], __ldcg(a.part + (static_cast<int64_t>(t) * a.top_k + j) * a.hidden + row), y);
-          const __nv_bfloat16 b = __float2bfloat16_rn(y);
+        if (s != per_tile && left > 0) continue;                    // more experts of this tile
+        const int64_t row = static_cast<int64_t>(tile) * 128 + rl;
+        auto store = [&](int t, float v) {
+          const __nv_bfloat16 b = __float2bfloat16_rn(v);
           a.y[static_cast<int64_t>(t) * a.hidden + row] = *reinterpret_cast<const uint16_t*>(&b);
+        };
+#pragma unroll
+        for (int t = 0; t < kSlots; ++t)
+          if (t < a.m) {
+            if (whole) store(t, y[t]);
+            else mine[t * 128] = y[t];
+            y[t] = 0.0f;
+          }
+        if (!whole) {
+          const Parts p = parts_of(a.slots + rl, slot_floats, total, static_cast<int64_t>(tile) * per_tile, per_tile, runs);
+          if (count_part(a.counters + tile * 4 + quarter, p.n)) join_columns(p, a.m, store);
         }
       }
-    }
-  }
-
-  if (kUp && splits > 1) {
-    // One tile pair per cluster: CTA q owns tokens q * 16 / splits ...; every CTA
-    // sends it that part of its tiles, into the stages, summed in rank order.
-    const bool work = first < units;
-    if (warp >= 2 && work) {
-      mbar_wait(&acc_full[0], 0, a.err);
-      tc_fence_after();
-    }
-    __syncwarp();
-    cluster_sync();
-    const int own = kSlots / splits;
-    if (warp >= 2 && work) {
-      const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-      uint32_t v[2][16];
-      tmem_ld16(taddr, v[0]);
-      tmem_ld16(taddr + kSlots, v[kW - 1]);
-      tmem_wait_ld();
-#pragma unroll
-      for (int t = 0; t < kSlots; ++t)
-#pragma unroll
-        for (int i = 0; i < kW; ++i)
-          st_cluster_f32(cluster_map(smem0 + static_cast<uint32_t>(((sp * own + t % own) * kW + i) * 128 + rl) * 4u,
-                                     static_cast<uint32_t>(t / own)),
-                         __uint_as_float(v[i][t]));
-    }
-    cluster_sync();
-    if (warp >= 2 && work) {
-      const int ex = first / row_tiles, rt = first - ex * row_tiles;
-      const MoeExpert info = a.list[ex];
-      const float* part = reinterpret_cast<const float*>(smem_gen) + rl;
-      for (int c = 0; c < own; ++c) {
-        const int t = sp * own + c;
-        if (!((info.tokens >> t) & 1u)) continue;
-        float g = 0.0f, up = 0.0f;
-        for (int q = 0; q < splits; ++q) {
-          g += part[((q * own + c) * kW) * 128];
-          up += part[((q * own + c) * kW + kW - 1) * 128];
-        }
-        emit_h(ex, rt, t, g, up);
-      }
+      ++tile;
+      s = from = 0;
     }
   }
 
   tc_fence_before();
+  __syncwarp();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -504,33 +514,26 @@ cudaError_t launch_product(const MxMoeArgs& a, const CUtensorMap& w, const CUten
   static std::atomic<uint64_t> done{0};
   cudaError_t e = smem_limit(k_moe_product<kUp>, moe_smem(kUp), done);
   if (e != cudaSuccess) return e;
-  const int64_t units = static_cast<int64_t>(max_used) * ((kUp ? a.inner : a.hidden) / 128);
-  const int splits = kUp ? a.splits : 1;
-  int64_t grid = units * splits;
-  if (splits == 1 && grid > num_sms) grid = num_sms;
+  // runs of two steps at least where every expert that can be in use is
+  const int64_t k = kUp ? a.hidden : a.inner, rows = kUp ? a.inner : a.hidden;
+  const int64_t steps = static_cast<int64_t>(max_used) * (rows / 128) * ((k + 255) / 256);
+  int64_t grid = (steps + 1) / 2;
+  if (grid > num_sms) grid = num_sms;
+  if (grid > kMxMaxRuns) grid = kMxMaxRuns;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = moe_smem(kUp);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = splits > 1 ? 2 : 1;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k_moe_product<kUp>, a, w, x);
 }
 
 }  // namespace
-
-int mx_moe_splits(int64_t units, int ksteps, int num_sms) {
-  int s = 1;
-  while (s < 4 && units * s * 2 <= num_sms && ksteps >= 4 * s) s *= 2;
-  return s;
-}
 
 cudaError_t launch_mx_moe(const MxMoeArgs& a, const CUtensorMap& w13, const CUtensorMap& x, const CUtensorMap& w2,
                           const CUtensorMap& h, int max_used, int num_sms, cudaStream_t stream) {

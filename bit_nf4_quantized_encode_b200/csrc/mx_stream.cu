@@ -13,9 +13,7 @@
 // side arrives divided by gx gw.
 //
 // The weight's bytes bound it, so every SM has to stream all the time: the steps
-// of all row tiles, one after the other, are dealt to the SMs in equal runs.  A
-// tile that two or more runs share is joined by the CTA that completes its count:
-// partial tiles lie in the work buffer and are summed in the order of the runs.
+// of all row tiles are dealt to the SMs in equal runs (mx_runs.cuh).
 // The first stages' weight tiles are requested before the kernel that quantises
 // the activations has ended.
 #include <cuda.h>
@@ -27,6 +25,7 @@
 
 #include "mx.h"
 #include "mx_ptx.cuh"
+#include "mx_runs.cuh"
 
 namespace qlora {
 namespace {
@@ -45,36 +44,6 @@ __host__ __device__ constexpr uint32_t stream_cols(int fmt, int bn) {
   uint32_t c = 32;
   while (static_cast<int>(c) < need) c *= 2;
   return c;
-}
-
-// Sums n partial columns sets (the first at `part`, the second `skip` floats on,
-// then `next` apart), kT tokens and kC parts at a time, in order, and hands on
-// each token's sum.
-template <int kT, int kC, typename F>
-__device__ __forceinline__ void join(const float* part, int64_t skip, int64_t next, int n, int m, const F& store) {
-  const float* rest = part + skip - next;              // part c >= 1 is at rest + c * next
-#pragma unroll 1
-  for (int t0 = 0; t0 < m; t0 += kT) {
-    float sum[kT];
-#pragma unroll
-    for (int i = 0; i < kT; ++i) sum[i] = 0.0f;
-#pragma unroll 1
-    for (int c0 = 0; c0 < n; c0 += kC) {
-      float v[kC][kT];
-#pragma unroll
-      for (int c = 0; c < kC; ++c)
-#pragma unroll
-        for (int i = 0; i < kT; ++i)
-          v[c][i] = c0 + c < n && t0 + i < m ? __ldcg((c0 + c == 0 ? part : rest + (c0 + c) * next) + (t0 + i) * 128) : 0.0f;
-#pragma unroll
-      for (int c = 0; c < kC; ++c)
-#pragma unroll
-        for (int i = 0; i < kT; ++i) sum[i] += v[c][i];
-    }
-#pragma unroll
-    for (int i = 0; i < kT; ++i)
-      if (t0 + i < m) store(t0 + i, sum[i]);
-  }
 }
 
 template <int kFmt, int kBN>
@@ -100,7 +69,9 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
   const int lane = threadIdx.x & 31;
   const int per_tile = a.ksteps + a.lora_steps;
   const int64_t total = static_cast<int64_t>(a.m_tiles) * per_tile;
-  const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+  const int runs = static_cast<int>(gridDim.x);
+  const int64_t begin = run_begin(total, static_cast<int>(blockIdx.x), runs);
+  const int64_t end = run_begin(total, static_cast<int>(blockIdx.x) + 1, runs);
   const int tile0 = static_cast<int>(begin / per_tile), step0 = static_cast<int>(begin - static_cast<int64_t>(tile0) * per_tile);
   const int nsteps = static_cast<int>(end - begin);
 
@@ -277,7 +248,7 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
       };
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ab * kBN;
       const bool whole = steps == per_tile;
-      float* mine = a.slots + (static_cast<int64_t>(blockIdx.x) * 2 + (tile == tile0 ? 0 : 1)) * slot_floats + rl;
+      float* mine = my_slot(a.slots, slot_floats, tile == tile0) + rl;
 #pragma unroll 1
       for (int cc = 0; cc * kChunk < m; ++cc) {
         uint32_t v[kChunk];
@@ -296,29 +267,9 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
       tc_fence_before();
       mbar_arrive(&acc_empty[ab]);
       if (whole) continue;
-      // the runs that share the tile: c0 .. c1.  Each warp counts its own 32 rows,
-      // so no warp waits for another.
-      const int64_t s0 = static_cast<int64_t>(tile) * per_tile, s1 = s0 + per_tile - 1;
-      const int c0 = static_cast<int>(((s0 + 1) * gridDim.x - 1) / total);
-      const int n = static_cast<int>(((s1 + 1) * gridDim.x - 1) / total) - c0 + 1;
-      __threadfence();
-      __syncwarp();
-      uint32_t before = 0;
-      if (lane == 0) before = atomicAdd(a.counters + tile * 4 + quarter, 1u);
-      if (__shfl_sync(0xFFFFFFFFu, before, 0) != static_cast<uint32_t>(n - 1)) continue;
-      __threadfence();
-      // run c0 may have begun in an earlier tile: this one is its last then
-      const int which0 = total * c0 / gridDim.x < s0 ? 1 : 0;
-      const float* part = a.slots + (static_cast<int64_t>(c0) * 2 + which0) * slot_floats + rl;
-      const int64_t skip = (2 - which0) * slot_floats, next = 2 * slot_floats;
-      // several parts are read at once, and added in the order of the runs
-      if (m <= 2) {
-        join<2, 16>(part, skip, next, n, m, store);
-      } else if (m <= 8) {
-        join<8, 4>(part, skip, next, n, m, store);
-      } else {
-        join<16, 2>(part, skip, next, n, m, store);
-      }
+      // each warp counts its own 32 rows, so no warp waits for another
+      const Parts p = parts_of(a.slots + rl, slot_floats, total, static_cast<int64_t>(tile) * per_tile, per_tile, runs);
+      if (count_part(a.counters + tile * 4 + quarter, p.n)) join_columns(p, m, store);
     }
   }
 

@@ -348,12 +348,12 @@ QLORA_EXPORT qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const u
  *   logits[t] = X[t] router^T (fp32); the top_k largest of a token are chosen,
  *   the lowest index first among equal ones; p[t] = softmax of their logits;
  *   [g; u] = deq(W13_e) deq(q(X[t])),  h = g / (1 + exp(-g)) * u,
- *   Y[t] = sum_j p[t, j] deq(W2_e) deq(q(h)),  e = ids[t, j], in the order of j.
+ *   Y[t] = sum_j p[t, j] deq(W2_e) deq(q(h)),  e = ids[t, j].
  * W13 stacks the experts' [2 inner, hidden] (gate rows, then up rows), W2 their
  * [hidden, inner]; router [experts, hidden] bf16, X, Y [M, hidden] bf16;
  * ids [M, top_k] and probs [M, top_k] receive the routing.  q is the MXFP4
  * quantiser.  The weights of an expert no token chose are not read.
- * Requirements: 1 <= M <= 16, 1 <= top_k <= min(16, experts), experts <= 1024,
+ * Requirements: 1 <= M <= 16, 1 <= top_k <= min(16, experts), experts <= 256,
  * hidden and inner multiples of 128 (at most 2^20), both weights QLORA_MXFP4.
  * Bit-reproducible from run to run on the same device.  The work buffer is as
  * for qlora_mx_linear_fwd.

@@ -414,7 +414,7 @@ def moe_reference(qb, q13, q2, router, x, top_k):
 
 @pytest.mark.parametrize("experts,hidden,inner,m,top_k", [
     (1, 128, 128, 1, 1), (4, 256, 128, 1, 2), (8, 384, 256, 16, 8), (16, 512, 384, 5, 3), (64, 1024, 128, 16, 6),
-    (33, 640, 128, 9, 16), (300, 256, 128, 16, 10), (5, 128, 1152, 3, 1), (2, 2048, 640, 16, 2)])
+    (33, 640, 128, 9, 16), (250, 256, 128, 16, 10), (5, 128, 1152, 3, 1), (2, 2048, 640, 16, 2)])
 def test_moe(qb, experts, hidden, inner, m, top_k):
     q13, q2, router, x = moe_case(qb, experts, hidden, inner, m, experts + m)
     ids, p, y, off = moe_reference(qb, q13, q2, router, x, top_k)

@@ -143,5 +143,5 @@ def test_moe_refusals():
         assert f(*args(**kw)) == ERR_SHAPE, kw
     assert f(*args(a=_t(1024, 256, 1))) == ERR_UNSUP
     assert f(*args(n=64)) == ERR_WS
-    assert size(1025, 256, 128, 1, 1, None) == ERR_SHAPE and size(32, 256, 128, 1, 17, None) == ERR_SHAPE
+    assert size(257, 256, 128, 1, 1, None) == ERR_SHAPE and size(32, 256, 128, 1, 17, None) == ERR_SHAPE
     assert size(4, 256, 128, 16, 4, None) == OK
