@@ -105,10 +105,10 @@ struct MxFewArgs {
 };
 // Every CTA reads the tokens (2 bytes an element, from L2) and keeps them: limits
 // of their number and of their shared memory.
-constexpr int64_t kMxFewElements = 65536;
+constexpr int64_t kMxFewElements = 16384;
 constexpr size_t kMxFewShared = 132 * 1024;
-// Token tile (8 or 16), or 0 where the tokens are too many.
-int mx_few_tile(int fmt, int64_t m, int64_t k, int lora_steps);
+// Token tile (8 or 16), or 0 where the tokens are too many or mx_stream.cu is faster.
+int mx_few_tile(int fmt, int64_t rows, int64_t m, int64_t k, int lora_steps, int num_sms);
 // Maps: w codes box {128, 32}; lora_w [rows, r] box {64, 32}; lora_x box {64, token_tile}.
 cudaError_t launch_mx_few(int fmt, int token_tile, const MxFewArgs& a, const MxMaps& m, int num_sms, cudaStream_t stream);
 

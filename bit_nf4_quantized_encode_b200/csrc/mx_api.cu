@@ -378,7 +378,7 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, in
   if ((st = device_info(&d)) != QLORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const int few = mx_few_tile(W->format, M, W->cols, r ? sh.lora_steps : 0);
+  const int few = mx_few_tile(W->format, W->rows, M, W->cols, r ? sh.lora_steps : 0, d.num_sms);
   if (!few && quantize_acts(W, X, M, ws, L.product, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
   const uint16_t* sxa = nullptr;
   if (r) {

@@ -229,7 +229,7 @@ __host__ __device__ constexpr int moe_tiles(bool up) { return up ? 2 : 1; }
 __host__ __device__ constexpr int moe_stage(bool up) {
   return moe_tiles(up) * (kTile + kAtoms * 512) + kSlots * 128 + kAtoms * 512;
 }
-__host__ __device__ constexpr int moe_stages(bool up) { return up ? 5 : 10; }
+__host__ __device__ constexpr int moe_stages(bool up) { return up ? 6 : 10; }
 __host__ __device__ constexpr size_t moe_smem(bool up) {
   return 1024 + static_cast<size_t>(moe_stages(up)) * moe_stage(up) + 256;
 }

@@ -31,10 +31,15 @@ namespace qlora {
 namespace {
 
 constexpr int kThreads = 6 * 32;            // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
-constexpr int kABytes = 128 * 128;          // 128 rows x 256 codes
+constexpr int kABytes = 128 * 128;          // 128 rows x 256 codes (or 64 ranks)
+// A step is two pieces of 256 of the contraction (of 64 ranks), one stage: issuing
+// the waits, the election and the commit of a stage costs 270 of the 650 cycles
+// that a piece takes, and 512 make the weight rows runs of 256 bytes.
+constexpr int kSub = 2;
 
 __host__ __device__ constexpr int atoms_of(int fmt) { return fmt == kMxFp4 ? 2 : 4; }
-__host__ __device__ constexpr int stream_stage(int fmt, int bn) { return kABytes + bn * 128 + 2 * atoms_of(fmt) * 512; }
+__host__ __device__ constexpr int piece_bytes(int fmt, int bn) { return kABytes + bn * 128 + 2 * atoms_of(fmt) * 512; }
+__host__ __device__ constexpr int stream_stage(int fmt, int bn) { return kSub * piece_bytes(fmt, bn); }
 __host__ __device__ constexpr int stream_stages(int fmt, int bn) { return (224 * 1024 - 2048) / stream_stage(fmt, bn); }
 __host__ __device__ constexpr size_t stream_smem(int fmt, int bn) {
   return 1024 + static_cast<size_t>(stream_stages(fmt, bn)) * stream_stage(fmt, bn) + 512;
@@ -51,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
             const __grid_constant__ CUtensorMap lwmap, const __grid_constant__ CUtensorMap lxmap) {
   constexpr int kStages = stream_stages(kFmt, kBN);
-  constexpr int kStageBytes = stream_stage(kFmt, kBN);
+  constexpr int kStageBytes = stream_stage(kFmt, kBN), kPiece = piece_bytes(kFmt, kBN);
   constexpr int kAtoms = atoms_of(kFmt);
   constexpr uint32_t kCols = stream_cols(kFmt, kBN);
   constexpr uint32_t kSfa = 2 * kBN, kSfb = kSfa + 4 * kAtoms;      // TMEM columns of the scales
@@ -67,7 +72,8 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
 
   const int warp = warp_index();
   const int lane = threadIdx.x & 31;
-  const int per_tile = a.ksteps + a.lora_steps;
+  // steps of a tile: ksteps of 512, then the rank-r ones
+  const int ksteps = (a.ksteps + kSub - 1) / kSub, per_tile = ksteps + (a.lora_steps + kSub - 1) / kSub;
   const int64_t total = static_cast<int64_t>(a.m_tiles) * per_tile;
   const int runs = static_cast<int>(gridDim.x);
   const int64_t begin = run_begin(total, static_cast<int>(blockIdx.x), runs);
@@ -105,31 +111,51 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
     // weight side of step (tile, j) into a stage, with the stage's byte count
     auto load_w = [&](int stage, int tile, int j) {
       uint8_t* sA = smem_gen + stage * kStageBytes;
-      if (j < a.ksteps) {
-        const uint32_t sbytes = static_cast<uint32_t>(min(kAtoms, static_cast<int>(a.kt) - j * kAtoms) * 512);
-        mbar_arrive_expect_tx(&full[stage], kABytes + kBN * 128 + 2 * sbytes);
-        tma_load_2d(sA, &wmap, j * 128, tile * 128, &full[stage]);
-        bulk_load(sA + kABytes + kBN * 128, a.w_scales + (static_cast<int64_t>(tile) * a.kt + j * kAtoms) * 512, sbytes,
-                  &full[stage]);
+      if (j < ksteps) {
+        const int pieces = min(kSub, a.ksteps - j * kSub);
+        const int atoms = min(kSub * kAtoms, static_cast<int>(a.kt) - j * (kSub * kAtoms));      // of all pieces
+        mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(pieces * (kABytes + kBN * 128) + 2 * atoms * 512));
+#pragma unroll
+        for (int p = 0; p < kSub; ++p)
+          if (p < pieces) {
+            tma_load_2d(sA + p * kPiece, &wmap, (j * kSub + p) * 128, tile * 128, &full[stage]);
+            bulk_load(sA + p * kPiece + kABytes + kBN * 128,
+                      a.w_scales + (static_cast<int64_t>(tile) * a.kt + (j * kSub + p) * kAtoms) * 512,
+                      static_cast<uint32_t>(min(kAtoms, atoms - p * kAtoms) * 512), &full[stage]);
+          }
       } else {
-        const int r0 = (j - a.ksteps) * 64;
-        mbar_arrive_expect_tx(&full[stage], kABytes + kBN * 128);
-        if (a.lora_mn) {
-          tma_load_2d(sA, &lwmap, tile * 128, r0, &full[stage]);
-          tma_load_2d(sA + 8192, &lwmap, tile * 128 + 64, r0, &full[stage]);
-        } else {
-          tma_load_2d(sA, &lwmap, r0, tile * 128, &full[stage]);
-        }
+        const int r0 = (j - ksteps) * kSub, pieces = min(kSub, a.lora_steps - r0);
+        mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(pieces * (kABytes + kBN * 128)));
+#pragma unroll
+        for (int p = 0; p < kSub; ++p)
+          if (p < pieces) {
+            if (a.lora_mn) {
+              tma_load_2d(sA + p * kPiece, &lwmap, tile * 128, (r0 + p) * 64, &full[stage]);
+              tma_load_2d(sA + p * kPiece + 8192, &lwmap, tile * 128 + 64, (r0 + p) * 64, &full[stage]);
+            } else {
+              tma_load_2d(sA + p * kPiece, &lwmap, (r0 + p) * 64, tile * 128, &full[stage]);
+            }
+          }
       }
     };
     auto load_x = [&](int stage, int j) {
       uint8_t* sB = smem_gen + stage * kStageBytes + kABytes;
-      if (j < a.ksteps) {
-        const uint32_t sbytes = static_cast<uint32_t>(min(kAtoms, static_cast<int>(a.kt) - j * kAtoms) * 512);
-        tma_load_2d(sB, &xmap, j * 128, 0, &full[stage]);
-        bulk_load(sB + kBN * 128 + kAtoms * 512, a.x_scales + static_cast<int64_t>(j) * (kAtoms * 512), sbytes, &full[stage]);
+      if (j < ksteps) {
+        const int pieces = min(kSub, a.ksteps - j * kSub);
+        const int atoms = min(kSub * kAtoms, static_cast<int>(a.kt) - j * (kSub * kAtoms));
+#pragma unroll
+        for (int p = 0; p < kSub; ++p)
+          if (p < pieces) {
+            tma_load_2d(sB + p * kPiece, &xmap, (j * kSub + p) * 128, 0, &full[stage]);
+            bulk_load(sB + p * kPiece + kBN * 128 + kAtoms * 512,
+                      a.x_scales + static_cast<int64_t>(j * kSub + p) * (kAtoms * 512),
+                      static_cast<uint32_t>(min(kAtoms, atoms - p * kAtoms) * 512), &full[stage]);
+          }
       } else {
-        tma_load_2d(sB, &lxmap, (j - a.ksteps) * 64, 0, &full[stage]);
+        const int r0 = (j - ksteps) * kSub, pieces = min(kSub, a.lora_steps - r0);
+#pragma unroll
+        for (int p = 0; p < kSub; ++p)
+          if (p < pieces) tma_load_2d(sB + p * kPiece, &lxmap, (r0 + p) * 64, 0, &full[stage]);
       }
     };
     const int early = min(kStages, nsteps);
@@ -147,25 +173,16 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
       __syncwarp();
       if (++jx == per_tile) jx = 0;
     }
-    // two stages at a time, so that a weight row is asked for 256 bytes in a row
     uint32_t stage = early == kStages ? 0 : early, phase = early == kStages ? 1 : 0;
-    for (int i = early; i < nsteps; i += 2) {
-      const bool two = i + 1 < nsteps;
-      const uint32_t stage2 = stage + 1 == kStages ? 0 : stage + 1, phase2 = stage2 == 0 ? phase ^ 1u : phase;
+    for (int i = early; i < nsteps; ++i) {
       if (!mbar_wait_warp(&empty[stage], phase ^ 1u, a.err)) break;
-      if (two && !mbar_wait_warp(&empty[stage2], phase2 ^ 1u, a.err)) break;
-      const int j2 = j + 1 == per_tile ? 0 : j + 1, tile2 = j2 == 0 ? tile + 1 : tile;
       if (elect_one()) {
         load_w(static_cast<int>(stage), tile, j);
-        if (two) load_w(static_cast<int>(stage2), tile2, j2);
         load_x(static_cast<int>(stage), j);
-        if (two) load_x(static_cast<int>(stage2), j2);
       }
       __syncwarp();
-      j = j2 + 1 == per_tile ? 0 : j2 + 1;
-      tile = j == 0 ? tile2 + 1 : tile2;
-      stage = stage2 + 1 == kStages ? 0 : stage2 + 1;
-      phase = stage == 0 ? phase2 ^ 1u : phase2;
+      if (++j == per_tile) { j = 0; ++tile; }
+      if (++stage == kStages) { stage = 0; phase ^= 1u; }
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
@@ -185,33 +202,45 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
       const uint64_t ad = desc0 + off, bd = ad + (kABytes >> 4);
       const bool last = j == per_tile - 1 || i == nsteps - 1;        // of this run's part of the tile
       if (elect_one()) {
-        if (j < a.ksteps) {
-          const uint64_t sa = sdesc0 + off + ((kABytes + kBN * 128) >> 4), sb = sa + (kAtoms * 512 >> 4);
-          const int atoms = min(kAtoms, static_cast<int>(a.kt) - j * kAtoms);
+        if (j < ksteps) {
+          const int pieces = min(kSub, a.ksteps - j * kSub);
+          const int atoms = min(kSub * kAtoms, static_cast<int>(a.kt) - j * (kSub * kAtoms));
+          const int slices = static_cast<int>(min(static_cast<int64_t>(4 * kSub), (a.k - static_cast<int64_t>(j) * (256 * kSub) + 63) / 64));
 #pragma unroll
-          for (int t = 0; t < kAtoms; ++t)
-            if (t < atoms) {
-              tmem_cp_scales(tmem + kSfa + 4 * t, sa + t * 32);
-              tmem_cp_scales(tmem + kSfb + 4 * t, sb + t * 32);
-            }
-          const int slices = static_cast<int>(min(static_cast<int64_t>(4), (a.k - static_cast<int64_t>(j) * 256 + 63) / 64));
+          for (int p = 0; p < kSub; ++p)
+            if (p < pieces) {
+              const uint64_t sa = sdesc0 + off + ((p * kPiece + kABytes + kBN * 128) >> 4), sb = sa + (kAtoms * 512 >> 4);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (q < slices) {
-              const uint32_t acc = !fresh || q != 0 ? 1u : 0u;
-              if (kFmt == kMxFp4)
-                mma_mxf4_ss(d, ad + q * 2, bd + q * 2, idesc_mxf4(128, kBN, true, 2u * (q & 1)), tmem + kSfa + 4 * (q >> 1),
-                            tmem + kSfb + 4 * (q >> 1), acc);
-              else
-                mma_nvf4_ss(d, ad + q * 2, bd + q * 2, idesc_mxf4(128, kBN, false, 0), tmem + kSfa + 4 * q,
-                            tmem + kSfb + 4 * q, acc);
+              for (int t = 0; t < kAtoms; ++t)
+                if (p * kAtoms + t < atoms) {
+                  tmem_cp_scales(tmem + kSfa + 4 * t, sa + t * 32);
+                  tmem_cp_scales(tmem + kSfb + 4 * t, sb + t * 32);
+                }
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                if (p * 4 + q < slices) {
+                  const uint32_t acc = !fresh || p + q != 0 ? 1u : 0u;
+                  const uint64_t x = ad + (p * kPiece >> 4) + q * 2, y = bd + (p * kPiece >> 4) + q * 2;
+                  if (kFmt == kMxFp4)
+                    mma_mxf4_ss(d, x, y, idesc_mxf4(128, kBN, true, 2u * (q & 1)), tmem + kSfa + 4 * (q >> 1),
+                                tmem + kSfb + 4 * (q >> 1), acc);
+                  else
+                    mma_nvf4_ss(d, x, y, idesc_mxf4(128, kBN, false, 0), tmem + kSfa + 4 * q, tmem + kSfb + 4 * q, acc);
+                }
             }
         } else {
           // A K = 16 slice: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
           const uint64_t la = a.lora_mn ? smem_desc_sw128(smem0, 8192, 1024) + off : ad;
           const uint32_t step = a.lora_mn ? 2048 >> 4 : 32 >> 4;
+          const int pieces = min(kSub, a.lora_steps - (j - ksteps) * kSub);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) mma_bf16_ss(d, la + q * step, bd + q * 2, lora_idesc, !fresh || q != 0 ? 1u : 0u);
+          for (int p = 0; p < kSub; ++p)
+            if (p < pieces) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                mma_bf16_ss(d, la + (p * kPiece >> 4) + q * step, bd + (p * kPiece >> 4) + q * 2, lora_idesc,
+                            !fresh || p + q != 0 ? 1u : 0u);
+            }
         }
         mma_commit(&empty[stage]);
         if (last) mma_commit(&acc_full[ab]);
@@ -295,10 +324,10 @@ cudaError_t launch_t(const MxGemmArgs& a, const MxMaps& m, int num_sms, cudaStre
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  const int64_t steps = static_cast<int64_t>(a.m_tiles) * (a.ksteps + a.lora_steps);
+  const int64_t steps =
+      static_cast<int64_t>(a.m_tiles) * ((a.ksteps + kSub - 1) / kSub + (a.lora_steps + kSub - 1) / kSub);
   int grid = num_sms < kMxMaxRuns ? num_sms : kMxMaxRuns;
-  // a run of fewer than two steps would save less than joining one more part costs
-  if ((steps + 1) / 2 < grid) grid = static_cast<int>((steps + 1) / 2);
+  if (steps < grid) grid = static_cast<int>(steps);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kThreads);
