@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_quant(const MxQuantArgs a) {
 
 // NVFP4 with a global scale per row: one CTA per row.  The first
 // kRowThreads * 32 * kHeld elements stay in registers between the row's maximum
-// and its codes; the rest of a longer row is read again (from L2).
+// and its codes; the rest of the row is read again (from L2).
 template <bool kVec, int kRowThreads, int kHeld>
 __global__ void __launch_bounds__(kRowThreads) k_mx_quant_rows(const MxQuantArgs a) {
   open_dependents(a);
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kRowThreads) k_mx_quant_rows(const MxQuantArgs
   const uint16_t* src = a.in + row * a.cols;
   const int64_t span = a.kt * 64;
   const int64_t c0 = threadIdx.x * 32, w0 = (threadIdx.x & ~31) * 32;
-  Elems32 held[kHeld];
+  Elems32 held[kHeld > 0 ? kHeld : 1];
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
@@ -164,8 +164,13 @@ __global__ void __launch_bounds__(kRowThreads) k_mx_quant_rows(const MxQuantArgs
 #pragma unroll
     for (int i = 0; i < 4; ++i) m = max(m, finite_mag8(held[j].q[i]));
   if (row < a.rows)
-    for (int64_t c = kHeld * kStep + threadIdx.x * 8; c < a.cols; c += kRowThreads * 8)
-      m = max(m, finite_mag8(load8<kVec>(src, c, a.cols)));
+    for (int64_t c = kHeld * kStep + threadIdx.x * 8; c < a.cols; c += 8 * kRowThreads * 8) {
+      uint4 q[8];                            // eight loads in flight (zero past the row)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = load8<kVec>(src, c + j * kRowThreads * 8, a.cols);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, finite_mag8(q[j]));
+    }
   m = __reduce_max_sync(0xFFFFFFFFu, m);
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
@@ -331,9 +336,13 @@ cudaError_t quant_t(bool transpose, const MxQuantArgs& a, int num_sms, cudaStrea
     const int64_t units = (a.kt * 4 * mx_block(kFmt) + kTileN - 1) / kTileN * ((a.tile_rows + kTileK - 1) / kTileK);
     k_mx_quant_t<kFmt, kVec><<<grid_of(units, num_sms, 8), kThreads, 0, stream>>>(a);
   } else if (kFmt == kNvFp4 && a.per_row) {
-    // registers for the whole row where that is possible
+    // Many rows: small CTAs that read a long row twice, the second time from L2, so
+    // that an SM has several rows in all phases at once (8192 rows of 22016: 119 us;
+    // held in the registers of 1024 threads 208 us).  Few rows: as many threads as
+    // hold the row (16 rows of 22016: 4.7 us; the small CTAs 9 us).
     const unsigned grid = static_cast<unsigned>(a.tile_rows);
     if (a.cols <= 4096) k_mx_quant_rows<kVec, 128, 1><<<grid, 128, 0, stream>>>(a);
+    else if (a.tile_rows >= 4 * static_cast<int64_t>(num_sms)) k_mx_quant_rows<kVec, 128, 0><<<grid, 128, 0, stream>>>(a);
     else if (a.cols <= 8192) k_mx_quant_rows<kVec, 256, 1><<<grid, 256, 0, stream>>>(a);
     else if (a.cols <= 16384) k_mx_quant_rows<kVec, 512, 1><<<grid, 512, 0, stream>>>(a);
     else k_mx_quant_rows<kVec, 1024, 1><<<grid, 1024, 0, stream>>>(a);
