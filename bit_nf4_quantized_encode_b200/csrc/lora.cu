@@ -200,14 +200,21 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
     if (lane == 0) {
       uint32_t it = 0, uctr = 0;
       bool alive = true;
-      for (int u = blockIdx.x; u < nunits && alive; u += gridDim.x, ++uctr) {
+      // uctr counts accumulator fillings: one per unit, or one per `flush` k-steps
+      for (int u = blockIdx.x; u < nunits && alive; u += gridDim.x) {
         const UnitPos w = unit_pos(a, u);
         const RankProblem& p = a.p[w.prob];
         const uint32_t idesc = idesc_bf16(128, 64, p.a_mn != 0, p.b_mn != 0);
-        const uint32_t ab = uctr & 1u, aphase = (uctr >> 1) & 1u;
-        if (!mbar_wait(&acc_empty[ab], aphase ^ 1u, a.err)) break;
-        tc_fence_after();
+        const int piece = p.flush > 0 ? p.flush : w.nk;
+        int left = 0;                          // k-steps to go of this filling
         for (int j = 0; j < w.nk; ++j, ++it) {
+          const uint32_t ab = uctr & 1u, aphase = (uctr >> 1) & 1u;
+          const bool fresh = left == 0;
+          if (fresh) {
+            left = w.nk - j < piece ? w.nk - j : piece;
+            if (!mbar_wait(&acc_empty[ab], aphase ^ 1u, a.err)) { alive = false; break; }
+            tc_fence_after();
+          }
           const uint32_t stage = it % kStages, phase = (it / kStages) & 1u;
           if (!mbar_wait(&full[stage], phase, a.err)) { alive = false; break; }
           tc_fence_after();
@@ -219,11 +226,14 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
                                           : smem_desc_sw128(sA + kk * 32, 16, 1024);
             const uint64_t bdesc = p.b_mn ? smem_desc_sw128(sB + kk * 2048, 8192, 1024)
                                           : smem_desc_sw128(sB + kk * 32, 16, 1024);
-            mma_bf16_ss(tmem_base + ab * 64, adesc, bdesc, idesc, (j | kk) != 0 ? 1u : 0u);
+            mma_bf16_ss(tmem_base + ab * 64, adesc, bdesc, idesc, !fresh || kk != 0 ? 1u : 0u);
           }
           mma_commit(&empty[stage]);
+          if (--left == 0) {
+            mma_commit(&acc_full[ab]);
+            ++uctr;
+          }
         }
-        if (alive) mma_commit(&acc_full[ab]);
       }
     }
   } else {
@@ -238,29 +248,32 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
       ephase ^= 1u;
       return ok;
     };
-    for (int u = blockIdx.x; u < nunits; u += gridDim.x, ++uctr) {
+    bool alive = true;
+    for (int u = blockIdx.x; u < nunits; u += gridDim.x) {
       const UnitPos w = unit_pos(a, u);
       const RankProblem& p = a.p[w.prob];
-      const uint32_t ab = uctr & 1u, aphase = (uctr >> 1) & 1u;
-      if (!mbar_wait(&acc_full[ab], aphase, a.err)) break;
-      tc_fence_after();
       const int rl = quarter * 32 + lane;                   // row inside the tile
       const int64_t row = static_cast<int64_t>(w.mt) * 128 + rl;
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + ab * 64;
+      const int fills = p.flush > 0 ? (w.nk + p.flush - 1) / p.flush : 1;
       float v[64];
-      {
+      for (int f = 0; f < fills; ++f, ++uctr) {
+        const uint32_t ab = uctr & 1u, aphase = (uctr >> 1) & 1u;
+        if (!mbar_wait(&acc_full[ab], aphase, a.err)) { alive = false; break; }
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + ab * 64;
         uint32_t r0[32], r1[32];
         tmem_ld32(taddr, r0);
         tmem_ld32(taddr + 32, r1);
         tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(&acc_empty[ab]);                         // TMEM free for the next filling
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-          v[c] = __uint_as_float(r0[c]);
-          v[32 + c] = __uint_as_float(r1[c]);
+          v[c] = f == 0 ? __uint_as_float(r0[c]) : v[c] + __uint_as_float(r0[c]);
+          v[32 + c] = f == 0 ? __uint_as_float(r1[c]) : v[32 + c] + __uint_as_float(r1[c]);
         }
       }
-      tc_fence_before();
-      mbar_arrive(&acc_empty[ab]);                           // TMEM free for the next unit
+      if (!alive) break;
       const int64_t c0 = static_cast<int64_t>(w.nt) * 64;
       if (p.splits == 1) {
         store_final(p, row, c0, v);

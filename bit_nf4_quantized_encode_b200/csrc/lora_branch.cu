@@ -128,7 +128,7 @@ BwdLayout bwd_layout(const LinearShape& s) {
 }
 
 qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_t* A, float s, float* XA_out, uint8_t* ws,
-                         const XaLayout& L, const RankDivide& div, const DeviceInfo& d, cudaStream_t cs) {
+                         const XaLayout& L, const RankDivide& div, int flush, const DeviceInfo& d, cudaStream_t cs) {
   RankPlan xp = rank_tiling(sh.m, sh.cols, sh.lora_steps);
   xp.splits = launch_splits(xp.tiles(), xp.ksteps, d.num_sms, L.slot_bytes);
   if (!slots_fit(xp.tiles(), xp.splits, L.slot_bytes)) return QLORA_ERR_WORKSPACE;
@@ -139,6 +139,7 @@ qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_
   RankArgs ra{};
   ra.p[0] = rank_problem(xp, sh.m, sh.r, false, false, 0, reinterpret_cast<float*>(ws + L.slots),
                          reinterpret_cast<uint32_t*>(ws + L.cnt));
+  ra.p[0].flush = flush;
   ra.p[0].out_f32 = XA_out; ra.p[0].ld_f32 = sh.r;
   ra.p[0].ld_bf16 = sh.rpad; ra.p[0].bf16_cols = sh.rpad; ra.p[0].bf16_scale = s;
   uint16_t* sxa = reinterpret_cast<uint16_t*>(ws + L.sxa);

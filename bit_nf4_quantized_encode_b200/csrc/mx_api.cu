@@ -390,7 +390,7 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, in
         div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
         div.all = all_div;
       }
-      if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, div, d, cs)) != QLORA_OK) return st;
+      if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, div, 8, d, cs)) != QLORA_OK) return st;
     } else {
       MxXaArgs xa{};
       xa.x = X;
