@@ -311,9 +311,12 @@ k_moe_product(const MxMoeArgs a, const __grid_constant__ CUtensorMap wmap, const
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n_used = *a.n_used;
   const int per_tile = kUp ? ksteps : ksteps * n_used;
-  const int64_t total = static_cast<int64_t>(kUp ? n_used * row_tiles : row_tiles) * per_tile;
-  // the grid is for the most experts that can be in use; no run is empty
-  const int runs = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + 1) / 2));
+  const int tiles = kUp ? n_used * row_tiles : row_tiles;
+  const int64_t total = static_cast<int64_t>(tiles) * per_tile;
+  // The grid is for the most experts that can be in use; no run is empty.  With
+  // fewer tiles than CTAs every tile has the same number of runs to itself.
+  const int runs = tiles <= static_cast<int>(gridDim.x) ? tiles * max(1, min(static_cast<int>(gridDim.x) / tiles, per_tile / 2))
+                                                        : static_cast<int>(gridDim.x);
   const int run = static_cast<int>(blockIdx.x);
   const int64_t begin = run_begin(total, min(run, runs), runs);
   const int nsteps = run < runs ? static_cast<int>(run_begin(total, run + 1, runs) - begin) : 0;

@@ -18,7 +18,7 @@
 namespace qlora {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kCluster = 8;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kCluster = 8;
 
 __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) k_mx_xa(const MxXaArgs a) {
   __shared__ float part[kWarps][16][17];       // per warp, then (CTA 0) per CTA of the cluster
@@ -80,13 +80,15 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) k_m
     }
   }
   __syncthreads();
-  const int rr = threadIdx.x >> 4, tt = threadIdx.x & 15;
+  const int rr = (threadIdx.x >> 4) & 15, tt = threadIdx.x & 15;
   float v = 0.0f;
+  if (threadIdx.x < 256) {
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) v += part[w][rr][tt];
-  st_cluster_f32(cluster_map(smem_u32(&joined[rank][rr][tt]), 0), v);
+    for (int w = 0; w < kWarps; ++w) v += part[w][rr][tt];
+    st_cluster_f32(cluster_map(smem_u32(&joined[rank][rr][tt]), 0), v);
+  }
   cluster_sync();
-  if (rank != 0) return;
+  if (rank != 0 || threadIdx.x >= 256) return;
   v = 0.0f;
 #pragma unroll
   for (int c = 0; c < kCluster; ++c) v += joined[c][rr][tt];
