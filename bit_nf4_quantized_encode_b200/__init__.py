@@ -487,8 +487,10 @@ def qlora_mx_sizes(rows: int, cols: int, fmt: str = "mxfp4", per_row: bool = Fal
     return dict(codes=v[0].value, scales=v[1].value, global_scale=v[2].value, workspace=v[3].value)
 
 
-# Work-buffer bytes of an NVFP4 quantisation with one global scale, whatever the size.
-_MX_QUANT_WORKSPACE = qlora_mx_sizes(1, 1, "nvfp4")["workspace"]
+@functools.lru_cache(maxsize=4096)
+def _mx_quant_workspace(rows: int, cols: int) -> int:
+    """Work-buffer bytes of an NVFP4 quantisation with one global scale."""
+    return qlora_mx_sizes(rows, cols, "nvfp4")["workspace"]
 
 
 def qlora_mx_quantize(W: torch.Tensor, fmt: str = "mxfp4", transpose: bool = False, per_row: bool = False,
@@ -508,8 +510,8 @@ def qlora_mx_quantize(W: torch.Tensor, fmt: str = "mxfp4", transpose: bool = Fal
     if rows == 0 or cols == 0:
         return out
     c = out.c_struct()
-    if workspace is None and out.fmt == "nvfp4" and not out.scale_per_row:
-        workspace = torch.empty(_MX_QUANT_WORKSPACE, dtype=torch.uint8, device=W.device)
+    if workspace is None and out.fmt == "nvfp4" and not out.scale_per_row and _mx_quant_workspace(rows, cols):
+        workspace = torch.empty(_mx_quant_workspace(rows, cols), dtype=torch.uint8, device=W.device)
     _on(W.device, "qlora_mx_quantize", _lib.qlora_mx_quantize, W.data_ptr(), int(transpose), c, _addr(workspace),
         _size(workspace))
     return out

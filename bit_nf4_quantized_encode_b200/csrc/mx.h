@@ -27,6 +27,8 @@ inline int64_t mx_scale_bytes(int fmt, int64_t rows, int64_t cols) {
 // CTAs of the amax pass of an NVFP4 tensor quantised with one global scale
 // (one partial maximum each).
 constexpr int kMxAmaxGrid = 1184;
+// Up to this many elements every CTA of the quantiser finds the maximum itself.
+constexpr int64_t kMxSmallElements = 131072;
 
 struct MxQuantArgs {
   const uint16_t* in;        // bf16 [in_rows, in_cols], contiguous
@@ -39,7 +41,7 @@ struct MxQuantArgs {
   int64_t tile_rows;         // rows whose scale bytes are written: rows, or rows padded to 128
   int per_row;
   uint32_t* amax;            // NVFP4, one global scale: partial maxima [amax_n]
-  int amax_n;
+  int amax_n;                // 0: none, a small matrix
   uint32_t* zero;            // words cleared on the way (the counters of the next kernel)
   int zero_n;
 };

@@ -33,8 +33,11 @@ qlora_status check_mx(const qlora_mx_tensor* t) {
   return QLORA_OK;
 }
 
-size_t quantize_workspace(int format, int per_row) {
-  return format == QLORA_NVFP4 && !per_row ? round_up(kMxAmaxGrid * sizeof(uint32_t), 256) : 0;
+// (rows, cols <= 2^31: the product fits)
+size_t quantize_workspace(int format, int per_row, int64_t rows, int64_t cols) {
+  return format == QLORA_NVFP4 && !per_row && rows * cols > kMxSmallElements
+             ? round_up(kMxAmaxGrid * sizeof(uint32_t), 256)
+             : 0;
 }
 
 // ------------------------------------------------------------------ linear layer
@@ -292,7 +295,7 @@ qlora_status qlora_mx_sizes(int64_t rows, int64_t cols, int32_t format, int32_t 
   if (scales_bytes) *scales_bytes = static_cast<size_t>(mx_scale_bytes(format, rows, cols));
   if (global_scale_bytes)
     *global_scale_bytes = format == QLORA_NVFP4 ? 4 * (scale_per_row ? static_cast<size_t>(rows) : 1) : 0;
-  if (workspace_bytes) *workspace_bytes = quantize_workspace(format, scale_per_row);
+  if (workspace_bytes) *workspace_bytes = quantize_workspace(format, scale_per_row, rows, cols);
   return QLORA_OK;
 }
 
@@ -302,7 +305,7 @@ qlora_status qlora_mx_quantize(const uint16_t* W, int32_t transpose, const qlora
   if (st != QLORA_OK) return st;
   if ((transpose != 0 && transpose != 1) || (transpose && out->scale_per_row)) return QLORA_ERR_UNSUPPORTED;
   if (out->rows == 0 || out->cols == 0) return QLORA_OK;
-  const size_t need = quantize_workspace(out->format, out->scale_per_row);
+  const size_t need = quantize_workspace(out->format, out->scale_per_row, out->rows, out->cols);
   if (!W || (need && !workspace)) return QLORA_ERR_NULL;
   if (!aligned16(W) || (need && !aligned16(workspace))) return QLORA_ERR_ALIGN;
   if (workspace_bytes < need) return QLORA_ERR_WORKSPACE;

@@ -54,26 +54,9 @@ __device__ __forceinline__ void emit1024(const MxQuantArgs& a, int64_t row, int6
     *reinterpret_cast<uint32_t*>(a.scales + mx_scale_offset(row, kt * 4, a.kt)) = word;
 }
 
-// Largest of the partial maxima, in every thread.
-__device__ uint32_t reduce_amax(const uint32_t* partials, int n) {
-  __shared__ uint32_t s_max[kThreads / 32];
-  uint32_t m = 0;
-  for (int i = threadIdx.x; i < n; i += kThreads) m = max(m, __ldcg(partials + i));
-  m = __reduce_max_sync(0xFFFFFFFFu, m);
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
-  __syncthreads();
-  m = s_max[0];
-#pragma unroll
-  for (int i = 1; i < kThreads / 32; ++i) m = max(m, s_max[i]);
-  __syncthreads();
-  return m;
-}
-
-__global__ void __launch_bounds__(kThreads) k_mx_amax(const uint16_t* in, int64_t numel, uint32_t* partials) {
-  __shared__ uint32_t s_max[kThreads / 32];
+// Largest finite magnitude of elements first, first + stride, ... (8 at a time).
+__device__ __forceinline__ uint32_t scan_amax(const uint16_t* in, int64_t numel, int64_t first, int64_t stride) {
   const int64_t nvec = numel / 8;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   uint32_t m = 0;
   bool bad = false;
   constexpr int kBatch = 8;                  // loads in flight per thread
@@ -87,6 +70,32 @@ __global__ void __launch_bounds__(kThreads) k_mx_amax(const uint16_t* in, int64_
   }
   for (; i < nvec; i += stride) m = max(m, finite_mag8(__ldg(reinterpret_cast<const uint4*>(in) + i)));
   if (first < numel - nvec * 8) m = max(m, mx_finite_mag(in[nvec * 8 + first], bad));
+  return m;
+}
+
+// Largest magnitude of the whole matrix, in every thread: of the partial maxima
+// or, for a small matrix (amax_n = 0), found by every CTA for itself, which is
+// faster than a launch.
+__device__ uint32_t reduce_amax(const MxQuantArgs& a) {
+  __shared__ uint32_t s_max[kThreads / 32];
+  uint32_t m = 0;
+  if (a.amax_n == 0) m = scan_amax(a.in, a.in_rows * a.in_cols, threadIdx.x, kThreads);
+  else
+    for (int i = threadIdx.x; i < a.amax_n; i += kThreads) m = max(m, __ldcg(a.amax + i));
+  m = __reduce_max_sync(0xFFFFFFFFu, m);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = s_max[0];
+#pragma unroll
+  for (int i = 1; i < kThreads / 32; ++i) m = max(m, s_max[i]);
+  __syncthreads();
+  return m;
+}
+
+__global__ void __launch_bounds__(kThreads) k_mx_amax(const uint16_t* in, int64_t numel, uint32_t* partials) {
+  __shared__ uint32_t s_max[kThreads / 32];
+  uint32_t m = scan_amax(in, numel, static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x,
+                         static_cast<int64_t>(gridDim.x) * kThreads);
   m = __reduce_max_sync(0xFFFFFFFFu, m);
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
@@ -125,7 +134,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_quant(const MxQuantArgs a) {
   open_dependents(a);
   float inv_g = 1.0f;
   if (kFmt == kNvFp4) {
-    const float g = mx_global_scale(reduce_amax(a.amax, a.amax_n) << 16);
+    const float g = mx_global_scale(reduce_amax(a) << 16);
     inv_g = mx_pow2_inverse(g);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.global_scale[0] = g;
   }
@@ -200,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_quant_t(const MxQuantArgs a) {
   __shared__ uint32_t tile[kTileN][kTileK / 2 + 1];
   float inv_g = 1.0f;
   if (kFmt == kNvFp4) {
-    const float g = mx_global_scale(reduce_amax(a.amax, a.amax_n) << 16);
+    const float g = mx_global_scale(reduce_amax(a) << 16);
     inv_g = mx_pow2_inverse(g);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.global_scale[0] = g;
   }

@@ -279,7 +279,7 @@ typedef struct {
 /*
  * Byte sizes of the buffers of a microscaled [rows, cols] matrix (global_scale
  * is 0 bytes for QLORA_MXFP4) and of the work buffer qlora_mx_quantize needs
- * (0 but for QLORA_NVFP4 with one global scale).  Any output pointer may be NULL.
+ * (0 but for QLORA_NVFP4 with one global scale and more than 131072 elements).  Any output pointer may be NULL.
  * Errors: QLORA_ERR_SHAPE (a size < 0 or > 2^31 - 256), QLORA_ERR_UNSUPPORTED.
  */
 QLORA_EXPORT qlora_status qlora_mx_sizes(int64_t rows, int64_t cols, int32_t format, int32_t scale_per_row,

@@ -74,9 +74,11 @@ def test_quantize_refusals():
     assert f(w, 0, _t(fmt=2), ws, 1 << 20, None) == ERR_UNSUP
     assert f(w, 0, _t(per_row=1), ws, 1 << 20, None) == ERR_UNSUP
     assert f(w, 0, _t(rows=-1), ws, 1 << 20, None) == ERR_SHAPE
-    assert f(w, 0, _t(fmt=1), None, 0, None) == ERR_NULL             # one global scale needs the work buffer
-    assert f(w, 0, _t(fmt=1), ws, 64, None) == ERR_WS
-    assert f(w, 0, _t(fmt=1), ws + 4, 1 << 20, None) == ERR_ALIGN
+    big = _t(rows=1024, cols=1024, fmt=1)
+    assert f(w, 0, big, None, 0, None) == ERR_NULL                   # one global scale needs the work buffer
+    assert f(w, 0, big, ws, 64, None) == ERR_WS
+    assert f(w, 0, big, ws + 4, 1 << 20, None) == ERR_ALIGN
+    assert qb.qlora_mx_sizes(1024, 1024, "nvfp4")["workspace"] and not qb.qlora_mx_sizes(100, 1000, "nvfp4")["workspace"]
     for field in ("codes", "scales", "global_scale"):
         nul, mis = _t(fmt=1), _t(fmt=1)
         setattr(nul, field, None)
