@@ -512,3 +512,85 @@ def test_layers_in_a_row(qb):
     d2 = qb.qlora_mx_linear_bwd(qct, dy)[0]
     gv, wt = mx.round_trip(f64(dy), "mxfp4"), f64(qb.qlora_mx_dequantize(qct))
     check(d2, gv @ wt.T, product_bound(gv @ wt.T, gv, wt), "back")
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("m,r", [(1, 0), (3, 64), (16, 8), (40, 64), (64, 0), (200, 64)])
+def test_work_buffers_may_hold_anything(qb, m, r, fmt):
+    """A work buffer full of NaN patterns gives what a fresh one gives, forward and backward."""
+    rows, cols = 520, 1344
+    w, x, dy = normal((rows, cols), 0.02, 1).cuda(), normal((m, cols), 1.0, 2).cuda(), normal((m, rows), 1e-3, 3).cuda()
+    q, qt = qb.qlora_mx_quantize(w, fmt), qb.qlora_mx_quantize(w, fmt, transpose=True)
+    a, b = (normal((r, cols), 0.02, 4).cuda(), normal((rows, r), 0.02, 5).cuda()) if r else (None, None)
+    f, g = qb.qlora_mx_linear_workspace_size(rows, cols, fmt, m, r)
+    for fill in (0xFF, 0x7F):
+        ws = torch.full((max(f, g),), fill, dtype=torch.uint8, device="cuda")
+        got = qb.qlora_mx_linear_fwd(q, x, a, b, 0.25, workspace=ws)
+        want = qb.qlora_mx_linear_fwd(q, x, a, b, 0.25)
+        assert all(torch.equal(u, v) for u, v in zip(got, want) if u is not None)
+        ws.fill_(fill)
+        back = qb.qlora_mx_linear_bwd(qt, dy, x, a, b, 0.25, workspace=ws)
+        want = qb.qlora_mx_linear_bwd(qt, dy, x, a, b, 0.25)
+        if m > 16 or not r:                       # with fewer tokens dA and dB are as of qlora_linear_bwd: no split
+            assert all(torch.equal(u, v) for u, v in zip(back, want) if u is not None)
+        else:
+            assert torch.equal(back[0], want[0])
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("m", [1, 20, 150])
+def test_zeros_and_far_magnitudes(qb, m, fmt):
+    """Zero tokens give exact zeros; tokens of 2^40 and 2^-40 (and zeros between
+    them) give the result of tokens of 1, scaled."""
+    w, x = normal((300, 640), 0.02, 1).cuda(), normal((m, 640), 1.0, 2).cuda()
+    q = qb.qlora_mx_quantize(w, fmt)
+    assert (qb.qlora_mx_linear_fwd(q, torch.zeros_like(x))[0] == 0).all()
+    y = qb.qlora_mx_linear_fwd(q, x)[0]
+    for e in (40, -40):
+        assert torch.equal(qb.qlora_mx_linear_fwd(q, x * 2.0 ** e)[0], y * 2.0 ** e)
+    x[0] = 0
+    y2 = qb.qlora_mx_linear_fwd(q, x)[0]
+    assert (y2[0] == 0).all() and torch.equal(y2[1:], y[1:])
+    z = qb.qlora_mx_quantize(torch.zeros_like(w), fmt)
+    assert (qb.qlora_mx_linear_fwd(z, x)[0] == 0).all() and (qb.qlora_mx_dequantize(z) == 0).all()
+
+
+def test_offsets_past_32_bits(qb):
+    """2.4e9 weights (4.8 GB): the last rows are quantised, dequantised and
+    multiplied as they are alone."""
+    rows, cols, tail = 40000, 60000, 192          # 40000 = 312 * 128 + 64: the tail begins on a scale tile
+    w = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    w.normal_(std=0.02, generator=torch.Generator(device="cuda").manual_seed(1))
+    q, small = qb.qlora_mx_quantize(w), qb.qlora_mx_quantize(w[rows - tail:].contiguous())
+    pitch = -(-cols // 32) * 16
+    assert torch.equal(q.codes[-tail * pitch:], small.codes) and torch.equal(q.scales[-small.scales.numel():], small.scales)
+    for m in (1, 16, 50, 200):
+        x = normal((m, cols), 1.0, m).cuda()
+        assert torch.equal(qb.qlora_mx_linear_fwd(q, x)[0][:, rows - tail:], qb.qlora_mx_linear_fwd(small, x)[0])
+    assert torch.equal(qb.qlora_mx_dequantize(q)[rows - tail:], qb.qlora_mx_dequantize(small))
+    del q
+    t = qb.qlora_mx_quantize(w, transpose=True)   # rows of w are its contraction
+    last = qb.qlora_mx_quantize(w[:, cols - 96:].contiguous(), transpose=True)
+    tp = -(-rows // 32) * 16
+    assert torch.equal(t.codes[-96 * tp:], last.codes)
+
+
+def test_two_calls_at_once(qb):
+    """Calls of different kinds on two streams, each with its own work buffers, give what they give alone."""
+    w, x, big = normal((3000, 2048), 0.02, 1).cuda(), normal((5, 2048), 1.0, 2).cuda(), normal((700, 2048), 1.0, 3).cuda()
+    q = qb.qlora_mx_quantize(w, "nvfp4")
+    q13, q2, router, xe = moe_case(qb, 16, 512, 256, 9, 4)
+    jobs = [lambda: qb.qlora_mx_linear_fwd(q, x)[0], lambda: qb.qlora_mx_linear_fwd(q, big)[0],
+            lambda: qb.qlora_mx_moe_fwd(q13, q2, router, xe, 4)[0], lambda: qb.qlora_mx_quantize(big, "nvfp4").codes,
+            lambda: qb.qlora_mx_linear_fwd(q, big[:40].contiguous())[0]]
+    want = [j() for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] += [j() for j in (jobs if i == 0 else jobs[::-1])]
+    torch.cuda.synchronize()
+    for k in range(25):
+        assert torch.equal(got[0][k], want[k % 5]) and torch.equal(got[1][k], want[4 - k % 5])
