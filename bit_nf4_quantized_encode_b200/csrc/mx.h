@@ -27,7 +27,9 @@ inline int64_t mx_scale_bytes(int fmt, int64_t rows, int64_t cols) {
 // CTAs of the amax pass of an NVFP4 tensor quantised with one global scale
 // (one partial maximum each).
 constexpr int kMxAmaxGrid = 1184;
-// Up to this many elements every CTA of the quantiser finds the maximum itself.
+// Up to this many elements every CTA of the quantiser finds the maximum itself:
+// 100 x 1000 takes 6.8 us of the GPU that way and 5.8 us in two launches, but the
+// second launch and its work buffer cost the host 4 us.
 constexpr int64_t kMxSmallElements = 131072;
 
 struct MxQuantArgs {

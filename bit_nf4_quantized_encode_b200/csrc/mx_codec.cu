@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_quant(const MxQuantArgs a) {
        w.row < a.tile_rows; w.next()) {
     const int64_t row = kFmt == kNvFp4 ? a.tile_rows - 1 - w.row : w.row, c = w.seg * 1024 + lane * 32;
     Elems32 e{};
-    if (row < a.rows) e = load32<kVec>(a.in + row * a.cols, c, a.cols);
+    if (row < a.rows) e = load32<kVec>(a.in + row * a.cols, c, a.cols, (a.rows - row) * a.cols);
     emit1024<kFmt>(a, row, c, e, inv_g);
   }
 }
@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kRowThreads) k_mx_quant_rows(const MxQuantArgs
   constexpr int kStep = kRowThreads * 32;
   const int64_t row = blockIdx.x;
   const uint16_t* src = a.in + row * a.cols;
+  const int64_t limit = (a.rows - row) * a.cols;
   const int64_t span = a.kt * 64;
   const int64_t c0 = threadIdx.x * 32, w0 = (threadIdx.x & ~31) * 32;
   Elems32 held[kHeld > 0 ? kHeld : 1];
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kRowThreads) k_mx_quant_rows(const MxQuantArgs
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
     held[j] = Elems32{};
-    if (row < a.rows) held[j] = load32<kVec>(src, c0 + j * kStep, a.cols);
+    if (row < a.rows) held[j] = load32<kVec>(src, c0 + j * kStep, a.cols, limit);
   }
 #pragma unroll
   for (int j = 0; j < kHeld; ++j)
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kRowThreads) k_mx_quant_rows(const MxQuantArgs
     for (int64_t c = kHeld * kStep + threadIdx.x * 8; c < a.cols; c += 8 * kRowThreads * 8) {
       uint4 q[8];                            // eight loads in flight (zero past the row)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = load8<kVec>(src, c + j * kRowThreads * 8, a.cols);
+      for (int j = 0; j < 8; ++j) q[j] = load8<kVec>(src, c + j * kRowThreads * 8, a.cols, limit);
 #pragma unroll
       for (int j = 0; j < 8; ++j) m = max(m, finite_mag8(q[j]));
     }
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kRowThreads) k_mx_quant_rows(const MxQuantArgs
     if (w0 + j * kStep < span) emit1024<kNvFp4>(a, row, c0 + j * kStep, held[j], inv_g);
   for (int64_t b = kHeld * kStep; w0 + b < span; b += kStep) {
     Elems32 e{};
-    if (row < a.rows) e = load32<kVec>(src, c0 + b, a.cols);
+    if (row < a.rows) e = load32<kVec>(src, c0 + b, a.cols, limit);
     emit1024<kNvFp4>(a, row, c0 + b, e, inv_g);
   }
 }
@@ -221,7 +222,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_quant_t(const MxQuantArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int64_t n = n0 + (threadIdx.x >> 3) + 32 * j;
-      q[j] = n < a.in_rows ? load8<kVec>(a.in + n * a.in_cols, k0 + (threadIdx.x & 7) * 8, a.in_cols)
+      q[j] = n < a.in_rows ? load8<kVec>(a.in + n * a.in_cols, k0 + (threadIdx.x & 7) * 8, a.in_cols,
+                                           (a.in_rows - n) * a.in_cols)
                            : make_uint4(0, 0, 0, 0);
     }
     __syncthreads();                       // the tile's readers of the unit before are done
@@ -290,6 +292,7 @@ template <int kFmt, bool kVec>
 __global__ void __launch_bounds__(kThreads)
 k_mx_dequant(const uint8_t* codes, const uint8_t* scales, const float* gs, int per_row, int64_t rows, int64_t cols,
              int64_t pitch, int64_t kt, uint16_t* out) {
+  __shared__ uint4 s_out[kThreads];          // a warp's 256 values on their way to a row that starts anywhere
   const int lane = threadIdx.x & 31;
   const float g0 = (kFmt == kNvFp4 && !per_row) ? __ldg(gs) : 1.0f;
   for (Walk w(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5),
@@ -310,7 +313,7 @@ k_mx_dequant(const uint8_t* codes, const uint8_t* scales, const float* gs, int p
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t c = c0 + j * 256;
-      if (c >= cols) continue;
+      if (kVec && c >= cols) continue;
       const float s = kFmt == kMxFp4 ? mx_e8m0_value(sb[j]) : e4m3_to_f32(sb[j]);
       uint32_t h[4], o[4];
       mx_levels8(word[j], h);
@@ -322,13 +325,19 @@ k_mx_dequant(const uint8_t* codes, const uint8_t* scales, const float* gs, int p
         const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
         o[i] = *reinterpret_cast<const uint32_t*>(&p);
       }
-      uint16_t* dst = out + w.row * cols + c;
       if constexpr (kVec) {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(out + w.row * cols + c) = make_uint4(o[0], o[1], o[2], o[3]);
       } else {
+        // 32 neighbouring values a store
+        uint4* mine = s_out + (threadIdx.x & ~31);
+        __syncwarp();
+        mine[lane] = make_uint4(o[0], o[1], o[2], o[3]);
+        __syncwarp();
+        const int64_t first = w.seg * 1024 + j * 256;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (c + i < cols) dst[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+          if (first + i * 32 + lane < cols)
+            out[w.row * cols + first + i * 32 + lane] = reinterpret_cast<const uint16_t*>(mine)[i * 32 + lane];
       }
     }
   }

@@ -12,16 +12,66 @@
 
 namespace qlora {
 
-// Eight consecutive elements of a row, from column c (zero past cols).
-template <bool kVec>
-__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t cols) {
-  if (c >= cols) return make_uint4(0, 0, 0, 0);
-  if constexpr (kVec) return __ldg(reinterpret_cast<const uint4*>(row + c));   // cols % 8 == 0
-  uint32_t w[4] = {0, 0, 0, 0};
+// 8 kN consecutive elements of a row, from column c (a multiple of 8; zero past
+// cols).  kVec: rows start on 16 bytes (cols % 8 == 0).  Otherwise the 16-byte
+// pieces that hold them are loaded and shifted into place; `limit`: elements from
+// the row's start to the end of the matrix, past which nothing is read.
+template <bool kVec, int kN>
+__device__ __forceinline__ void load_elems(const uint16_t* row, int64_t c, int64_t cols, int64_t limit, uint4 (&out)[kN]) {
+  if constexpr (kVec) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < cols) w[i >> 1] |= static_cast<uint32_t>(__ldg(row + c + i)) << (16 * (i & 1));
-  return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < kN; ++i)
+      out[i] = c + 8 * i < cols ? __ldg(reinterpret_cast<const uint4*>(row + c) + i) : make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const int d = static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 7u);    // elements past a 16-byte border
+  const uint16_t* at = row + c - d;
+  uint32_t w[4 * kN + 4];
+#pragma unroll
+  for (int i = 0; i <= kN; ++i) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    const int64_t e = c - d + 8 * i;                      // first element of the piece, counted from the row's start
+    if (e < cols) {
+      if (e + 8 <= limit) {
+        q = __ldg(reinterpret_cast<const uint4*>(at) + i);
+      } else {
+        uint32_t* qw = &q.x;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (e + k < limit) qw[k >> 1] |= static_cast<uint32_t>(__ldg(at + 8 * i + k)) << (16 * (k & 1));
+      }
+    }
+    w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+  }
+  // shift by d elements: 4, 2, then 1 (d is the row's, the same in all lanes of a warp)
+  if (d & 4) {
+#pragma unroll
+    for (int i = 0; i < 4 * kN + 2; ++i) w[i] = w[i + 2];
+  }
+  if (d & 2) {
+#pragma unroll
+    for (int i = 0; i < 4 * kN + 1; ++i) w[i] = w[i + 1];
+  }
+  if (d & 1) {
+#pragma unroll
+    for (int i = 0; i < 4 * kN; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+  if (c + 8 * kN > cols) {                                // the row's end: nothing of the next row
+#pragma unroll
+    for (int i = 0; i < 4 * kN; ++i) {
+      const int64_t left = cols - c - 2 * i;
+      w[i] = left >= 2 ? w[i] : (left == 1 ? w[i] & 0xFFFFu : 0u);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+template <bool kVec>
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t cols, int64_t limit) {
+  uint4 q[1];
+  load_elems<kVec, 1>(row, c, cols, limit, q);
+  return q[0];
 }
 
 // Thirty-two consecutive elements: what one thread encodes, one MXFP4 block or
@@ -30,10 +80,9 @@ struct Elems32 {
   uint4 q[4];
 };
 template <bool kVec>
-__device__ __forceinline__ Elems32 load32(const uint16_t* row, int64_t c, int64_t cols) {
+__device__ __forceinline__ Elems32 load32(const uint16_t* row, int64_t c, int64_t cols, int64_t limit) {
   Elems32 e;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) e.q[i] = load8<kVec>(row, c + 8 * i, cols);
+  load_elems<kVec, 4>(row, c, cols, limit, e.q);
   return e;
 }
 

@@ -239,7 +239,8 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
       const int t = i / per_row;
       const int64_t c = static_cast<int64_t>(i - t * per_row) * 32;
       const uint16_t* row = a.x + static_cast<int64_t>(t) * a.k;
-      return a.vec ? load32<true>(row, c, a.k) : load32<false>(row, c, a.k);
+      const int64_t limit = (m - t) * a.k;
+      return a.vec ? load32<true>(row, c, a.k, limit) : load32<false>(row, c, a.k, limit);
     };
     Elems32 first = {};
     if (tid < tasks) first = load(tid);

@@ -75,7 +75,7 @@ k_moe_route(const MxMoeArgs a) {
   const int segs = static_cast<int>((a.hidden + 1023) / 1024), kt = static_cast<int>(a.hidden / 128);
   for (int u = rank * kRouteWarps + warp; u < a.m * segs; u += kRouteCtas * kRouteWarps) {
     const int tok = u / segs, c = (u - tok * segs) * 1024 + lane * 32;
-    const Elems32 e = load32<true>(a.x + static_cast<int64_t>(tok) * a.hidden, c, a.hidden);
+    const Elems32 e = load32<true>(a.x + static_cast<int64_t>(tok) * a.hidden, c, a.hidden, a.hidden);
     uint32_t sb;
     const uint4 codes = encode32<kMxFp4>(e, 1.0f, sb);
     uint32_t word = sb << (8 * (lane & 3));

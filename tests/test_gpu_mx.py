@@ -59,7 +59,7 @@ def same_as_oracle(q, x, fmt, per_row):
 
 FORMS = [("mxfp4", False), ("nvfp4", False), ("nvfp4", True)]
 SHAPES = [(1, 1), (1, 8192), (3, 31), (5, 32), (7, 33), (128, 64), (129, 1000), (100, 1999), (257, 8200), (2, 22016),
-          (300, 16), (33, 8193), (700, 4160), (601, 9001), (20, 16000)]
+          (300, 16), (33, 8193), (700, 4160), (601, 9001), (20, 16000), (9, 1001), (17, 2047), (64, 36), (40, 4098)]
 
 
 @pytest.mark.parametrize("fmt,per_row", FORMS)
