@@ -364,7 +364,7 @@ cudaError_t launch_t(MxFewArgs a, const MxMaps& m, int num_sms, cudaStream_t str
 // Where one launch is faster than the quantiser's and the streamed product's.
 // Measured on 148 SMs, one token, MXFP4: here a step of 256 costs 0.30 us and 0.045
 // us a unit, or 0.1 us a unit (its 4.3 KB at an SM's share of memory bandwidth),
-// quantising 0.25 us per 1024 elements; there a tile's step costs 0.42 us, and 5 us
+// quantising 0.12 us per 1024 elements; there a tile's step costs 0.42 us, and 5.5 us
 // more are spent on the second kernel and on joining.  22016 x 8192: 19.5 us here,
 // 23.7 there; 4096 x 4096: 8.1 and 9.7; 8192 x 8192: 16.6 and 15.4; 8192 x 22016: 62 and 32.
 int mx_few_tile(int fmt, int64_t rows, int64_t m, int64_t k, int lora_steps, int num_sms) {
@@ -374,8 +374,8 @@ int mx_few_tile(int fmt, int64_t rows, int64_t m, int64_t k, int lora_steps, int
   const int64_t units = (rows + 31) / 32, most = (units + num_sms - 1) / num_sms, chunks = (most + kUnits - 1) / kUnits;
   const double per = static_cast<double>(most) / chunks;
   const double step = 0.30 + 0.045 * per > 0.1 * per ? 0.30 + 0.045 * per : 0.1 * per;
-  const double here = chunks * (ksteps + lora_steps) * step + 0.25 * m * k / 1024;
-  const double there = 5.0 + 0.42 * static_cast<double>((rows + 127) / 128) * (ksteps + lora_steps) / num_sms;
+  const double here = chunks * (ksteps + lora_steps) * step + 0.12 * m * k / 1024;
+  const double there = 5.5 + 0.42 * static_cast<double>((rows + 127) / 128) * (ksteps + lora_steps) / num_sms;
   return here < there ? n : 0;
 }
 

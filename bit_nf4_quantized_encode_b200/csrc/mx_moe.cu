@@ -133,7 +133,7 @@ k_moe_route(const MxMoeArgs a) {
     }
     __syncthreads();
     if (round == 0) cluster_wait();
-    // this round's experts: the warps of a group in order
+    // the experts of these tiles: the warps of a group in order
     const int e0 = round * kRouteWarps / share * 16, here = min(a.experts - e0, kRouteWarps / share * 16);
     for (int i = threadIdx.x; i < here * 16; i += kRouteThreads) {
       const int e = i >> 4, tok = i & 15;

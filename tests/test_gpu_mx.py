@@ -594,3 +594,58 @@ def test_two_calls_at_once(qb):
     torch.cuda.synchronize()
     for k in range(25):
         assert torch.equal(got[0][k], want[k % 5]) and torch.equal(got[1][k], want[4 - k % 5])
+
+
+@pytest.mark.parametrize("m,r", [(1, 0), (1, 64), (30, 0), (300, 64)])
+def test_inputs_that_arrive_just_before(qb, m, r):
+    """The tokens are written by a copy, or by another stream that is waited for,
+    right before the call; eagerly and in a captured graph."""
+    w = normal((11008, 1024), 0.02, 1).cuda()
+    q = qb.qlora_mx_quantize(w, "nvfp4")
+    a, b = (normal((r, 1024), 0.02, 4).cuda(), normal((11008, r), 0.02, 5).cuda()) if r else (None, None)
+    xs = [normal((m, 1024), 1.0, i).cuda() for i in range(3)]
+    want = [qb.qlora_mx_linear_fwd(q, x, a, b, 0.25)[0] for x in xs]
+    x, src, side = xs[0].clone(), xs[0].clone(), torch.cuda.Stream()
+
+    def copied():
+        x.copy_(src)
+        return qb.qlora_mx_linear_fwd(q, x, a, b, 0.25)[0]
+
+    def from_another_stream():
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            w.float().sum()
+            x.copy_(src)
+        torch.cuda.current_stream().wait_stream(side)
+        return qb.qlora_mx_linear_fwd(q, x, a, b, 0.25)[0]
+
+    for call in (copied, from_another_stream):
+        for v, y in zip(xs, want):
+            src.copy_(v)
+            assert torch.equal(call(), y)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = call()
+        for v, y in zip(xs, want):
+            src.copy_(v)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, y)
+
+
+def test_weight_quantised_just_before(qb):
+    """Quantise, use, overwrite and use again without a wait between."""
+    ws = [normal((4096, 1024), 0.02, i).cuda() for i in range(4)]
+    x = normal((2, 1024), 1.0, 9).cuda()
+    for fmt in ("mxfp4", "nvfp4"):
+        want = []
+        for w in ws:
+            want.append(qb.qlora_mx_linear_fwd(qb.qlora_mx_quantize(w, fmt), x)[0])
+            torch.cuda.synchronize()
+        out, got = qb.empty_mx(4096, 1024, x.device, fmt), []
+        for _ in range(5):
+            for w in ws:
+                got.append(qb.qlora_mx_linear_fwd(qb.qlora_mx_quantize(w, out=out), x)[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, want[i % 4]) for i, g in enumerate(got))
