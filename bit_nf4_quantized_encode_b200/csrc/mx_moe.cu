@@ -424,8 +424,24 @@ k_moe_product(const MxMoeArgs a, const __grid_constant__ CUtensorMap wmap, const
       s += steps;
       const MoeExpert info = a.list[ex];
       const uint32_t ab = seg & 1u;
-      if (!mbar_wait(&acc_full[ab], (seg >> 1) & 1u, a.err)) break;
+      const bool whole = from == 0 && s == per_tile, ends = kUp || s == per_tile || left == 0;
+      // all that does not need the products, before waiting for them
+      Parts p{};
+      uint32_t* counter = (kUp ? a.up_counters : a.counters) + tile * 4 + quarter;
+      bool alone = false;                                         // the other runs' parts are there
+      if (ends && !whole) {
+        p = parts_of(a.slots + rl, slot_floats, total, static_cast<int64_t>(tile) * per_tile, per_tile, runs);
+        alone = others_counted(counter, p.n);
+      }
+      float pr[kSlots];
+      if (!kUp) {
+#pragma unroll
+        for (int t = 0; t < kSlots; ++t)
+          pr[t] = (info.tokens >> t) & 1u ? __ldg(a.probs + t * a.top_k + static_cast<int>((info.slots >> (4 * t)) & 15u)) : 0.0f;
+      }
+      if (!mbar_wait_warp(&acc_full[ab], (seg >> 1) & 1u, a.err)) break;
       tc_fence_after();
+      if (ends && !whole && !alone && left == 0) alone = others_counted(counter, p.n);
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ab * kAcc;
       uint32_t v0[16], v1[16];
       tmem_ld16(taddr, v0);
@@ -433,57 +449,52 @@ k_moe_product(const MxMoeArgs a, const __grid_constant__ CUtensorMap wmap, const
       tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(&acc_empty[ab]);
-      const bool whole = from == 0 && s == per_tile;
       float* mine = my_slot(a.slots, slot_floats, tile == tile0) + rl;
+      const int me = run - p.c0;
       if constexpr (kUp) {
         const int rt = tile - ex * row_tiles;
         auto emit = [&](int t, float g, float up) { emit_h(a, ex, rt, row_tiles, t, quarter, lane, g, up); };
 #pragma unroll
         for (int t = 0; t < kSlots; ++t)
           if ((info.tokens >> t) & 1u) {
-            if (whole) {
-              emit(t, __uint_as_float(v0[t]), __uint_as_float(v1[t]));
+            float gu[2] = {__uint_as_float(v0[t]), __uint_as_float(v1[t])};
+            if (alone) add_parts<2>(p, me, 2 * t, 2 * kSlots, gu);
+            if (whole || alone) {
+              emit(t, gu[0], gu[1]);
             } else {
-              mine[(2 * t) * 128] = __uint_as_float(v0[t]);
-              mine[(2 * t + 1) * 128] = __uint_as_float(v1[t]);
+              mine[(2 * t) * 128] = gu[0];
+              mine[(2 * t + 1) * 128] = gu[1];
             }
           }
-        if (!whole) {
-          const Parts p = parts_of(a.slots + rl, slot_floats, total, static_cast<int64_t>(tile) * per_tile, per_tile, runs);
-          if (count_part(a.up_counters + tile * 4 + quarter, p.n))
-            for (uint32_t left_t = info.tokens; left_t != 0u; left_t &= left_t - 1u) {
-              const int t = __ffs(static_cast<int>(left_t)) - 1;
-              Parts pt = p;
-              pt.first += (2 * t) * 128;
-              float gu[2];
-              join_parts<2, 8>(pt, 2, [&](int i, float v) { gu[i] = v; });
-              emit(t, gu[0], gu[1]);
-            }
-        }
+        if (!whole && !alone && count_part(counter, p.n))
+          for (uint32_t left_t = info.tokens; left_t != 0u; left_t &= left_t - 1u) {
+            const int t = __ffs(static_cast<int>(left_t)) - 1;
+            Parts pt = p;
+            pt.first += (2 * t) * 128;
+            float gu[2];
+            join_parts<2, 8>(pt, 2, [&](int i, float v) { gu[i] = v; });
+            emit(t, gu[0], gu[1]);
+          }
       } else {
 #pragma unroll
         for (int t = 0; t < kSlots; ++t)
-          if ((info.tokens >> t) & 1u) {
-            const int j = static_cast<int>((info.slots >> (4 * t)) & 15u);
-            y[t] = __fmaf_rn(__ldg(a.probs + t * a.top_k + j), __uint_as_float(v0[t]), y[t]);
-          }
-        if (s != per_tile && left > 0) continue;                    // more experts of this tile
+          if ((info.tokens >> t) & 1u) y[t] = __fmaf_rn(pr[t], __uint_as_float(v0[t]), y[t]);
+        if (!ends) continue;                                      // more experts of this tile
         const int64_t row = static_cast<int64_t>(tile) * 128 + rl;
         auto store = [&](int t, float v) {
           const __nv_bfloat16 b = __float2bfloat16_rn(v);
           a.y[static_cast<int64_t>(t) * a.hidden + row] = *reinterpret_cast<const uint16_t*>(&b);
         };
+        if (alone) add_parts<kSlots>(p, me, 0, a.m, y);
 #pragma unroll
-        for (int t = 0; t < kSlots; ++t)
+        for (int t = 0; t < kSlots; ++t) {
           if (t < a.m) {
-            if (whole) store(t, y[t]);
+            if (whole || alone) store(t, y[t]);
             else mine[t * 128] = y[t];
-            y[t] = 0.0f;
           }
-        if (!whole) {
-          const Parts p = parts_of(a.slots + rl, slot_floats, total, static_cast<int64_t>(tile) * per_tile, per_tile, runs);
-          if (count_part(a.counters + tile * 4 + quarter, p.n)) join_columns(p, a.m, store);
+          y[t] = 0.0f;
         }
+        if (!whole && !alone && count_part(counter, p.n)) join_columns(p, a.m, store);
       }
       ++tile;
       s = from = 0;

@@ -6,6 +6,10 @@
 // have whole goes to one of its two slots in the work buffer (its first tile's, or
 // its last one's); the warp that completes the count of its rows of the tile sums
 // the parts in the order of the runs, so results do not depend on who that is.
+// Writing a part, making it visible, counting it and reading the others take 4 to
+// 5 us at the end of a run.  The run behind usually has counted its part of a tile
+// long before, with its first steps: a warp that finds all others counted sums
+// them with its own values and writes nothing (0.6 us).
 #pragma once
 #include <cuda_runtime.h>
 
@@ -39,6 +43,41 @@ __device__ __forceinline__ Parts parts_of(const float* slots, int64_t slot_float
 }
 __device__ __forceinline__ float* my_slot(float* slots, int64_t slot_floats, bool first_tile) {
   return slots + (static_cast<int64_t>(blockIdx.x) * 2 + (first_tile ? 0 : 1)) * slot_floats;
+}
+
+// Whether all parts but this warp's are counted (one load, acquired).
+__device__ __forceinline__ bool others_counted(const uint32_t* counter, int n) {
+  uint32_t v = 0;
+  if ((threadIdx.x & 31) == 0) asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+  const bool all = __shfl_sync(0xFFFFFFFFu, v, 0) == static_cast<uint32_t>(n - 1);
+  __syncwarp();                              // the other lanes' reads come after the acquired one
+  return all;
+}
+
+// Adds the other parts of columns t0 .. t0 + kT - 1 below m to this run's `mine`,
+// everything in the order of the runs.
+template <int kT>
+__device__ __forceinline__ void add_parts(const Parts& p, int me, int t0, int m, float (&mine)[kT]) {
+  const float* rest = p.first + p.skip - p.next;
+  float sum[kT];
+#pragma unroll
+  for (int i = 0; i < kT; ++i) sum[i] = 0.0f;
+#pragma unroll 1
+  for (int c = 0; c < p.n; ++c) {
+    if (c == me) {
+#pragma unroll
+      for (int i = 0; i < kT; ++i) sum[i] += mine[i];
+      continue;
+    }
+    const float* part = (c == 0 ? p.first : rest + c * p.next) + t0 * 128;
+    float v[kT];
+#pragma unroll
+    for (int i = 0; i < kT; ++i) v[i] = t0 + i < m ? __ldcg(part + i * 128) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kT; ++i) sum[i] += v[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kT; ++i) mine[i] = sum[i];
 }
 
 // Counts this warp's part of a tile (its stores before are visible to whoever

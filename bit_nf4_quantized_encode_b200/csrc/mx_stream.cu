@@ -256,6 +256,12 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
     asm volatile("griddepcontrol.wait;" ::: "memory");      // x_global and the zeroed counters
     const int quarter = warp & 3, rl = quarter * 32 + lane;
     const int m = static_cast<int>(a.m);
+    // lane t: the global scales of tokens t and t + 32
+    float gx0 = 1.0f, gx1 = 1.0f;
+    if (kFmt == kNvFp4) {
+      if (lane < m) gx0 = __ldg(a.x_global + lane);
+      if (lane + 32 < m) gx1 = __ldg(a.x_global + lane + 32);
+    }
     constexpr int kChunk = kBN < 32 ? kBN : 32;
     const int64_t slot_floats = static_cast<int64_t>(m) * 128;
     int tile = tile0, j = step0, left = nsteps;
@@ -263,20 +269,29 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
       const int steps = min(per_tile - j, left);
       left -= steps;
       const uint32_t ab = seg & 1u;
-      if (!mbar_wait(&acc_full[ab], (seg >> 1) & 1u, a.err)) break;
-      tc_fence_after();
+      const bool whole = steps == per_tile;
       const int64_t row = static_cast<int64_t>(tile) * 128 + rl;
       const bool row_ok = row < a.rows;
+      // all that does not need the products, before waiting for them
+      Parts p{};
+      uint32_t* counter = a.counters + tile * 4 + quarter;
+      bool alone = false;                    // the other runs' parts are there
+      if (!whole) {
+        p = parts_of(a.slots + rl, slot_floats, total, static_cast<int64_t>(tile) * per_tile, per_tile, runs);
+        alone = others_counted(counter, p.n);
+      }
       float gw = 1.0f;
       if (kFmt == kNvFp4 && row_ok) gw = __ldg(a.w_global + (a.w_per_row ? row : 0));
       auto store = [&](int t, float v) {
+        if (kFmt == kNvFp4) v = __fmul_rn(v, __fmul_rn(__shfl_sync(0xFFFFFFFFu, t < 32 ? gx0 : gx1, t & 31), gw));
         if (!row_ok) return;
-        if (kFmt == kNvFp4) v = __fmul_rn(v, __fmul_rn(__ldg(a.x_global + t), gw));
         const __nv_bfloat16 b = __float2bfloat16_rn(v);
         a.out[t * a.rows + row] = *reinterpret_cast<const uint16_t*>(&b);
       };
+      if (!mbar_wait_warp(&acc_full[ab], (seg >> 1) & 1u, a.err)) break;
+      tc_fence_after();
+      if (!whole && !alone && left == 0) alone = others_counted(counter, p.n);
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + ab * kBN;
-      const bool whole = steps == per_tile;
       float* mine = my_slot(a.slots, slot_floats, tile == tile0) + rl;
 #pragma unroll 1
       for (int cc = 0; cc * kChunk < m; ++cc) {
@@ -284,21 +299,23 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
         if constexpr (kChunk == 32) tmem_ld32(taddr + cc * 32, v);
         else tmem_ld16(taddr, v);
         tmem_wait_ld();
+        float f[kChunk];
+#pragma unroll
+        for (int c = 0; c < kChunk; ++c) f[c] = __uint_as_float(v[c]);
+        if (alone) add_parts<kChunk>(p, static_cast<int>(blockIdx.x) - p.c0, cc * kChunk, m, f);
 #pragma unroll
         for (int c = 0; c < kChunk; ++c) {
           const int t = cc * kChunk + c;
           if (t < m) {
-            if (whole) store(t, __uint_as_float(v[c]));
-            else mine[t * 128] = __uint_as_float(v[c]);
+            if (whole || alone) store(t, f[c]);
+            else mine[t * 128] = f[c];
           }
         }
       }
       tc_fence_before();
       mbar_arrive(&acc_empty[ab]);
-      if (whole) continue;
       // each warp counts its own 32 rows, so no warp waits for another
-      const Parts p = parts_of(a.slots + rl, slot_floats, total, static_cast<int64_t>(tile) * per_tile, per_tile, runs);
-      if (count_part(a.counters + tile * 4 + quarter, p.n)) join_columns(p, m, store);
+      if (!whole && !alone && count_part(counter, p.n)) join_columns(p, m, store);
     }
   }
 
