@@ -106,7 +106,14 @@ __device__ __forceinline__ void store_final(const RankProblem& p, int64_t row, i
     }
   }
   if (p.out_bf16) store_bf16_row(p, p.out_bf16, row, c0, v, p.bf16_scale);
-  if (p.out_div) store_bf16_row(p, p.out_div, row, c0, v, p.bf16_scale / (p.row_div[row] * p.all_div[0]));
+  if (p.out_div) {
+    // one divisor after the other: their product may be below what a float holds
+    const float by_row = 1.0f / p.row_div[row], by_all = 1.0f / p.all_div[0];
+    float d[64];
+#pragma unroll
+    for (int c = 0; c < 64; ++c) d[c] = __fmul_rn(__fmul_rn(p.bf16_scale, v[c]), by_row);
+    store_bf16_row(p, p.out_div, row, c0, d, by_all);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)

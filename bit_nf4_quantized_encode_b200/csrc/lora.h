@@ -31,7 +31,7 @@ struct RankProblem {
   int64_t ld_bf16;
   int64_t bf16_cols;         // a multiple of 64, <= 64 * n_tiles
   float bf16_scale;
-  // optional: bf16(bf16_scale * D / (row_div[row] * all_div[0])), shaped as out_bf16
+  // optional: bf16(bf16_scale * D / row_div[row] / all_div[0]), shaped as out_bf16
   // (the rank-r operand of a product whose accumulator is scaled at its end)
   uint16_t* out_div;
   const float* row_div;

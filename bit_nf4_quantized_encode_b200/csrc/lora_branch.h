@@ -51,7 +51,7 @@ struct BwdLayout {
 BwdLayout bwd_layout(const LinearShape& s);
 
 // Divisors of the rank-r activations of a product whose accumulator is scaled
-// at its end: bf16(s v / (row[i] * all[0])) goes to `out`; row null: none.
+// at its end: bf16(s v / row[i] / all[0]) goes to `out`; row null: none.
 struct RankDivide {
   const float* row = nullptr;
   const float* all = nullptr;

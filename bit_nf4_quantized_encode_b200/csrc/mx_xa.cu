@@ -97,8 +97,10 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) k_m
   if (tok >= a.m) return;
   if (a.xa && rank_row < a.r) a.xa[static_cast<int64_t>(tok) * a.r + rank_row] = v;
   if (rank_row < a.rpad) {
-    const float s = a.all_div ? a.s / (mx_global_scale(s_amax[tt] << 16) * a.all_div[0]) : a.s;
-    const __nv_bfloat16 b = __float2bfloat16_rn(__fmul_rn(s, v));
+    v = __fmul_rn(a.s, v);
+    // one divisor after the other: their product may be below what a float holds
+    if (a.all_div) v = __fdiv_rn(__fmul_rn(v, mx_pow2_inverse(mx_global_scale(s_amax[tt] << 16))), a.all_div[0]);
+    const __nv_bfloat16 b = __float2bfloat16_rn(v);
     a.sxa[static_cast<int64_t>(tok) * a.rpad + rank_row] = *reinterpret_cast<const uint16_t*>(&b);
   }
 }

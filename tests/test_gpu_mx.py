@@ -555,6 +555,21 @@ def test_zeros_and_far_magnitudes(qb, m, fmt):
     assert (qb.qlora_mx_linear_fwd(z, x)[0] == 0).all() and (qb.qlora_mx_dequantize(z) == 0).all()
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("m", [1, 12, 40, 150])
+def test_adapter_with_far_magnitudes(qb, m, fmt):
+    """Tokens and gradients of 2^-100 and 2^100 give the result of ones of 1, scaled:
+    the rank-r term rides on global scales whose product no float holds."""
+    rows, cols, r = 256, 640, 64
+    w, x, dy = normal((rows, cols), 0.02, 1).cuda(), normal((m, cols), 1.0, 2).cuda(), normal((m, rows), 1.0, 3).cuda()
+    a, b = normal((r, cols), 0.02, 4).cuda(), normal((rows, r), 0.02, 5).cuda()
+    q, qt = qb.qlora_mx_quantize(w, fmt), qb.qlora_mx_quantize(w, fmt, transpose=True)
+    y, d = qb.qlora_mx_linear_fwd(q, x, a, b, 0.25)[0], qb.qlora_mx_linear_bwd(qt, dy, x, a, b, 0.25)[0]
+    for e in (-100, 100):
+        assert torch.equal(qb.qlora_mx_linear_fwd(q, x * 2.0 ** e, a, b, 0.25)[0], y * 2.0 ** e)
+        assert torch.equal(qb.qlora_mx_linear_bwd(qt, dy * 2.0 ** e, x, a, b, 0.25)[0], d * 2.0 ** e)
+
+
 def test_offsets_past_32_bits(qb):
     """2.4e9 weights (4.8 GB): the last rows are quantised, dequantised and
     multiplied as they are alone."""
