@@ -314,7 +314,7 @@ k_mx_dequant(const uint8_t* codes, const uint8_t* scales, const float* gs, int p
     for (int j = 0; j < 4; ++j) {
       const int64_t c = c0 + j * 256;
       if (kVec && c >= cols) continue;
-      const float s = kFmt == kMxFp4 ? mx_e8m0_value(sb[j]) : e4m3_to_f32(sb[j]);
+      const float s = kFmt == kMxFp4 ? mx_e8m0_value(sb[j]) : mx_e4m3_value(sb[j]);
       uint32_t h[4], o[4];
       mx_levels8(word[j], h);
 #pragma unroll

@@ -119,7 +119,9 @@ __device__ __forceinline__ uint32_t finite_mag8(const uint4& q) {
 template <int kFmt>
 __device__ __forceinline__ uint32_t scale_byte(uint32_t mag, float inv_g) {
   if (kFmt == kMxFp4) return mag >= 0x7F80u ? 255u : mx_e8m0(mag << 16);
-  return mag >= 0x7F80u ? 0x7Fu : mx_e4m3(__fdiv_rn(__fmul_rn(__uint_as_float(mag << 16), inv_g), 6.0f));
+  // v / 6 as mx_quotient2 has it: exact where it is half way between two E4M3 values
+  const float v = __fmul_rn(__uint_as_float(mag << 16), inv_g), r = 1.0f / 6.0f, q = __fmul_rn(v, r);
+  return mag >= 0x7F80u ? 0x7Fu : mx_e4m3(__fmaf_rn(__fmaf_rn(-6.0f, q, v), r, q));
 }
 
 // Multiplier (MXFP4), or scale and its reciprocal (NVFP4), of a block's elements.
@@ -135,8 +137,8 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t sb) {
     b.s = b.r = mx_e8m0_inverse(b.zero ? 127u : sb);
   } else {
     b.zero = sb == 0x7Fu || sb == 0u;
-    b.s = e4m3_to_f32(b.zero ? 0x38u : sb);
-    b.r = __frcp_rn(b.s);
+    b.s = mx_e4m3_value(b.zero ? 0x38u : sb);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b.r) : "f"(b.s));      // the quotient's step makes up for its error
   }
   return b;
 }

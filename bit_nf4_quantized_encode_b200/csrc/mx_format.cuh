@@ -52,6 +52,15 @@ __device__ __forceinline__ uint32_t mx_e4m3(float v) {
   return h & 0xFFu;
 }
 
+// The value of an E4M3 byte.
+__device__ __forceinline__ float mx_e4m3_value(uint32_t byte) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(byte)));
+  float f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(h));
+  return f;
+}
+
 // The NVFP4 global scale of magnitudes up to `amax` (bits of a non-negative
 // finite float): the smallest power of two g with amax <= 6 * 448 * g
 // (2688 = 1.3125 * 2^11), at least 2^-126; 1 for amax = 0.  A power of two, so
@@ -86,8 +95,8 @@ __device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c
   return v;
 }
 
-// Quotients v / s rounded to nearest, from r = RN(1 / s): one Newton step on the
-// remainder (minus_s = -s).  Where v / s is exactly half way between two levels
+// Quotients v / s to within a rounding, from r = 1 / s to within 2^-22: one Newton
+// step on the remainder (minus_s = -s).  Where v / s is exactly half way between two levels
 // it is representable and the step returns it exactly, so the tie stays a tie;
 // every other quotient of an 8-bit by a 4-bit significand is 2^-8 away from one.
 // The step turns -0 into +0, so the caller puts the sign back.
