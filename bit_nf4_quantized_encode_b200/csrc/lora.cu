@@ -29,7 +29,7 @@
 #include <cstdint>
 
 #include "lora.h"
-#include "sm100_ptx.cuh"
+#include "mx_ptx.cuh"
 
 namespace qlora {
 namespace {
@@ -131,7 +131,7 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
   uint32_t* last_flag = tmem_slot + 1;
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = warp_index();             // TMA and MMA are issued by an elected lane of a uniform warp
   const int lane = threadIdx.x & 31;
   const int nunits = a.total_units;
 
@@ -151,7 +151,7 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && elect_one()) {
     tma_prefetch_desc(&am0);
     tma_prefetch_desc(&bm0);
     if (a.nprob > 1) {
@@ -159,6 +159,7 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
       tma_prefetch_desc(&bm1);
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -166,81 +167,86 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool alive = true;
-      for (int u = blockIdx.x; u < nunits && alive; u += gridDim.x) {
-        const UnitPos w = unit_pos(a, u);
-        const RankProblem& p = a.p[w.prob];
-        const CUtensorMap* am = w.prob ? &am1 : &am0;
-        const CUtensorMap* bm = w.prob ? &bm1 : &bm0;
-        // two consecutive k-steps at a time: both stages are claimed first and
-        // their loads issued back to back, so every row of the long operand is
-        // requested in 256-byte runs rather than 128-byte ones
-        for (int j = 0; j < w.nk && alive; j += 2) {
-          const int cnt = w.nk - j < 2 ? w.nk - j : 2;
-          for (int q = 0; q < cnt; ++q) {
-            const uint32_t stage = (it + q) % kStages, phase = ((it + q) / kStages) & 1u;
-            if (!mbar_wait(&empty[stage], phase ^ 1u, a.err)) { alive = false; break; }
-          }
-          if (!alive) break;
-          for (int q = 0; q < cnt; ++q, ++it) {
-            const uint32_t stage = it % kStages;
-            uint8_t* sA = smem_gen + stage * kStageBytes;
-            uint8_t* sB = sA + kABytes;
-            const int k0 = (w.kbeg + j + q) * 64;
-            mbar_arrive_expect_tx(&full[stage], kStageBytes);
-            if (p.a_mn) {   // A^T stored [k][m]: two 64-wide MN boxes
-              tma_load_2d(sA, am, w.mt * 128, k0, &full[stage]);
-              tma_load_2d(sA + 8192, am, w.mt * 128 + 64, k0, &full[stage]);
-            } else {
-              tma_load_2d(sA, am, k0, w.mt * 128, &full[stage]);
-            }
-            if (p.b_mn) tma_load_2d(sB, bm, w.nt * 64, k0, &full[stage]);
-            else tma_load_2d(sB, bm, k0, w.nt * 64, &full[stage]);
-          }
+    uint32_t stage = 0, phase = 0;
+    bool alive = true;
+    for (int u = blockIdx.x; u < nunits && alive; u += gridDim.x) {
+      const UnitPos w = unit_pos(a, u);
+      const RankProblem& p = a.p[w.prob];
+      const CUtensorMap* am = w.prob ? &am1 : &am0;
+      const CUtensorMap* bm = w.prob ? &bm1 : &bm0;
+      const bool a_mn = p.a_mn != 0, b_mn = p.b_mn != 0;
+      auto load = [&](uint32_t st, int k0) {
+        uint8_t* sA = smem_gen + st * kStageBytes;
+        uint8_t* sB = sA + kABytes;
+        mbar_arrive_expect_tx(&full[st], kStageBytes);
+        if (a_mn) {   // A^T stored [k][m]: two 64-wide MN boxes
+          tma_load_2d(sA, am, w.mt * 128, k0, &full[st]);
+          tma_load_2d(sA + 8192, am, w.mt * 128 + 64, k0, &full[st]);
+        } else {
+          tma_load_2d(sA, am, k0, w.mt * 128, &full[st]);
         }
+        if (b_mn) tma_load_2d(sB, bm, w.nt * 64, k0, &full[st]);
+        else tma_load_2d(sB, bm, k0, w.nt * 64, &full[st]);
+      };
+      // two consecutive k-steps at a time: both stages are claimed first and
+      // their loads issued back to back, so every row of the long operand is
+      // requested in 256-byte runs rather than 128-byte ones
+      for (int j = 0; j < w.nk; j += 2) {
+        const bool two = j + 1 < w.nk;
+        const uint32_t stage2 = stage + 1 == kStages ? 0 : stage + 1, phase2 = stage2 == 0 ? phase ^ 1u : phase;
+        if (!mbar_wait_warp(&empty[stage], phase ^ 1u, a.err) ||
+            (two && !mbar_wait_warp(&empty[stage2], phase2 ^ 1u, a.err))) {
+          alive = false;
+          break;
+        }
+        if (elect_one()) {
+          load(stage, (w.kbeg + j) * 64);
+          if (two) load(stage2, (w.kbeg + j + 1) * 64);
+        }
+        __syncwarp();
+        stage = two ? stage2 : stage;
+        phase = two ? phase2 : phase;
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      uint32_t it = 0, uctr = 0;
-      bool alive = true;
-      // uctr counts accumulator fillings: one per unit, or one per `flush` k-steps
-      for (int u = blockIdx.x; u < nunits && alive; u += gridDim.x) {
-        const UnitPos w = unit_pos(a, u);
-        const RankProblem& p = a.p[w.prob];
-        const uint32_t idesc = idesc_bf16(128, 64, p.a_mn != 0, p.b_mn != 0);
-        const int piece = p.flush > 0 ? p.flush : w.nk;
-        int left = 0;                          // k-steps to go of this filling
-        for (int j = 0; j < w.nk; ++j, ++it) {
-          const uint32_t ab = uctr & 1u, aphase = (uctr >> 1) & 1u;
-          const bool fresh = left == 0;
-          if (fresh) {
-            left = w.nk - j < piece ? w.nk - j : piece;
-            if (!mbar_wait(&acc_empty[ab], aphase ^ 1u, a.err)) { alive = false; break; }
-            tc_fence_after();
-          }
-          const uint32_t stage = it % kStages, phase = (it / kStages) & 1u;
-          if (!mbar_wait(&full[stage], phase, a.err)) { alive = false; break; }
-          tc_fence_after();
-          const uint32_t sA = smem0 + stage * kStageBytes;
-          const uint32_t sB = sA + kABytes;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t adesc = p.a_mn ? smem_desc_sw128(sA + kk * 2048, 8192, 1024)
-                                          : smem_desc_sw128(sA + kk * 32, 16, 1024);
-            const uint64_t bdesc = p.b_mn ? smem_desc_sw128(sB + kk * 2048, 8192, 1024)
-                                          : smem_desc_sw128(sB + kk * 32, 16, 1024);
-            mma_bf16_ss(tmem_base + ab * 64, adesc, bdesc, idesc, !fresh || kk != 0 ? 1u : 0u);
-          }
-          mma_commit(&empty[stage]);
-          if (--left == 0) {
-            mma_commit(&acc_full[ab]);
-            ++uctr;
-          }
+    uint32_t stage = 0, phase = 0, uctr = 0;
+    bool alive = true;
+    // uctr counts accumulator fillings: one per unit, or one per `flush` k-steps
+    for (int u = blockIdx.x; u < nunits && alive; u += gridDim.x) {
+      const UnitPos w = unit_pos(a, u);
+      const RankProblem& p = a.p[w.prob];
+      const bool a_mn = p.a_mn != 0, b_mn = p.b_mn != 0;
+      const uint32_t idesc = idesc_bf16(128, 64, a_mn, b_mn);
+      const int piece = p.flush > 0 ? p.flush : w.nk;
+      // a K = 16 slice: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
+      const uint64_t a0 = a_mn ? smem_desc_sw128(smem0, 8192, 1024) : smem_desc_sw128(smem0, 16, 1024);
+      const uint64_t b0 = (b_mn ? smem_desc_sw128(smem0, 8192, 1024) : smem_desc_sw128(smem0, 16, 1024)) + (kABytes >> 4);
+      const uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
+      int left = 0;                            // k-steps to go of this filling
+      for (int j = 0; j < w.nk; ++j) {
+        const uint32_t ab = uctr & 1u, aphase = (uctr >> 1) & 1u;
+        const bool fresh = left == 0;
+        if (fresh) {
+          left = w.nk - j < piece ? w.nk - j : piece;
+          if (!mbar_wait_warp(&acc_empty[ab], aphase ^ 1u, a.err)) { alive = false; break; }
         }
+        if (!mbar_wait_warp(&full[stage], phase, a.err)) { alive = false; break; }
+        tc_fence_after();
+        const uint32_t off = stage * (kStageBytes >> 4);
+        const bool last = --left == 0;
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_ss(tmem_base + ab * 64, a0 + off + kk * a_step, b0 + off + kk * b_step, idesc,
+                        !fresh || kk != 0 ? 1u : 0u);
+          mma_commit(&empty[stage]);
+          if (last) mma_commit(&acc_full[ab]);
+        }
+        __syncwarp();
+        if (last) ++uctr;
+        if (++stage == kStages) { stage = 0; phase ^= 1u; }
       }
     }
   } else {
@@ -339,6 +345,7 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
   }
 
   tc_fence_before();
+  __syncwarp();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
