@@ -79,20 +79,24 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
   const uint32_t x_off = stage_bytes * stages;       // tokens' codes, scales, rank-r activations
   const uint32_t sx_off = x_off + a.ksteps * (kN * 128), l_off = (sx_off + a.ksteps * kSx + 512u + 1023u) & ~1023u;
   // this CTA's units, in chunks of nearly equal size
-  const int64_t total_units = (a.rows + 31) / 32;
-  const int64_t u0 = total_units * blockIdx.x / gridDim.x, u1 = total_units * (blockIdx.x + 1) / gridDim.x;
+  // (the first `more` CTAs have one more than the others)
+  const int total_units = static_cast<int>((a.rows + 31) / 32), cta = static_cast<int>(blockIdx.x);
+  const int least = total_units / static_cast<int>(gridDim.x), more = total_units - least * static_cast<int>(gridDim.x);
+  const int u0 = cta * least + min(cta, more), units = least + (cta < more ? 1 : 0);
   const int chunks = a.chunks;
   const int per_chunk = a.ksteps + a.lora_steps;
   struct Chunk {
-    int64_t unit;                                    // first
+    int unit;                                        // first
     int n, tile, tiles, col;                         // units, first row tile of its scales, how many, first column
   };
   auto chunk_of = [&](int c) {
     Chunk k;
-    k.unit = u0 + (u1 - u0) * c / chunks;
-    k.n = static_cast<int>(u0 + (u1 - u0) * (c + 1) / chunks - k.unit);
-    k.tile = static_cast<int>(k.unit >> 2);
-    k.col = static_cast<int>(k.unit & 3);
+    // chunk c has one unit more than the last ones while c is below the remainder
+    const int each = units / chunks, left = units - each * chunks;
+    k.unit = u0 + each * c + min(c, left);
+    k.n = each + (c < left ? 1 : 0);
+    k.tile = k.unit >> 2;
+    k.col = k.unit & 3;
     k.tiles = (k.col + k.n + 3) >> 2;
     return k;
   };
@@ -142,7 +146,7 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
             mbar_arrive_expect_tx(&full[stage], k.n * 4096 + k.tiles * sbytes);
 #pragma unroll
             for (int i = 0; i < kUnits; ++i)
-              if (i < k.n) tma_load_2d(sA + i * 4096, &wmap, j * 128, static_cast<int32_t>((k.unit + i) * 32), &full[stage]);
+              if (i < k.n) tma_load_2d(sA + i * 4096, &wmap, j * 128, (k.unit + i) * 32, &full[stage]);
             uint8_t* sS = sA + a.units * 4096;
 #pragma unroll
             for (int i = 0; i < kTiles; ++i)
@@ -152,7 +156,7 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
             mbar_arrive_expect_tx(&full[stage], k.n * 4096);
 #pragma unroll
             for (int i = 0; i < kUnits; ++i)
-              if (i < k.n) tma_load_2d(sA + i * 4096, &lwmap, (j - a.ksteps) * 64, static_cast<int32_t>((k.unit + i) * 32), &full[stage]);
+              if (i < k.n) tma_load_2d(sA + i * 4096, &lwmap, (j - a.ksteps) * 64, (k.unit + i) * 32, &full[stage]);
           }
         }
         __syncwarp();
@@ -285,7 +289,7 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
         if constexpr (kN == 8) tmem_ld8(taddr, v);
         else tmem_ld16(taddr, v);
         tmem_wait_ld();
-        const int64_t row = (k.unit + unit) * 32 + lane;
+        const int row = (k.unit + unit) * 32 + lane;
         if (row < a.rows) {
           float gw = 1.0f;
           if (kFmt == kNvFp4) gw = __ldg(a.w_global + (a.w_per_row ? row : 0));
@@ -295,7 +299,7 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
               float y = __uint_as_float(v[t]);
               if (kFmt == kNvFp4) y = __fmul_rn(__fmul_rn(y, s_g[t]), gw);
               const __nv_bfloat16 b = __float2bfloat16_rn(y);
-              a.out[t * a.rows + row] = *reinterpret_cast<const uint16_t*>(&b);
+              a.out[static_cast<int64_t>(t) * a.rows + row] = *reinterpret_cast<const uint16_t*>(&b);
             }
         }
       }

@@ -323,8 +323,9 @@ def test_linear_refusals(qb):
         qb.qlora_mx_linear_bwd(q, normal((4, 128)).cuda(), A=normal((8, 64)).cuda(), B=normal((128, 8)).cuda())
 
 
-def test_linear_with_a_scale_per_weight_row(qb):
-    w, x = f64(normal((200, 300), 0.02, 1)) * np.logspace(-3, 3, 200)[:, None], normal((5, 300), 1.0, 2)
+@pytest.mark.parametrize("m", [1, 5, 16, 40, 150])
+def test_linear_with_a_scale_per_weight_row(qb, m):
+    w, x = f64(normal((200, 300), 0.02, 1)) * np.logspace(-3, 3, 200)[:, None], normal((m, 300), 1.0, 2)
     w = f64(torch.from_numpy(w).to(torch.bfloat16))
     q = upload(qb, w, "nvfp4", True)
     wv, xv = mx.round_trip(w, "nvfp4", True), mx.round_trip(f64(x), "nvfp4", True)
