@@ -436,7 +436,7 @@ qlora_status qlora_linear_fwd(const qlora_nf4_tensor* W, const uint16_t* X, int6
   // 1) X A^T (fp32 to XA_out when asked) and bf16(s X A^T), zero-padded to a
   //    multiple of 64 columns, as the LoRA k-step operand of the fused GEMM
   uint16_t* sxa = reinterpret_cast<uint16_t*>(ws + L.xa.sxa);
-  if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, RankDivide(), 0, d, cs)) != QLORA_OK) return st;
+  if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, RankDivide(), 0, false, d, cs)) != QLORA_OK) return st;
 
   // 2) Y = X deq(W)^T + (s XA) B^T  (fused dequant GEMM)
   const int bn = 256;

@@ -128,11 +128,12 @@ BwdLayout bwd_layout(const LinearShape& s) {
 }
 
 qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_t* A, float s, float* XA_out, uint8_t* ws,
-                         const XaLayout& L, const RankDivide& div, int flush, const DeviceInfo& d, cudaStream_t cs) {
+                         const XaLayout& L, const RankDivide& div, int flush, bool cleared, const DeviceInfo& d,
+                         cudaStream_t cs) {
   RankPlan xp = rank_tiling(sh.m, sh.cols, sh.lora_steps);
   xp.splits = launch_splits(xp.tiles(), xp.ksteps, d.num_sms, L.slot_bytes);
   if (!slots_fit(xp.tiles(), xp.splits, L.slot_bytes)) return QLORA_ERR_WORKSPACE;
-  if (xp.splits > 1 && cudaMemsetAsync(ws + L.cnt, 0, L.cnt_end - L.cnt, cs) != cudaSuccess) return QLORA_ERR_CUDA;
+  if (xp.splits > 1 && !cleared && cudaMemsetAsync(ws + L.cnt, 0, L.cnt_end - L.cnt, cs) != cudaSuccess) return QLORA_ERR_CUDA;
   CUtensorMap x_k, a_k;
   if (!make_map(&x_k, X, sh.cols, sh.m, sh.cols * 2, 128) || !make_map(&a_k, A, sh.cols, sh.r, sh.cols * 2, 64))
     return QLORA_ERR_CUDA;

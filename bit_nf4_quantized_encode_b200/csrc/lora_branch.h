@@ -60,9 +60,10 @@ struct RankDivide {
 
 // XA = X A^T (fp32 to XA_out when asked) and bf16(s XA) [M, rpad], zero-padded
 // to a multiple of 64 columns; `div` (out null) divides the bf16 result; `flush`
-// as RankProblem's.
+// as RankProblem's; `cleared`: a kernel before has zeroed the counters [cnt, cnt_end).
 qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_t* A, float s, float* XA_out, uint8_t* ws,
-                         const XaLayout& L, const RankDivide& div, int flush, const DeviceInfo& d, cudaStream_t cs);
+                         const XaLayout& L, const RankDivide& div, int flush, bool cleared, const DeviceInfo& d,
+                         cudaStream_t cs);
 // Launch 1 of the backward (after clearing [0, clear_end)); `div` adds a divided copy of bf16(s G).
 qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uint16_t* dY, const uint16_t* A,
                              const uint16_t* B, float s, const float* XA, uint8_t* ws, BwdLayout* L,

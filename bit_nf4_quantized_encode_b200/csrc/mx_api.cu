@@ -123,8 +123,10 @@ int mx_group(int m_tiles, int64_t pitch) {
 }
 
 // q(X) into the work buffer (NVFP4: a global scale per token).
+// Words of the work buffer that a later kernel of the call counts in ([zero,
+// zero_end) bytes; a streamed product's counters by themselves) are cleared on the way.
 cudaError_t quantize_acts(const qlora_mx_tensor* W, const uint16_t* X, int64_t M, uint8_t* ws, const ProductLayout& P,
-                          const DeviceInfo& d, cudaStream_t cs) {
+                          size_t zero, size_t zero_end, const DeviceInfo& d, cudaStream_t cs) {
   const ActLayout& L = P.act;
   MxQuantArgs a{};
   a.in = X;
@@ -137,9 +139,11 @@ cudaError_t quantize_acts(const qlora_mx_tensor* W, const uint16_t* X, int64_t M
   a.kt = mx_tiles_k(W->format, W->cols);
   a.per_row = W->format == QLORA_NVFP4;
   if (M <= kMxStreamTokens) {
-    a.zero = reinterpret_cast<uint32_t*>(ws + P.counters);
-    a.zero_n = static_cast<int>((W->rows + 127) / 128 * 4);
+    zero = P.counters;
+    zero_end = zero + static_cast<size_t>((W->rows + 127) / 128) * 16;
   }
+  a.zero = reinterpret_cast<uint32_t*>(ws + zero);
+  a.zero_n = static_cast<int>((zero_end - zero) / 4);
   return counted(launch_mx_quant(W->format, false, a, d.num_sms, cs));
 }
 
@@ -382,7 +386,7 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, in
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const int few = mx_few_tile(W->format, W->rows, M, W->cols, r ? sh.lora_steps : 0, d.num_sms);
-  if (!few && quantize_acts(W, X, M, ws, L.product, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
+  if (!few && quantize_acts(W, X, M, ws, L.product, L.xa.cnt, L.xa.cnt_end, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
   const uint16_t* sxa = nullptr;
   if (r) {
     sxa = reinterpret_cast<const uint16_t*>(ws + L.xa.sxa);
@@ -393,7 +397,7 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, in
         div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
         div.all = all_div;
       }
-      if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, div, 8, d, cs)) != QLORA_OK) return st;
+      if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, div, 8, true, d, cs)) != QLORA_OK) return st;
     } else {
       MxXaArgs xa{};
       xa.x = X;
@@ -436,7 +440,7 @@ qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, c
   if ((st = device_info(&d)) != QLORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (dX && quantize_acts(WT, dY, M, ws, L.product, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
+  if (dX && quantize_acts(WT, dY, M, ws, L.product, 0, 0, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
   const uint16_t* sg = nullptr;
   if (r) {
     // G = dY B and X A^T as the backward over an NF4 weight has them
