@@ -1,5 +1,6 @@
 // mx.h -- launch interfaces of the microscaled 4-bit kernels: quantise and
-// dequantise (mx_codec.cu), the product (mx_gemm.cu) and the
+// dequantise (mx_codec.cu), the product for a token or a few (mx_few.cu), few
+// (mx_stream.cu) and many (mx_pair.cu), X A^T beside it (mx_xa.cu) and the
 // mixture-of-experts layer for a few tokens (mx_moe.cu).
 #pragma once
 #include <cuda.h>

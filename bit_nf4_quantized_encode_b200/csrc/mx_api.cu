@@ -1,6 +1,6 @@
 // mx_api.cu -- the C entry points of the microscaled 4-bit formats (declared in
 // include/qlora.h): argument validation, work-buffer layout, tensor maps and
-// launch sequences.  The kernels are in mx_codec.cu.
+// launch sequences.  mx.h names the files of the kernels.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
