@@ -114,6 +114,12 @@ qlora_status mx_layer_shape(int64_t rows, int64_t cols, int64_t M, int32_t r, Li
   return QLORA_OK;
 }
 
+// Whether a product's tiles and scale tiles can be counted and addressed in 32 bits.
+bool product_fits(int format, int64_t rows, int64_t k, int64_t m) {
+  const int64_t kt = mx_tiles_k(format, k), wt = (rows + 127) / 128, xt = (m + 127) / 128;
+  return wt * xt <= (int64_t{1} << 28) && wt * kt <= kMxMaxDim && xt * kt <= kMxMaxDim;
+}
+
 // Row tiles swept across all token tiles before the next group: about 48 MB of
 // weight codes, so that they stay in L2 meanwhile.
 int mx_group(int m_tiles, int64_t pitch) {
@@ -183,7 +189,6 @@ qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const
   a.out = out;
   const int64_t m_tiles = pair ? (W->rows + 255) / 256 : (W->rows + 127) / 128, t_tiles = (M + bn - 1) / bn;
   const int64_t w_tiles = (W->rows + 127) / 128 * a.kt, x_tiles = (M + 127) / 128 * a.kt;
-  if (m_tiles * t_tiles > (int64_t{1} << 28) || w_tiles > kMxMaxDim || x_tiles > kMxMaxDim) return QLORA_ERR_SHAPE;
   a.m_tiles = static_cast<int>(m_tiles);
   a.t_tiles = static_cast<int>(t_tiles);
   a.m_group = mx_group(a.m_tiles, 2 * pitch);
@@ -373,6 +378,7 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, in
   if (st != QLORA_OK) return st;
   LinearShape sh{};
   if ((st = mx_layer_shape(W->rows, W->cols, M, r, &sh)) != QLORA_OK) return st;
+  if (!product_fits(W->format, W->rows, W->cols, M)) return QLORA_ERR_SHAPE;
   if (r && W->scale_per_row) return QLORA_ERR_UNSUPPORTED;
   if (!X || !Y || !workspace || (r && (!A || !B))) return QLORA_ERR_NULL;
   if (!aligned16(X) || !aligned16(Y) || !aligned16(workspace) ||
@@ -427,6 +433,7 @@ qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, c
   const int64_t rows = WT->cols, cols = WT->rows;          // the layer's W is [rows, cols]
   LinearShape sh{};
   if ((st = mx_layer_shape(rows, cols, M, r, &sh)) != QLORA_OK) return st;
+  if (!product_fits(WT->format, cols, rows, M)) return QLORA_ERR_SHAPE;
   if (r && WT->scale_per_row) return QLORA_ERR_UNSUPPORTED;
   if (!dY || !workspace || (!r && !dX) || (r && (!X || !A || !B || !dA || !dB))) return QLORA_ERR_NULL;
   if (!aligned16(dY) || !aligned16(workspace) || (dX && !aligned16(dX)) ||

@@ -121,6 +121,9 @@ def test_linear_refusals():
     assert f(*args(w=_t(64, 72))) == ERR_SHAPE and f(*args(w=_t(60, 128))) == ERR_SHAPE
     assert f(*args(w=_t(0, 128))) == ERR_SHAPE and f(*args(w=_t(64, 128, 7))) == ERR_UNSUP
     assert f(*args(w=_t(64, 128, 1, 1))) == ERR_UNSUP                     # a scale per weight row with an adapter
+    far = _t((1 << 31) - 256, (1 << 31) - 256)                           # more scale tiles than 32 bits count
+    assert f(far, p, 4, None, None, 0, s, p, None, p, 1 << 62, None) == ERR_SHAPE
+    assert b(far, None, p, 4, None, None, 0, s, None, p, None, None, p, 1 << 62, None) == ERR_SHAPE
     assert f(*args(n=64)) == ERR_WS and f(W, p, 4, None, None, 0, s, p, None, p, 64, None) == ERR_WS
     assert f(W, p, 4, p, p, 8, ctypes.c_float(float("inf")), p, None, p, 1 << 40, None) == ERR_SHAPE
     bargs = lambda dx=p, da=p, x=p, r=8, xa=None, n=1 << 40: (W, x, p, 4, p, p, r, s, xa, dx, da, p, p, n, None)  # noqa: E731
