@@ -16,7 +16,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libqlora.so")
 SOURCES = ["api.cu", "codec.cu", "gemm.cu", "gemv.cu", "lora.cu", "lora_branch.cu", "mx_api.cu",
            "mx_codec.cu", "mx_few.cu", "mx_moe.cu", "mx_pair.cu", "mx_stream.cu", "mx_xa.cu", "noalloc.cu", "selftest.cu", "nf4_tables.cpp"]
-HEADERS = ["codec.h", "gemm.h", "gemv.h", "internal.h", "lora.h", "lora_branch.h", "mx.h", "mx_encode.cuh", "mx_format.cuh", "mx_ptx.cuh", "mx_runs.cuh",
+HEADERS = ["bf16_parts.cuh", "codec.h", "gemm.h", "gemv.h", "internal.h", "lora.h", "lora_branch.h", "mx.h", "mx_encode.cuh", "mx_format.cuh", "mx_ptx.cuh", "mx_runs.cuh",
            "nf4_device.cuh", "nf4_tables.h", "sm100_ptx.cuh"]
 
 

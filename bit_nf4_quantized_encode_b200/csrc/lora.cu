@@ -28,6 +28,7 @@
 #include <atomic>
 #include <cstdint>
 
+#include "bf16_parts.cuh"
 #include "lora.h"
 #include "mx_ptx.cuh"
 
@@ -73,11 +74,18 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// First and second parts of two values, packed.
+__device__ __forceinline__ void bf16_parts2(float a, float b, uint32_t& first, uint32_t& second) {
+  const BfParts x = bf16_parts(a), y = bf16_parts(b);
+  first = pack_bf16x2(x.first, y.first);
+  second = pack_bf16x2(x.second, y.second);
+}
+
 // bf16(s * v) of row `row`, columns c0 .. c0 + 63 below bf16_cols; columns past
 // ndim hold zeros (zero-filled operand).
-__device__ __forceinline__ void store_bf16_row(const RankProblem& p, uint16_t* out, int64_t row, int64_t c0,
-                                               const float (&v)[64], float s) {
-  uint16_t* dst = out + row * p.ld_bf16 + c0;
+__device__ __forceinline__ void store_bf16_row(const RankProblem& p, int64_t row, int64_t c0, const float (&v)[64]) {
+  uint16_t* dst = p.out_bf16 + row * p.ld_bf16 + c0;
+  const float s = p.bf16_scale;
 #pragma unroll
   for (int c = 0; c < 64; c += 8)
     if (c0 + c < p.bf16_cols) {
@@ -88,6 +96,19 @@ __device__ __forceinline__ void store_bf16_row(const RankProblem& p, uint16_t* o
       q.w = pack_bf16x2(__fmul_rn(s, v[c + 6]), __fmul_rn(s, v[c + 7]));
       *reinterpret_cast<uint4*>(dst + c) = q;
     }
+}
+
+// v as two bf16 parts (lora.h), 64 columns: v rounded, then what is left of it
+// rounded (nothing where the first part is not finite).
+__device__ __forceinline__ void store_parts_row(uint16_t* dst, const float (&v)[64]) {
+#pragma unroll
+  for (int c = 0; c < 64; c += 8) {
+    uint32_t first[4], second[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bf16_parts2(v[c + 2 * i], v[c + 2 * i + 1], first[i], second[i]);
+    *reinterpret_cast<uint4*>(dst + c) = make_uint4(first[0], first[1], first[2], first[3]);
+    *reinterpret_cast<uint4*>(dst + 64 + c) = make_uint4(second[0], second[1], second[2], second[3]);
+  }
 }
 
 // The final values of row `row`, columns c0 .. c0 + 63 of problem p's D.
@@ -105,14 +126,14 @@ __device__ __forceinline__ void store_final(const RankProblem& p, int64_t row, i
         if (c0 + c < p.ndim) *reinterpret_cast<float4*>(dst + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
     }
   }
-  if (p.out_bf16) store_bf16_row(p, p.out_bf16, row, c0, v, p.bf16_scale);
-  if (p.out_div) {
+  if (p.out_bf16) store_bf16_row(p, row, c0, v);
+  if (p.out_parts && c0 < p.bf16_cols) {
     // one divisor after the other: their product may be below what a float holds
-    const float by_row = 1.0f / p.row_div[row], by_all = 1.0f / p.all_div[0];
+    const float by_row = p.row_div ? 1.0f / p.row_div[row] : 1.0f, by_all = p.row_div ? 1.0f / p.all_div[0] : 1.0f;
     float d[64];
 #pragma unroll
-    for (int c = 0; c < 64; ++c) d[c] = __fmul_rn(__fmul_rn(p.bf16_scale, v[c]), by_row);
-    store_bf16_row(p, p.out_div, row, c0, d, by_all);
+    for (int c = 0; c < 64; ++c) d[c] = __fmul_rn(__fmul_rn(__fmul_rn(p.bf16_scale, v[c]), by_row), by_all);
+    store_parts_row(p.out_parts + row * (2 * p.bf16_cols) + 2 * c0, d);
   }
 }
 

@@ -31,9 +31,12 @@ struct RankProblem {
   int64_t ld_bf16;
   int64_t bf16_cols;         // a multiple of 64, <= 64 * n_tiles
   float bf16_scale;
-  // optional: bf16(bf16_scale * D / row_div[row] / all_div[0]), shaped as out_bf16
-  // (the rank-r operand of a product whose accumulator is scaled at its end)
-  uint16_t* out_div;
+  // optional: v = bf16_scale * D [/ row_div[row] / all_div[0]] as two bf16 parts whose
+  // sum is within 2^-17 of it, bf16(v) and bf16(v - bf16(v)): [mdim][2 bf16_cols],
+  // after 64 first parts the 64 second ones.  The rank-r operand of a product, and
+  // where that product's accumulator is scaled at its end, divided by the scales
+  // (row_div null: not).
+  uint16_t* out_parts;
   const float* row_div;
   const float* all_div;
   // split contraction (splits > 1): fp32 partial tiles and per-tile counters,

@@ -86,7 +86,7 @@ size_t sized_slots(int tiles, int ksteps) {
 
 // Work buffer layout, in bytes, each offset 256-aligned; every size is
 // independent of the device.
-XaLayout xa_layout(const LinearShape& s, size_t base) {
+XaLayout xa_layout(const LinearShape& s, int parts, size_t base) {
   XaLayout l{};
   const RankPlan xa = rank_tiling(s.m, s.cols, s.lora_steps);
   size_t o = base;
@@ -94,7 +94,7 @@ XaLayout xa_layout(const LinearShape& s, size_t base) {
   l.cnt_end = o;
   l.slot_bytes = sized_slots(xa.tiles(), xa.ksteps);
   l.slots = o; o = round_up(o + l.slot_bytes, 256);
-  l.sxa = o;   o = round_up(o + size_t(s.m) * s.rpad * 2, 256);
+  l.sxa = o;   o = round_up(o + size_t(s.m) * s.rpad * 2 * parts, 256);
   l.end = o;
   return l;
 }
@@ -128,7 +128,7 @@ BwdLayout bwd_layout(const LinearShape& s) {
 }
 
 qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_t* A, float s, float* XA_out, uint8_t* ws,
-                         const XaLayout& L, const RankDivide& div, int flush, bool cleared, const DeviceInfo& d,
+                         const XaLayout& L, const RankParts& parts, int flush, bool cleared, const DeviceInfo& d,
                          cudaStream_t cs) {
   RankPlan xp = rank_tiling(sh.m, sh.cols, sh.lora_steps);
   xp.splits = launch_splits(xp.tiles(), xp.ksteps, d.num_sms, L.slot_bytes);
@@ -143,11 +143,10 @@ qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_
   ra.p[0].flush = flush;
   ra.p[0].out_f32 = XA_out; ra.p[0].ld_f32 = sh.r;
   ra.p[0].ld_bf16 = sh.rpad; ra.p[0].bf16_cols = sh.rpad; ra.p[0].bf16_scale = s;
-  uint16_t* sxa = reinterpret_cast<uint16_t*>(ws + L.sxa);
-  if (div.row) {
-    ra.p[0].row_div = div.row; ra.p[0].all_div = div.all; ra.p[0].out_div = sxa;
+  if (parts.out) {
+    ra.p[0].out_parts = parts.out; ra.p[0].row_div = parts.row; ra.p[0].all_div = parts.all;
   } else {
-    ra.p[0].out_bf16 = sxa;
+    ra.p[0].out_bf16 = reinterpret_cast<uint16_t*>(ws + L.sxa);
   }
   ra.nprob = 1;
   ra.total_units = xp.tiles() * xp.splits;
@@ -157,7 +156,7 @@ qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_
 
 qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uint16_t* dY, const uint16_t* A,
                              const uint16_t* B, float s, const float* XA, uint8_t* ws, BwdLayout* L,
-                             const RankDivide& div, const DeviceInfo& d, cudaStream_t cs) {
+                             const RankParts& parts, const DeviceInfo& d, cudaStream_t cs) {
   float* g32 = sh.decode ? reinterpret_cast<float*>(ws + L->g) : nullptr;     // fp32 G and X A^T: few-token grads
   float* xa32 = sh.decode ? reinterpret_cast<float*>(ws + L->xa) : nullptr;
   uint16_t* sg = reinterpret_cast<uint16_t*>(ws + L->sg);
@@ -192,7 +191,7 @@ qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uin
     ra.p[0] = rank_problem(L->g_plan, sh.m, sh.r, false, true, 0, slots, cnt);
     ra.p[0].out_f32 = g32; ra.p[0].ld_f32 = sh.rpad;
     ra.p[0].out_bf16 = sg; ra.p[0].ld_bf16 = sh.rpad; ra.p[0].bf16_cols = sh.rpad; ra.p[0].bf16_scale = s;
-    ra.p[0].row_div = div.row; ra.p[0].all_div = div.all; ra.p[0].out_div = div.out;
+    ra.p[0].out_parts = parts.out; ra.p[0].row_div = parts.row; ra.p[0].all_div = parts.all;
     ra.nprob = 1;
     ra.total_units = L->g_plan.tiles() * L->g_plan.splits;
     if (recompute) {

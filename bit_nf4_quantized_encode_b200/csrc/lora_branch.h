@@ -34,11 +34,12 @@ RankPlan rank_tiling(int64_t mdim, int64_t contraction, int lora_steps);
 size_t sized_slots(int tiles, int ksteps);
 
 // Work space of X A^T -> bf16(s X A^T) (offsets from `base`): counters (cleared
-// by the launch when it splits), partial tiles, the bf16 [M, rpad] result.
+// by the launch when it splits), partial tiles, the bf16 [M, parts * rpad] result
+// (parts: 1 rounded, 2 as RankProblem::out_parts).
 struct XaLayout {
   size_t cnt, cnt_end, slots, slot_bytes, sxa, end;
 };
-XaLayout xa_layout(const LinearShape& s, size_t base);
+XaLayout xa_layout(const LinearShape& s, int parts, size_t base);
 
 // Backward: launch 1 = dY B (and X A^T when it is not supplied), launch 2 =
 // dX, launch 3 = dY^T (s X A^T) and X^T (s dY B) (more than 16 tokens; with
@@ -50,24 +51,24 @@ struct BwdLayout {
 };
 BwdLayout bwd_layout(const LinearShape& s);
 
-// Divisors of the rank-r activations of a product whose accumulator is scaled
-// at its end: bf16(s v / row[i] / all[0]) goes to `out`; row null: none.
-struct RankDivide {
+// The rank-r activations in two bf16 parts (RankProblem::out_parts) in `out`, null:
+// none; divided by row[i] and all[0] unless row is null.
+struct RankParts {
+  uint16_t* out = nullptr;
   const float* row = nullptr;
   const float* all = nullptr;
-  uint16_t* out = nullptr;
 };
 
 // XA = X A^T (fp32 to XA_out when asked) and bf16(s XA) [M, rpad], zero-padded
-// to a multiple of 64 columns; `div` (out null) divides the bf16 result; `flush`
-// as RankProblem's; `cleared`: a kernel before has zeroed the counters [cnt, cnt_end).
+// to a multiple of 64 columns, or `parts` in its place; `flush` as RankProblem's;
+// `cleared`: a kernel before has zeroed the counters [cnt, cnt_end).
 qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_t* A, float s, float* XA_out, uint8_t* ws,
-                         const XaLayout& L, const RankDivide& div, int flush, bool cleared, const DeviceInfo& d,
+                         const XaLayout& L, const RankParts& parts, int flush, bool cleared, const DeviceInfo& d,
                          cudaStream_t cs);
-// Launch 1 of the backward (after clearing [0, clear_end)); `div` adds a divided copy of bf16(s G).
+// Launch 1 of the backward (after clearing [0, clear_end)); `parts`: s G for dX, beside bf16(s G).
 qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uint16_t* dY, const uint16_t* A,
                              const uint16_t* B, float s, const float* XA, uint8_t* ws, BwdLayout* L,
-                             const RankDivide& div, const DeviceInfo& d, cudaStream_t cs);
+                             const RankParts& parts, const DeviceInfo& d, cudaStream_t cs);
 // Launch 3: dA and dB.
 qlora_status run_lora_grads(const LinearShape& sh, const uint16_t* X, const uint16_t* dY, float s, const float* XA,
                             float* dA, float* dB, uint8_t* ws, BwdLayout* L, const DeviceInfo& d, cudaStream_t cs);

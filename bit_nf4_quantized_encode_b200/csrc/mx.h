@@ -67,7 +67,7 @@ struct MxGemmArgs {
   const float* x_global;     // NVFP4: [m]
   int64_t rows, m, k;
   int ksteps;                // ceil(k / 256)
-  int lora_steps;            // 64-wide steps of the rank-r term (0: none)
+  int lora_steps;            // 64 ranks each of the rank-r term (0: none), its activations in two bf16 parts
   int lora_mn;               // its weight-side operand: 0 [rows, r], 1 [r, rows] (rows contiguous)
   uint16_t* out;             // bf16 [m, rows]
   int m_tiles, t_tiles;      // tiles of rows (128, of a pair 256) and of tokens
@@ -82,7 +82,7 @@ struct MxGemmArgs {
 // {128, 128} / {128, x rows}; w_scales / x_scales the scale tiles as 32-bit
 // words [row tiles * kt][128], box {128, 2 (MXFP4) or 4} (pairs only); lora_w
 // bf16, box {64, 128} ([rows, r]) or {64, 64} ([r, rows]); lora_x bf16
-// [m, 64 lora_steps], box {64, x rows}.
+// [m, 128 lora_steps] (after 64 ranks' first parts their second ones), box {64, x rows}.
 struct MxMaps {
   CUtensorMap w, x, w_scales, x_scales, lora_w, lora_x;
 };
@@ -125,7 +125,8 @@ struct MxXaArgs {
   int m, r, rpad;
   float s;
   float* xa;                 // fp32 [m, r] or null
-  uint16_t* sxa;             // bf16 [m, rpad]: s X A^T [/ (g all_div)], zero from column r
+  uint16_t* sxa;             // bf16 [m, 2 rpad]: s X A^T [/ (g all_div)], zero from column r, in two
+                             // parts (RankProblem::out_parts)
   const float* all_div;      // [1]: divide by it and the token's NVFP4 global scale g; or null
   // the first kernel of its call starts when all before it has ended, a later one
   // beside the one before

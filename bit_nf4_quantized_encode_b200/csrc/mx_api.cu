@@ -80,28 +80,31 @@ ProductLayout product_layout(int format, int64_t rows, int64_t k, int64_t m, siz
   return l;
 }
 
+// The rank-r activations of a product, two bf16 parts (RankProblem::out_parts).
+size_t parts_bytes(int64_t m, const LinearShape& sh) { return static_cast<size_t>(m) * sh.rpad * 4; }
+
 struct MxFwdLayout {
   XaLayout xa;             // of its members only sxa for few tokens
   ProductLayout product;
 };
 MxFwdLayout mx_fwd_layout(int format, int64_t rows, int64_t cols, int64_t m, int r, const LinearShape& sh) {
   MxFwdLayout l{};
-  if (r && m > kMxStreamTokens) l.xa = xa_layout(sh, 0);
-  else if (r) l.xa.end = round_up(static_cast<size_t>(m) * sh.rpad * 2, 256);
+  if (r && m > kMxStreamTokens) l.xa = xa_layout(sh, 2, 0);
+  else if (r) l.xa.end = round_up(parts_bytes(m, sh), 256);
   l.product = product_layout(format, rows, cols, m, l.xa.end);
   return l;
 }
 struct MxBwdLayout {
   BwdLayout lora;
-  size_t sg_div;           // NVFP4: bf16(s G / (gx gw))
+  size_t sg_parts;         // s G [/ (gx gw)] for dX
   ProductLayout product;
 };
 MxBwdLayout mx_bwd_layout(int format, int64_t rows, int64_t cols, int64_t m, int r, const LinearShape& sh) {
   MxBwdLayout l{};
   if (r) l.lora = bwd_layout(sh);
   size_t o = round_up(l.lora.total, 256);
-  l.sg_div = o;
-  if (r && format == QLORA_NVFP4) o = round_up(o + static_cast<size_t>(m) * sh.rpad * 2, 256);
+  l.sg_parts = o;
+  if (r) o = round_up(o + parts_bytes(m, sh), 256);
   l.product = product_layout(format, cols, rows, m, o);
   return l;
 }
@@ -162,7 +165,8 @@ int pair_token_tile(int64_t rows, int64_t m, int num_sms) {
   return narrow < wide ? 128 : 256;
 }
 
-// out [M, W->rows] = q(X) deq(W)^T + lora_x lora_w (see mx_stream.cu).
+// out [M, W->rows] = q(X) deq(W)^T + lora_x lora_w (see mx_stream.cu); lora_x in two
+// bf16 parts, [M][2 * 64 lora_steps].
 qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const ProductLayout& P, const uint16_t* lora_w,
                          bool lora_mn, const uint16_t* lora_x, int r, int lora_steps, uint16_t* out,
                          const DeviceInfo& d, cudaStream_t cs) {
@@ -202,10 +206,10 @@ qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const
                    CU_TENSOR_MAP_SWIZZLE_128B))
     return QLORA_ERR_CUDA;
   if (lora_steps) {
-    const uint64_t rpad = static_cast<uint64_t>(lora_steps) * 64, n = static_cast<uint64_t>(W->rows);
+    const uint64_t both = static_cast<uint64_t>(lora_steps) * 128, n = static_cast<uint64_t>(W->rows);
     if (!(lora_mn ? make_map(&m.lora_w, lora_w, n, r, n * 2, 64)
                   : make_map(&m.lora_w, lora_w, r, n, static_cast<uint64_t>(r) * 2, 128)) ||
-        !make_map(&m.lora_x, lora_x, rpad, static_cast<uint64_t>(M), rpad * 2, static_cast<uint32_t>(box_x)))
+        !make_map(&m.lora_x, lora_x, both, static_cast<uint64_t>(M), both * 2, static_cast<uint32_t>(box_x)))
       return QLORA_ERR_CUDA;
   } else {
     m.lora_w = m.w;
@@ -248,9 +252,9 @@ qlora_status run_mx_few(const qlora_mx_tensor* W, const uint16_t* X, int64_t M, 
   const uint64_t up = static_cast<uint64_t>(mx_pitch(W->cols)), n = static_cast<uint64_t>(W->rows);
   if (!make_map_u8(&m.w, W->codes, up, n, up, 128, 32, CU_TENSOR_MAP_SWIZZLE_128B)) return QLORA_ERR_CUDA;
   if (lora_steps) {
-    const uint64_t rpad = static_cast<uint64_t>(lora_steps) * 64;
+    const uint64_t both = static_cast<uint64_t>(lora_steps) * 128;
     if (!make_map(&m.lora_w, lora_w, r, n, static_cast<uint64_t>(r) * 2, 32) ||
-        !make_map(&m.lora_x, lora_x, rpad, static_cast<uint64_t>(M), rpad * 2, static_cast<uint32_t>(tile)))
+        !make_map(&m.lora_x, lora_x, both, static_cast<uint64_t>(M), both * 2, static_cast<uint32_t>(tile)))
       return QLORA_ERR_CUDA;
   } else {
     m.lora_w = m.lora_x = m.w;
@@ -398,12 +402,13 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, in
     sxa = reinterpret_cast<const uint16_t*>(ws + L.xa.sxa);
     const float* all_div = W->format == QLORA_NVFP4 ? W->global_scale : nullptr;
     if (M > kMxStreamTokens) {
-      RankDivide div;
+      RankParts parts;
+      parts.out = reinterpret_cast<uint16_t*>(ws + L.xa.sxa);
       if (all_div) {
-        div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
-        div.all = all_div;
+        parts.row = reinterpret_cast<const float*>(ws + L.product.act.global);
+        parts.all = all_div;
       }
-      if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, div, 8, true, d, cs)) != QLORA_OK) return st;
+      if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, parts, 8, true, d, cs)) != QLORA_OK) return st;
     } else {
       MxXaArgs xa{};
       xa.x = X;
@@ -451,15 +456,15 @@ qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, c
   const uint16_t* sg = nullptr;
   if (r) {
     // G = dY B and X A^T as the backward over an NF4 weight has them
-    RankDivide div;
-    sg = reinterpret_cast<const uint16_t*>(ws + L.lora.sg);
-    if (dX && WT->format == QLORA_NVFP4) {
-      div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
-      div.all = WT->global_scale;
-      div.out = reinterpret_cast<uint16_t*>(ws + L.sg_div);
-      sg = div.out;
+    RankParts parts;
+    if (dX) {
+      sg = parts.out = reinterpret_cast<uint16_t*>(ws + L.sg_parts);
+      if (WT->format == QLORA_NVFP4) {
+        parts.row = reinterpret_cast<const float*>(ws + L.product.act.global);
+        parts.all = WT->global_scale;
+      }
     }
-    if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L.lora, div, d, cs)) != QLORA_OK) return st;
+    if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L.lora, parts, d, cs)) != QLORA_OK) return st;
   }
   if (dX && (st = run_mx_gemm(WT, M, ws, L.product, A, true, sg, r, r ? sh.lora_steps : 0, dX, d, cs)) != QLORA_OK) return st;
   return r ? run_lora_grads(sh, X, dY, s, XA, dA, dB, ws, &L.lora, d, cs) : QLORA_OK;

@@ -168,8 +168,8 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
     if (a.lora_steps != 0) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
       if (elect_one()) {
-        mbar_arrive_expect_tx(l_full, static_cast<uint32_t>(a.lora_steps) * kN * 128);
-        for (int i = 0; i < a.lora_steps; ++i) tma_load_2d(smem_gen + l_off + i * (kN * 128), &lxmap, i * 64, 0, l_full);
+        mbar_arrive_expect_tx(l_full, static_cast<uint32_t>(2 * a.lora_steps) * kN * 128);
+        for (int i = 0; i < 2 * a.lora_steps; ++i) tma_load_2d(smem_gen + l_off + i * (kN * 128), &lxmap, i * 64, 0, l_full);
       }
       __syncwarp();
     }
@@ -220,12 +220,16 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
                 }
               }
           } else {
-            const uint64_t bd = desc0 + ((l_off + (j - a.ksteps) * (kN * 128)) >> 4);
+            const uint64_t bd = desc0 + ((l_off + (j - a.ksteps) * (2 * kN * 128)) >> 4);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int p = 0; p < 2; ++p)                                  // the activations' two bf16 parts
 #pragma unroll
-              for (int i = 0; i < kTiles; ++i)
-                if (i < k.tiles) mma_bf16_ss(d + i * kN, ad + i * 1024 + q * 2, bd + q * 2, idesc_bf16(128, kN, false, false), 1u);
+              for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i)
+                  if (i < k.tiles)
+                    mma_bf16_ss(d + i * kN, ad + i * 1024 + q * 2, bd + p * (kN * 128 >> 4) + q * 2,
+                                idesc_bf16(128, kN, false, false), 1u);
           }
           mma_commit(&empty[stage]);
           if (j == per_chunk - 1) mma_commit(&acc_full[c & 1]);
@@ -320,7 +324,7 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
 // Shared memory behind the weight's stages.
 size_t tokens_bytes(int fmt, int n, int ksteps, int lora_steps) {
   return (static_cast<size_t>(ksteps) * (n * 128 + token_scales(fmt, n)) + 512 + 1023) / 1024 * 1024 +
-         static_cast<size_t>(lora_steps) * n * 128;
+         static_cast<size_t>(2 * lora_steps) * n * 128;
 }
 
 template <int kFmt, int kN>

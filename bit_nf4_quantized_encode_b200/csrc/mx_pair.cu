@@ -80,7 +80,7 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
   const uint32_t rank = cluster_rank();
   const int ntiles = a.m_tiles * a.t_tiles;
   const int first = static_cast<int>(blockIdx.x) >> 1, stride = static_cast<int>(gridDim.x) >> 1;
-  const int nk = a.ksteps + a.lora_steps;
+  const int nk = a.ksteps + 2 * a.lora_steps;      // each 64 ranks twice: the activations' two bf16 parts
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -136,7 +136,7 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
             for (int b = 0; b < kRB; ++b)
               tma_load_2d_pair(sSb + b * (kAtoms * 512), &xsmap, 0, xs0 + b * static_cast<int>(a.kt) + j * kAtoms, bar);
           } else {
-            const int r0 = (j - a.ksteps) * 64;
+            const int part = j - a.ksteps, r0 = (part >> 1) * 64;
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (kABytes + kBBytes));
             if (a.lora_mn) {
               tma_load_2d_pair(sA, &lwmap, row0, r0, bar);
@@ -144,7 +144,7 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
             } else {
               tma_load_2d_pair(sA, &lwmap, r0, row0, bar);
             }
-            tma_load_2d_pair(sB, &lxmap, r0, tok0, bar);
+            tma_load_2d_pair(sB, &lxmap, part * 64, tok0, bar);
           }
         }
         __syncwarp();

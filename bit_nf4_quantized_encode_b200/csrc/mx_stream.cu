@@ -9,8 +9,9 @@
 // the contraction a stage holds 128 bytes of codes per row and the scale tiles,
 // which tcgen05.cp moves to TMEM.  The weight is the M operand (128 rows), the
 // tokens the N operand.  The rank-r term is a bf16 x bf16 product accumulated
-// into the same TMEM tile (64 ranks a step); with global scales its activation
-// side arrives divided by gx gw.
+// into the same TMEM tile (64 ranks a step); its activation side arrives in two
+// bf16 parts (bf16_parts.cuh) that meet the same weight tile, and with global
+// scales divided by gx gw.
 //
 // The weight's bytes bound it, so every SM has to stream all the time: the steps
 // of all row tiles are dealt to the SMs in equal runs (mx_runs.cuh).
@@ -74,8 +75,9 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
 
   const int warp = warp_index();
   const int lane = threadIdx.x & 31;
-  // steps of a tile: ksteps of 512, then the rank-r ones
-  const int ksteps = (a.ksteps + kSub - 1) / kSub, per_tile = ksteps + (a.lora_steps + kSub - 1) / kSub;
+  // steps of a tile: ksteps of 512, then the rank-r ones of 64 (two pieces of activations, one of weight)
+  static_assert(kSub == 2);
+  const int ksteps = (a.ksteps + kSub - 1) / kSub, per_tile = ksteps + a.lora_steps;
   const int64_t total = static_cast<int64_t>(a.m_tiles) * per_tile;
   const int runs = static_cast<int>(gridDim.x);
   const int64_t begin = run_begin(total, static_cast<int>(blockIdx.x), runs);
@@ -126,18 +128,14 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
                       static_cast<uint32_t>(min(kAtoms, atoms - p * kAtoms) * 512), &full[stage]);
           }
       } else {
-        const int r0 = (j - ksteps) * kSub, pieces = min(kSub, a.lora_steps - r0);
-        mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(pieces * (kABytes + kBN * 128)));
-#pragma unroll
-        for (int p = 0; p < kSub; ++p)
-          if (p < pieces) {
-            if (a.lora_mn) {
-              tma_load_2d(sA + p * kPiece, &lwmap, tile * 128, (r0 + p) * 64, &full[stage]);
-              tma_load_2d(sA + p * kPiece + 8192, &lwmap, tile * 128 + 64, (r0 + p) * 64, &full[stage]);
-            } else {
-              tma_load_2d(sA + p * kPiece, &lwmap, (r0 + p) * 64, tile * 128, &full[stage]);
-            }
-          }
+        const int r0 = (j - ksteps) * 64;
+        mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(kABytes + 2 * kBN * 128));
+        if (a.lora_mn) {
+          tma_load_2d(sA, &lwmap, tile * 128, r0, &full[stage]);
+          tma_load_2d(sA + 8192, &lwmap, tile * 128 + 64, r0, &full[stage]);
+        } else {
+          tma_load_2d(sA, &lwmap, r0, tile * 128, &full[stage]);
+        }
       }
     };
     auto load_x = [&](int stage, int j) {
@@ -154,10 +152,8 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
                       static_cast<uint32_t>(min(kAtoms, atoms - p * kAtoms) * 512), &full[stage]);
           }
       } else {
-        const int r0 = (j - ksteps) * kSub, pieces = min(kSub, a.lora_steps - r0);
 #pragma unroll
-        for (int p = 0; p < kSub; ++p)
-          if (p < pieces) tma_load_2d(sB + p * kPiece, &lxmap, (r0 + p) * 64, 0, &full[stage]);
+        for (int p = 0; p < 2; ++p) tma_load_2d(sB + p * kPiece, &lxmap, (j - ksteps) * 128 + p * 64, 0, &full[stage]);
       }
     };
     const int early = min(kStages, nsteps);
@@ -234,15 +230,11 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
           // A K = 16 slice: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
           const uint64_t la = a.lora_mn ? smem_desc_sw128(smem0, 8192, 1024) + off : ad;
           const uint32_t step = a.lora_mn ? 2048 >> 4 : 32 >> 4;
-          const int pieces = min(kSub, a.lora_steps - (j - ksteps) * kSub);
 #pragma unroll
-          for (int p = 0; p < kSub; ++p)
-            if (p < pieces) {
+          for (int p = 0; p < 2; ++p)
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                mma_bf16_ss(d, la + (p * kPiece >> 4) + q * step, bd + (p * kPiece >> 4) + q * 2, lora_idesc,
-                            !fresh || p + q != 0 ? 1u : 0u);
-            }
+            for (int q = 0; q < 4; ++q)
+              mma_bf16_ss(d, la + q * step, bd + (p * kPiece >> 4) + q * 2, lora_idesc, !fresh || p + q != 0 ? 1u : 0u);
         }
         mma_commit(&empty[stage]);
         if (last) mma_commit(&acc_full[ab]);
@@ -343,8 +335,7 @@ cudaError_t launch_t(const MxGemmArgs& a, const MxMaps& m, int num_sms, cudaStre
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  const int64_t steps =
-      static_cast<int64_t>(a.m_tiles) * ((a.ksteps + kSub - 1) / kSub + (a.lora_steps + kSub - 1) / kSub);
+  const int64_t steps = static_cast<int64_t>(a.m_tiles) * ((a.ksteps + kSub - 1) / kSub + a.lora_steps);
   int grid = num_sms < kMxMaxRuns ? num_sms : kMxMaxRuns;
   if (steps < grid) grid = static_cast<int>(steps);
   cudaLaunchConfig_t cfg{};

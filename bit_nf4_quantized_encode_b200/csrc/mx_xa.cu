@@ -12,6 +12,7 @@
 
 #include <cstdint>
 
+#include "bf16_parts.cuh"
 #include "mx.h"
 #include "mx_encode.cuh"
 #include "mx_ptx.cuh"
@@ -101,8 +102,10 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) k_m
     v = __fmul_rn(a.s, v);
     // one divisor after the other: their product may be below what a float holds
     if (a.all_div) v = __fdiv_rn(__fmul_rn(v, mx_pow2_inverse(mx_global_scale(s_amax[tt] << 16))), a.all_div[0]);
-    const __nv_bfloat16 b = __float2bfloat16_rn(v);
-    a.sxa[static_cast<int64_t>(tok) * a.rpad + rank_row] = *reinterpret_cast<const uint16_t*>(&b);
+    const BfParts p = bf16_parts(v);
+    uint16_t* dst = a.sxa + static_cast<int64_t>(tok) * (2 * a.rpad) + (rank_row >> 6) * 128 + (rank_row & 63);
+    dst[0] = bf16_bits(p.first);
+    dst[64] = bf16_bits(p.second);
   }
 }
 

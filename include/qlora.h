@@ -319,8 +319,9 @@ QLORA_EXPORT qlora_status qlora_mx_linear_workspace_size(int64_t rows, int64_t c
  * X [M, cols] bf16, Y [M, rows] bf16; sums are fp32, Y is rounded once.
  *   r = 0: no adapter; A, B and XA_out are ignored, any rows, cols, M >= 1.
  *   r > 0: A [r, cols], B [rows, r] bf16 and XA_out [M, r] float (or NULL) with
- *   the requirements of qlora_linear_fwd; the rank-r term is taken as
- *   bf16(s X A^T) B^T.  Not with scale_per_row (QLORA_ERR_UNSUPPORTED).
+ *   the requirements of qlora_linear_fwd; in the rank-r term s X A^T is carried
+ *   as the sum of two bf16 numbers, within 2^-17 of each element.  Not with
+ *   scale_per_row (QLORA_ERR_UNSUPPORTED).
  * Bit-reproducible from run to run on the same device.
  */
 QLORA_EXPORT qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, int64_t M, const uint16_t* A,
@@ -332,7 +333,7 @@ QLORA_EXPORT qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const ui
  * quantised along the weight's rows (qlora_mx_quantize with transpose = 1), so
  * that this product too takes two 4-bit operands; q is passed straight through:
  *   G  = dY B
- *   dX = deq(q(dY)) deq(WT)^T + s G A     [M, cols] bf16 (skipped when dX is NULL)
+ *   dX = deq(q(dY)) deq(WT)^T + s G A     [M, cols] bf16 (skipped when dX is NULL); s G as s X A^T of the forward
  *   dB = s dY^T (X A^T), dA = s G^T X     [rows, r], [r, cols] float, as qlora_linear_bwd
  * WT [cols, rows], dY [M, rows].  r = 0: no adapter; X, A, B, XA, dA, dB are
  * ignored and dX is required.  XA: X A^T of the forward, or NULL to recompute it.
