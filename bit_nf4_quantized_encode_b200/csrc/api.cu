@@ -407,7 +407,7 @@ qlora_status qlora_linear_workspace_size(int64_t rows, int64_t cols, int64_t M, 
   const qlora_status st = linear_shape(rows, cols, M, r, &sh);
   if (st != QLORA_OK) return st;
   if (fwd_bytes) *fwd_bytes = fwd_layout(sh).total;
-  if (bwd_bytes) *bwd_bytes = bwd_layout(sh).total;
+  if (bwd_bytes) *bwd_bytes = bwd_layout(sh, 1).total;
   return QLORA_OK;
 }
 
@@ -436,7 +436,7 @@ qlora_status qlora_linear_fwd(const qlora_nf4_tensor* W, const uint16_t* X, int6
   // 1) X A^T (fp32 to XA_out when asked) and bf16(s X A^T), zero-padded to a
   //    multiple of 64 columns, as the LoRA k-step operand of the fused GEMM
   uint16_t* sxa = reinterpret_cast<uint16_t*>(ws + L.xa.sxa);
-  if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, RankParts(), 0, false, d, cs)) != QLORA_OK) return st;
+  if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, 1, RankDivide(), 0, false, d, cs)) != QLORA_OK) return st;
 
   // 2) Y = X deq(W)^T + (s XA) B^T  (fused dequant GEMM)
   const int bn = 256;
@@ -497,7 +497,7 @@ qlora_status qlora_linear_bwd(const qlora_nf4_tensor* W, const uint16_t* X, cons
       !aligned16(dB) || !aligned16(workspace) || (XA && !aligned16(XA)) || (dX && !aligned16(dX)))
     return QLORA_ERR_ALIGN;
   if (!std::isfinite(s)) return QLORA_ERR_SHAPE;
-  BwdLayout L = bwd_layout(sh);
+  BwdLayout L = bwd_layout(sh, 1);
   if (workspace_bytes < L.total) return QLORA_ERR_WORKSPACE;
   DeviceInfo d;
   if ((st = device_info(&d)) != QLORA_OK) return st;
@@ -508,7 +508,7 @@ qlora_status qlora_linear_bwd(const qlora_nf4_tensor* W, const uint16_t* X, cons
 
   // 1) G = dY B -> bf16(s G) (+ fp32 G for few tokens), and X A^T -> bf16(s X A^T)
   //    (recomputed when not supplied, else converted from the caller's fp32)
-  if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L, RankParts(), d, cs)) != QLORA_OK) return st;
+  if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L, RankDivide(), d, cs)) != QLORA_OK) return st;
 
   // 2) dX = dY deq(W) + (s G) A   (fused dequant GEMM, deq(W)^T as the MN-major operand)
   if (dX) {

@@ -19,8 +19,11 @@
 // atomics anywhere.  The epilogue writes any of: the fp32 result (optionally
 // transposed, for dA), and bf16(scale * result) zero-padded to a multiple of
 // 64 columns (the rank-r operand of the fused dequant-GEMM and of the next
-// contraction), so no separate convert kernel runs.  A side job converts a
-// caller-supplied fp32 X A^T to bf16(s X A^T) the same way.
+// contraction), or that value as two bf16 parts, so no separate convert kernel
+// runs.  A side job converts a caller-supplied fp32 X A^T the same way.  A rank-r
+// operand in two parts (the layer over a microscaled weight) has both beside the
+// one tile of the long operand: dA and dB of 8192 tokens, 22016 x 8192, rank 64:
+// 209 us without dX, 192 us from rounded operands, which put them 1e-3 off.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -38,10 +41,12 @@ namespace {
 constexpr int kStages = 6;
 constexpr int kABytes = 128 * 128;     // 128 x 64 bf16
 constexpr int kBBytes = 64 * 128;      // 64 x 64 bf16
-constexpr int kStageBytes = kABytes + kBBytes;
+// Q in two parts: both tiles beside the one of P, multiplied one after the other,
+// so the long operand is still read once.
+__host__ __device__ constexpr int stage_bytes(bool parts) { return kABytes + (parts ? 2 : 1) * kBBytes; }
 constexpr int kThreads = 6 * 32;       // warp 0 TMA, warp 1 MMA, warps 2..5 epilogue
 constexpr uint32_t kTmemCols = 128;    // two 64-column accumulators
-constexpr size_t kSmem = 1024 + kStages * kStageBytes + 256;
+constexpr size_t rank_smem(bool parts) { return 1024 + kStages * stage_bytes(parts) + 256; }
 
 struct UnitPos {
   int prob, mt, nt, sp, kbeg, nk;
@@ -127,19 +132,27 @@ __device__ __forceinline__ void store_final(const RankProblem& p, int64_t row, i
     }
   }
   if (p.out_bf16) store_bf16_row(p, row, c0, v);
-  if (p.out_parts && c0 < p.bf16_cols) {
-    // one divisor after the other: their product may be below what a float holds
-    const float by_row = p.row_div ? 1.0f / p.row_div[row] : 1.0f, by_all = p.row_div ? 1.0f / p.all_div[0] : 1.0f;
+  if ((p.out_parts || p.out_div) && c0 < p.bf16_cols) {
     float d[64];
 #pragma unroll
-    for (int c = 0; c < 64; ++c) d[c] = __fmul_rn(__fmul_rn(__fmul_rn(p.bf16_scale, v[c]), by_row), by_all);
-    store_parts_row(p.out_parts + row * (2 * p.bf16_cols) + 2 * c0, d);
+    for (int c = 0; c < 64; ++c) d[c] = __fmul_rn(p.bf16_scale, v[c]);
+    const int64_t at = row * (2 * p.bf16_cols) + 2 * c0;
+    if (p.out_parts) store_parts_row(p.out_parts + at, d);
+    if (p.out_div) {
+      // one divisor after the other: their product may be below what a float holds
+      const float by_row = 1.0f / p.row_div[row], by_all = 1.0f / p.all_div[0];
+#pragma unroll
+      for (int c = 0; c < 64; ++c) d[c] = __fmul_rn(__fmul_rn(d[c], by_row), by_all);
+      store_parts_row(p.out_div + at, d);
+    }
   }
 }
 
+template <bool kParts>
 __global__ void __launch_bounds__(kThreads, 1)
 k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_constant__ CUtensorMap bm0,
        const __grid_constant__ CUtensorMap am1, const __grid_constant__ CUtensorMap bm1) {
+  constexpr int kStageBytes = stage_bytes(kParts);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem_gen = smem_raw + (smem0 - smem_u32(smem_raw));
@@ -195,7 +208,7 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
       const RankProblem& p = a.p[w.prob];
       const CUtensorMap* am = w.prob ? &am1 : &am0;
       const CUtensorMap* bm = w.prob ? &bm1 : &bm0;
-      const bool a_mn = p.a_mn != 0, b_mn = p.b_mn != 0;
+      const bool a_mn = p.a_mn != 0, b_mn = kParts || p.b_mn != 0;
       auto load = [&](uint32_t st, int k0) {
         uint8_t* sA = smem_gen + st * kStageBytes;
         uint8_t* sB = sA + kABytes;
@@ -206,8 +219,14 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
         } else {
           tma_load_2d(sA, am, k0, w.mt * 128, &full[st]);
         }
-        if (b_mn) tma_load_2d(sB, bm, w.nt * 64, k0, &full[st]);
-        else tma_load_2d(sB, bm, k0, w.nt * 64, &full[st]);
+        if constexpr (kParts) {
+          tma_load_2d(sB, bm, w.nt * 128, k0, &full[st]);
+          tma_load_2d(sB + kBBytes, bm, w.nt * 128 + 64, k0, &full[st]);
+        } else if (b_mn) {
+          tma_load_2d(sB, bm, w.nt * 64, k0, &full[st]);
+        } else {
+          tma_load_2d(sB, bm, k0, w.nt * 64, &full[st]);
+        }
       };
       // two consecutive k-steps at a time: both stages are claimed first and
       // their loads issued back to back, so every row of the long operand is
@@ -238,7 +257,7 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
     for (int u = blockIdx.x; u < nunits && alive; u += gridDim.x) {
       const UnitPos w = unit_pos(a, u);
       const RankProblem& p = a.p[w.prob];
-      const bool a_mn = p.a_mn != 0, b_mn = p.b_mn != 0;
+      const bool a_mn = p.a_mn != 0, b_mn = kParts || p.b_mn != 0;
       const uint32_t idesc = idesc_bf16(128, 64, a_mn, b_mn);
       const int piece = p.flush > 0 ? p.flush : w.nk;
       // a K = 16 slice: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
@@ -259,9 +278,11 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
         const bool last = --left == 0;
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_bf16_ss(tmem_base + ab * 64, a0 + off + kk * a_step, b0 + off + kk * b_step, idesc,
-                        !fresh || kk != 0 ? 1u : 0u);
+          for (int q = 0; q < (kParts ? 2 : 1); ++q)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ss(tmem_base + ab * 64, a0 + off + kk * a_step, b0 + off + q * (kBBytes >> 4) + kk * b_step, idesc,
+                          !fresh || q + kk != 0 ? 1u : 0u);
           mma_commit(&empty[stage]);
           if (last) mma_commit(&acc_full[ab]);
         }
@@ -343,8 +364,8 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
       }
       store_final(p, row, c0, sum);
     }
-    // side job: bf16(scale * in) of a caller's fp32 matrix, zero-padded,
-    // one row per epilogue thread over the whole grid
+    // side job: bf16(scale * in) of a caller's fp32 matrix, zero-padded (or its
+    // two parts), one row per epilogue thread over the whole grid
     if (a.cvt_in) {
       const int64_t gt = static_cast<int64_t>(blockIdx.x) * 128 + et;
       for (int64_t i = gt; i < a.cvt_rows; i += static_cast<int64_t>(gridDim.x) * 128) {
@@ -354,12 +375,12 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
           float f[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = (c + e < a.cvt_cols) ? __fmul_rn(a.cvt_scale, src[c + e]) : 0.0f;
-          uint4 q;
-          q.x = pack_bf16x2(f[0], f[1]);
-          q.y = pack_bf16x2(f[2], f[3]);
-          q.z = pack_bf16x2(f[4], f[5]);
-          q.w = pack_bf16x2(f[6], f[7]);
-          *reinterpret_cast<uint4*>(dst + c) = q;
+          uint32_t first[4], second[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) bf16_parts2(f[2 * e], f[2 * e + 1], first[e], second[e]);
+          uint16_t* at = dst + (a.cvt_parts ? (c & ~int64_t{63}) * 2 + (c & 63) : c);
+          *reinterpret_cast<uint4*>(at) = make_uint4(first[0], first[1], first[2], first[3]);
+          if (a.cvt_parts) *reinterpret_cast<uint4*>(at + 64) = make_uint4(second[0], second[1], second[2], second[3]);
         }
       }
     }
@@ -374,7 +395,24 @@ k_rank(const RankArgs a, const __grid_constant__ CUtensorMap am0, const __grid_c
   }
 }
 
-std::atomic<uint64_t> g_attr_done{0};
+template <bool kParts>
+cudaError_t launch_t(const RankArgs& args, const CUtensorMap& am0, const CUtensorMap& bm0, const CUtensorMap& am1,
+                     const CUtensorMap& bm1, int num_sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> attr_done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(k_rank<kParts>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(rank_smem(kParts)));
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int grid = args.total_units < num_sms ? args.total_units : num_sms;
+  k_rank<kParts><<<grid, kThreads, rank_smem(kParts), stream>>>(args, am0, bm0, am1, bm1);
+  return cudaGetLastError();
+}
 
 }  // namespace
 
@@ -407,18 +445,8 @@ size_t rank_slot_bytes(int tiles, int splits) {
 
 cudaError_t launch_rank(const RankArgs& args, const CUtensorMap& am0, const CUtensorMap& bm0,
                         const CUtensorMap& am1, const CUtensorMap& bm1, int num_sms, cudaStream_t stream) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(g_attr_done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(k_rank, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
-    if (e != cudaSuccess) return e;
-    g_attr_done.fetch_or(bit, std::memory_order_acq_rel);
-  }
-  const int grid = args.total_units < num_sms ? args.total_units : num_sms;
-  k_rank<<<grid, kThreads, kSmem, stream>>>(args, am0, bm0, am1, bm1);
-  return cudaGetLastError();
+  return args.b_parts ? launch_t<true>(args, am0, bm0, am1, bm1, num_sms, stream)
+                      : launch_t<false>(args, am0, bm0, am1, bm1, num_sms, stream);
 }
 
 }  // namespace qlora

@@ -31,12 +31,13 @@ struct RankProblem {
   int64_t ld_bf16;
   int64_t bf16_cols;         // a multiple of 64, <= 64 * n_tiles
   float bf16_scale;
-  // optional: v = bf16_scale * D [/ row_div[row] / all_div[0]] as two bf16 parts whose
-  // sum is within 2^-17 of it, bf16(v) and bf16(v - bf16(v)): [mdim][2 bf16_cols],
-  // after 64 first parts the 64 second ones.  The rank-r operand of a product, and
-  // where that product's accumulator is scaled at its end, divided by the scales
-  // (row_div null: not).
+  // optional: v = bf16_scale * D as two bf16 parts whose sum is within 2^-17 of it,
+  // bf16(v) and bf16(v - bf16(v)): [mdim][2 bf16_cols], after 64 first parts the 64
+  // second ones.  The rank-r operand of a product or of the next contraction.
   uint16_t* out_parts;
+  // optional: v / row_div[row] / all_div[0] the same way, for a product whose
+  // accumulator is scaled at its end
+  uint16_t* out_div;
   const float* row_div;
   const float* all_div;
   // split contraction (splits > 1): fp32 partial tiles and per-tile counters,
@@ -56,6 +57,8 @@ struct RankArgs {
   uint16_t* cvt_out;
   int64_t cvt_ld_out, cvt_cols_out;
   float cvt_scale;
+  int cvt_parts;             // 1: in two bf16 parts, as out_parts
+  int b_parts;               // 1: Q of every problem is MN-major and in two bf16 parts, as out_parts
   uint32_t* err;
 };
 
@@ -67,7 +70,8 @@ int rank_splits(int tiles, int ksteps, int num_sms, int max_splits);
 // Bytes of the partial-tile slots of a problem.
 size_t rank_slot_bytes(int tiles, int splits);
 // Tensor maps: am*/bm* of the problems' P and Q (bf16, 128B swizzle, box
-// {64, 128} / {64, 64} K-major, {64, 64} MN-major); am1/bm1 unused when nprob == 1.
+// {64, 128} / {64, 64} K-major, {64, 64} MN-major; Q in parts: twice as wide);
+// am1/bm1 unused when nprob == 1.
 cudaError_t launch_rank(const RankArgs& args, const CUtensorMap& am0, const CUtensorMap& bm0,
                         const CUtensorMap& am1, const CUtensorMap& bm1, int num_sms, cudaStream_t stream);
 

@@ -101,8 +101,9 @@ XaLayout xa_layout(const LinearShape& s, int parts, size_t base) {
 
 // The region cleared by one memset first (counters, and the decode backward's
 // split-K dX accumulator), then the rest.
-BwdLayout bwd_layout(const LinearShape& s) {
+BwdLayout bwd_layout(const LinearShape& s, int parts) {
   BwdLayout l{};
+  l.parts = parts;
   l.g_plan = rank_tiling(s.m, s.rows, s.lora_steps);
   l.xa_plan = rank_tiling(s.m, s.cols, s.lora_steps);
   l.db_plan = rank_tiling(s.rows, s.m, s.lora_steps);
@@ -121,14 +122,14 @@ BwdLayout bwd_layout(const LinearShape& s) {
   l.slots2 = o; o = round_up(o + l.slots2_bytes, 256);
   l.g = o;      if (s.decode) o = round_up(o + size_t(s.m) * s.rpad * 4, 256);
   l.xa = o;     if (s.decode) o = round_up(o + size_t(s.m) * s.rpad * 4, 256);
-  l.sg = o;     o = round_up(o + size_t(s.m) * s.rpad * 2, 256);
-  l.sxa = o;    o = round_up(o + size_t(s.m) * s.rpad * 2, 256);
+  l.sg = o;     o = round_up(o + size_t(s.m) * s.rpad * 2 * parts, 256);
+  l.sxa = o;    o = round_up(o + size_t(s.m) * s.rpad * 2 * parts, 256);
   l.total = o;
   return l;
 }
 
 qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_t* A, float s, float* XA_out, uint8_t* ws,
-                         const XaLayout& L, const RankParts& parts, int flush, bool cleared, const DeviceInfo& d,
+                         const XaLayout& L, int parts, const RankDivide& div, int flush, bool cleared, const DeviceInfo& d,
                          cudaStream_t cs) {
   RankPlan xp = rank_tiling(sh.m, sh.cols, sh.lora_steps);
   xp.splits = launch_splits(xp.tiles(), xp.ksteps, d.num_sms, L.slot_bytes);
@@ -143,11 +144,9 @@ qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_
   ra.p[0].flush = flush;
   ra.p[0].out_f32 = XA_out; ra.p[0].ld_f32 = sh.r;
   ra.p[0].ld_bf16 = sh.rpad; ra.p[0].bf16_cols = sh.rpad; ra.p[0].bf16_scale = s;
-  if (parts.out) {
-    ra.p[0].out_parts = parts.out; ra.p[0].row_div = parts.row; ra.p[0].all_div = parts.all;
-  } else {
-    ra.p[0].out_bf16 = reinterpret_cast<uint16_t*>(ws + L.sxa);
-  }
+  uint16_t* sxa = reinterpret_cast<uint16_t*>(ws + L.sxa);
+  ra.p[0].out_div = div.out; ra.p[0].row_div = div.row; ra.p[0].all_div = div.all;
+  if (!div.out) (parts == 2 ? ra.p[0].out_parts : ra.p[0].out_bf16) = sxa;
   ra.nprob = 1;
   ra.total_units = xp.tiles() * xp.splits;
   ra.err = d.err;
@@ -156,7 +155,7 @@ qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_
 
 qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uint16_t* dY, const uint16_t* A,
                              const uint16_t* B, float s, const float* XA, uint8_t* ws, BwdLayout* L,
-                             const RankParts& parts, const DeviceInfo& d, cudaStream_t cs) {
+                             const RankDivide& div, const DeviceInfo& d, cudaStream_t cs) {
   float* g32 = sh.decode ? reinterpret_cast<float*>(ws + L->g) : nullptr;     // fp32 G and X A^T: few-token grads
   float* xa32 = sh.decode ? reinterpret_cast<float*>(ws + L->xa) : nullptr;
   uint16_t* sg = reinterpret_cast<uint16_t*>(ws + L->sg);
@@ -190,8 +189,10 @@ qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uin
     float* slots = reinterpret_cast<float*>(ws + L->slots1);
     ra.p[0] = rank_problem(L->g_plan, sh.m, sh.r, false, true, 0, slots, cnt);
     ra.p[0].out_f32 = g32; ra.p[0].ld_f32 = sh.rpad;
-    ra.p[0].out_bf16 = sg; ra.p[0].ld_bf16 = sh.rpad; ra.p[0].bf16_cols = sh.rpad; ra.p[0].bf16_scale = s;
-    ra.p[0].out_parts = parts.out; ra.p[0].row_div = parts.row; ra.p[0].all_div = parts.all;
+    const bool two = L->parts == 2;
+    (two ? ra.p[0].out_parts : ra.p[0].out_bf16) = sg;
+    ra.p[0].ld_bf16 = sh.rpad; ra.p[0].bf16_cols = sh.rpad; ra.p[0].bf16_scale = s;
+    ra.p[0].out_div = div.out; ra.p[0].row_div = div.row; ra.p[0].all_div = div.all;
     ra.nprob = 1;
     ra.total_units = L->g_plan.tiles() * L->g_plan.splits;
     if (recompute) {
@@ -199,13 +200,14 @@ qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uin
                              slots + rank_slot_bytes(L->g_plan.tiles(), L->g_plan.splits) / 4,
                              cnt + L->g_plan.tiles());
       ra.p[1].out_f32 = xa32; ra.p[1].ld_f32 = sh.rpad;
-      ra.p[1].out_bf16 = sh.decode ? nullptr : sxa;
+      if (!sh.decode) (two ? ra.p[1].out_parts : ra.p[1].out_bf16) = sxa;
       ra.p[1].ld_bf16 = sh.rpad; ra.p[1].bf16_cols = sh.rpad; ra.p[1].bf16_scale = s;
       ra.nprob = 2;
       ra.total_units += L->xa_plan.tiles() * L->xa_plan.splits;
     } else if (!sh.decode) {
       ra.cvt_in = XA; ra.cvt_rows = sh.m; ra.cvt_cols = sh.r; ra.cvt_ld_in = sh.r;
-      ra.cvt_out = sxa; ra.cvt_ld_out = sh.rpad; ra.cvt_cols_out = sh.rpad; ra.cvt_scale = s;
+      ra.cvt_out = sxa; ra.cvt_ld_out = sh.rpad * L->parts; ra.cvt_cols_out = sh.rpad; ra.cvt_scale = s;
+      ra.cvt_parts = two ? 1 : 0;
     }
     ra.err = d.err;
     if (counted(launch_rank(ra, dy_k, b_mn, x_k, a_k, d.num_sms, cs)) != cudaSuccess) return QLORA_ERR_CUDA;
@@ -227,13 +229,14 @@ qlora_status run_lora_grads(const LinearShape& sh, const uint16_t* X, const uint
       return QLORA_ERR_CUDA;
     return QLORA_OK;
   }
-  // many tokens, one launch of two contractions over the tokens (bf16 operands):
+  // many tokens, one launch of two contractions over the tokens (bf16 operands, the
+  // rank-r ones in as many parts as launch 1 left):
   // dB = dY^T (s X A^T) [rows, r] and dA = (X^T (s G))^T [r, cols], stored transposed.
   CUtensorMap dy_mn, sxa_mn, x_mn, sg_mn;
   if (!make_map(&dy_mn, dY, sh.rows, sh.m, sh.rows * 2, 64) ||
-      !make_map(&sxa_mn, sxa, sh.rpad, sh.m, sh.rpad * 2, 64) ||
+      !make_map(&sxa_mn, sxa, sh.rpad * L->parts, sh.m, sh.rpad * L->parts * 2, 64) ||
       !make_map(&x_mn, X, sh.cols, sh.m, sh.cols * 2, 64) ||
-      !make_map(&sg_mn, sg, sh.rpad, sh.m, sh.rpad * 2, 64))
+      !make_map(&sg_mn, sg, sh.rpad * L->parts, sh.m, sh.rpad * L->parts * 2, 64))
     return QLORA_ERR_CUDA;
   L->db_plan.splits = L->da_plan.splits =
       launch_splits(L->db_plan.tiles() + L->da_plan.tiles(), L->db_plan.ksteps, d.num_sms, L->slots2_bytes);
@@ -251,6 +254,7 @@ qlora_status run_lora_grads(const LinearShape& sh, const uint16_t* X, const uint
   rb.p[1].out_f32 = dA; rb.p[1].ld_f32 = sh.cols; rb.p[1].transpose = 1;
   rb.nprob = 2;
   rb.total_units = u0 + L->da_plan.tiles() * L->da_plan.splits;
+  rb.b_parts = L->parts == 2 ? 1 : 0;
   rb.err = d.err;
   if (counted(launch_rank(rb, dy_mn, sxa_mn, x_mn, sg_mn, d.num_sms, cs)) != cudaSuccess) return QLORA_ERR_CUDA;
   return QLORA_OK;

@@ -44,31 +44,33 @@ XaLayout xa_layout(const LinearShape& s, int parts, size_t base);
 // Backward: launch 1 = dY B (and X A^T when it is not supplied), launch 2 =
 // dX, launch 3 = dY^T (s X A^T) and X^T (s dY B) (more than 16 tokens; with
 // fewer, k_small_grads from the fp32 G and X A^T).  Launch 1's slot space
-// covers both of its forms.
+// covers both of its forms.  parts: how many bf16 parts s G and s X A^T have (1:
+// rounded; 2: RankProblem::out_parts).
 struct BwdLayout {
+  int parts;
   size_t cnt1, cnt2, dx_acc, clear_end, slots1, slots1_bytes, slots2, slots2_bytes, g, xa, sg, sxa, total;
   RankPlan g_plan, xa_plan, db_plan, da_plan;
 };
-BwdLayout bwd_layout(const LinearShape& s);
+BwdLayout bwd_layout(const LinearShape& s, int parts);
 
-// The rank-r activations in two bf16 parts (RankProblem::out_parts) in `out`, null:
-// none; divided by row[i] and all[0] unless row is null.
-struct RankParts {
+// Rank-r activations as out_div of RankProblem; out null: none.
+struct RankDivide {
   uint16_t* out = nullptr;
   const float* row = nullptr;
   const float* all = nullptr;
 };
 
 // XA = X A^T (fp32 to XA_out when asked) and bf16(s XA) [M, rpad], zero-padded
-// to a multiple of 64 columns, or `parts` in its place; `flush` as RankProblem's;
-// `cleared`: a kernel before has zeroed the counters [cnt, cnt_end).
+// to a multiple of 64 columns, or (parts = 2) its two parts, or `div` in its place;
+// `flush` as RankProblem's; `cleared`: a kernel before has zeroed the counters
+// [cnt, cnt_end).
 qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_t* A, float s, float* XA_out, uint8_t* ws,
-                         const XaLayout& L, const RankParts& parts, int flush, bool cleared, const DeviceInfo& d,
+                         const XaLayout& L, int parts, const RankDivide& div, int flush, bool cleared, const DeviceInfo& d,
                          cudaStream_t cs);
-// Launch 1 of the backward (after clearing [0, clear_end)); `parts`: s G for dX, beside bf16(s G).
+// Launch 1 of the backward (after clearing [0, clear_end)); `div`: s G for dX, beside the one in L->sg.
 qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uint16_t* dY, const uint16_t* A,
                              const uint16_t* B, float s, const float* XA, uint8_t* ws, BwdLayout* L,
-                             const RankParts& parts, const DeviceInfo& d, cudaStream_t cs);
+                             const RankDivide& div, const DeviceInfo& d, cudaStream_t cs);
 // Launch 3: dA and dB.
 qlora_status run_lora_grads(const LinearShape& sh, const uint16_t* X, const uint16_t* dY, float s, const float* XA,
                             float* dA, float* dB, uint8_t* ws, BwdLayout* L, const DeviceInfo& d, cudaStream_t cs);

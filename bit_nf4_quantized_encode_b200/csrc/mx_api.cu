@@ -96,15 +96,15 @@ MxFwdLayout mx_fwd_layout(int format, int64_t rows, int64_t cols, int64_t m, int
 }
 struct MxBwdLayout {
   BwdLayout lora;
-  size_t sg_parts;         // s G [/ (gx gw)] for dX
+  size_t sg_div;           // NVFP4: s G / (gx gw) for dX
   ProductLayout product;
 };
 MxBwdLayout mx_bwd_layout(int format, int64_t rows, int64_t cols, int64_t m, int r, const LinearShape& sh) {
   MxBwdLayout l{};
-  if (r) l.lora = bwd_layout(sh);
+  if (r) l.lora = bwd_layout(sh, 2);
   size_t o = round_up(l.lora.total, 256);
-  l.sg_parts = o;
-  if (r) o = round_up(o + parts_bytes(m, sh), 256);
+  l.sg_div = o;
+  if (r && format == QLORA_NVFP4) o = round_up(o + parts_bytes(m, sh), 256);
   l.product = product_layout(format, cols, rows, m, o);
   return l;
 }
@@ -402,13 +402,13 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, in
     sxa = reinterpret_cast<const uint16_t*>(ws + L.xa.sxa);
     const float* all_div = W->format == QLORA_NVFP4 ? W->global_scale : nullptr;
     if (M > kMxStreamTokens) {
-      RankParts parts;
-      parts.out = reinterpret_cast<uint16_t*>(ws + L.xa.sxa);
+      RankDivide div;
       if (all_div) {
-        parts.row = reinterpret_cast<const float*>(ws + L.product.act.global);
-        parts.all = all_div;
+        div.out = reinterpret_cast<uint16_t*>(ws + L.xa.sxa);
+        div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
+        div.all = all_div;
       }
-      if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, parts, 8, true, d, cs)) != QLORA_OK) return st;
+      if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, 2, div, 8, true, d, cs)) != QLORA_OK) return st;
     } else {
       MxXaArgs xa{};
       xa.x = X;
@@ -456,15 +456,14 @@ qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, c
   const uint16_t* sg = nullptr;
   if (r) {
     // G = dY B and X A^T as the backward over an NF4 weight has them
-    RankParts parts;
-    if (dX) {
-      sg = parts.out = reinterpret_cast<uint16_t*>(ws + L.sg_parts);
-      if (WT->format == QLORA_NVFP4) {
-        parts.row = reinterpret_cast<const float*>(ws + L.product.act.global);
-        parts.all = WT->global_scale;
-      }
+    RankDivide div;
+    sg = reinterpret_cast<const uint16_t*>(ws + L.lora.sg);
+    if (dX && WT->format == QLORA_NVFP4) {
+      sg = div.out = reinterpret_cast<uint16_t*>(ws + L.sg_div);
+      div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
+      div.all = WT->global_scale;
     }
-    if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L.lora, parts, d, cs)) != QLORA_OK) return st;
+    if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L.lora, div, d, cs)) != QLORA_OK) return st;
   }
   if (dX && (st = run_mx_gemm(WT, M, ws, L.product, A, true, sg, r, r ? sh.lora_steps : 0, dX, d, cs)) != QLORA_OK) return st;
   return r ? run_lora_grads(sh, X, dY, s, XA, dA, dB, ws, &L.lora, d, cs) : QLORA_OK;

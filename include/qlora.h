@@ -333,8 +333,10 @@ QLORA_EXPORT qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const ui
  * quantised along the weight's rows (qlora_mx_quantize with transpose = 1), so
  * that this product too takes two 4-bit operands; q is passed straight through:
  *   G  = dY B
- *   dX = deq(q(dY)) deq(WT)^T + s G A     [M, cols] bf16 (skipped when dX is NULL); s G as s X A^T of the forward
- *   dB = s dY^T (X A^T), dA = s G^T X     [rows, r], [r, cols] float, as qlora_linear_bwd
+ *   dX = deq(q(dY)) deq(WT)^T + s G A     [M, cols] bf16 (skipped when dX is NULL)
+ *   dB = s dY^T (X A^T), dA = s G^T X     [rows, r], [r, cols] float
+ * s G and s X A^T enter these as s X A^T does the forward (dA and dB of at most 16
+ * tokens: in fp32).
  * WT [cols, rows], dY [M, rows].  r = 0: no adapter; X, A, B, XA, dA, dB are
  * ignored and dX is required.  XA: X A^T of the forward, or NULL to recompute it.
  */

@@ -40,3 +40,28 @@ def test_adapter_term_is_not_taken_from_rounded_operands(qb, rows, cols, m, r, f
     check(Y, *term_and_bound(f64(x), f64(a), f64(b), s), "Y")
     dX, _, _ = qb.qlora_mx_linear_bwd(qt, dy.cuda(), x.cuda(), a.cuda(), b.cuda(), s)
     check(dX, *term_and_bound(f64(dy), f64(b).T, f64(a).T, s), "dX")
+
+
+def gradient_and_bound(g, x, k, s, exact):
+    """s g^T x with g a sum of k products (magnitudes `exact` of them summed): g, times s, carried as two bf16
+    parts, the tokens summed in fp32."""
+    m = len(x)
+    want = s * g.T @ x
+    off = np.abs(g) * (PARTS + 2.0 ** -22) + sums(k) * exact
+    return want, abs(s) * (off.T @ np.abs(x) + sums(2 * m) * (np.abs(g).T @ np.abs(x))) + 2.0 ** -23 * np.abs(want)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("given_xa", [True, False])
+@pytest.mark.parametrize("rows,cols,m,r", [(72, 128, 5, 8), (72, 128, 17, 136), (136, 64, 40, 64), (72, 128, 64, 256), (64, 192, 300, 64),
+                                           (1000, 64, 150, 72)])
+def test_adapter_gradients_are_not_taken_from_rounded_operands(qb, rows, cols, m, r, given_xa, fmt):  # noqa: F811
+    a, b, s = normal((r, cols), 0.02, 3), normal((rows, r), 0.02, 4), 16.0 / r
+    x, dy = normal((m, cols), 1.0, 2), normal((m, rows), 1.0, 5)
+    qt = qb.qlora_mx_quantize(normal((rows, cols), 0.02, 1).cuda(), fmt, transpose=True)
+    X, dY, A, B = f64(x), f64(dy), f64(a), f64(b)
+    xa = torch.from_numpy(X @ A.T).float().cuda() if given_xa else None
+    dA, dB = qb.qlora_mx_linear_bwd(qt, dy.cuda(), x.cuda(), a.cuda(), b.cuda(), s, XA=xa)[1:]
+    check(dA, *gradient_and_bound(dY @ B, X, rows, s, np.abs(dY) @ np.abs(B)), "dA")
+    want, bound = gradient_and_bound(X @ A.T, dY, cols, s, np.abs(X) @ np.abs(A).T)
+    check(dB, want.T, bound.T, "dB")
