@@ -155,7 +155,7 @@ qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_
 
 qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uint16_t* dY, const uint16_t* A,
                              const uint16_t* B, float s, const float* XA, uint8_t* ws, BwdLayout* L,
-                             const RankDivide& div, const DeviceInfo& d, cudaStream_t cs) {
+                             const RankDivide& div, int flush, const DeviceInfo& d, cudaStream_t cs) {
   float* g32 = sh.decode ? reinterpret_cast<float*>(ws + L->g) : nullptr;     // fp32 G and X A^T: few-token grads
   float* xa32 = sh.decode ? reinterpret_cast<float*>(ws + L->xa) : nullptr;
   uint16_t* sg = reinterpret_cast<uint16_t*>(ws + L->sg);
@@ -190,6 +190,7 @@ qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uin
     ra.p[0] = rank_problem(L->g_plan, sh.m, sh.r, false, true, 0, slots, cnt);
     ra.p[0].out_f32 = g32; ra.p[0].ld_f32 = sh.rpad;
     const bool two = L->parts == 2;
+    ra.p[0].flush = flush;
     (two ? ra.p[0].out_parts : ra.p[0].out_bf16) = sg;
     ra.p[0].ld_bf16 = sh.rpad; ra.p[0].bf16_cols = sh.rpad; ra.p[0].bf16_scale = s;
     ra.p[0].out_div = div.out; ra.p[0].row_div = div.row; ra.p[0].all_div = div.all;
@@ -199,6 +200,7 @@ qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uin
       ra.p[1] = rank_problem(L->xa_plan, sh.m, sh.r, false, false, ra.total_units,
                              slots + rank_slot_bytes(L->g_plan.tiles(), L->g_plan.splits) / 4,
                              cnt + L->g_plan.tiles());
+      ra.p[1].flush = flush;
       ra.p[1].out_f32 = xa32; ra.p[1].ld_f32 = sh.rpad;
       if (!sh.decode) (two ? ra.p[1].out_parts : ra.p[1].out_bf16) = sxa;
       ra.p[1].ld_bf16 = sh.rpad; ra.p[1].bf16_cols = sh.rpad; ra.p[1].bf16_scale = s;
@@ -216,7 +218,8 @@ qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uin
 }
 
 qlora_status run_lora_grads(const LinearShape& sh, const uint16_t* X, const uint16_t* dY, float s, const float* XA,
-                            float* dA, float* dB, uint8_t* ws, BwdLayout* L, const DeviceInfo& d, cudaStream_t cs) {
+                            float* dA, float* dB, uint8_t* ws, BwdLayout* L, int flush, const DeviceInfo& d,
+                            cudaStream_t cs) {
   const uint16_t* sg = reinterpret_cast<const uint16_t*>(ws + L->sg);
   const uint16_t* sxa = reinterpret_cast<const uint16_t*>(ws + L->sxa);
   // few tokens: fp32 on CUDA cores from the fp32 G and X A^T
@@ -254,6 +257,7 @@ qlora_status run_lora_grads(const LinearShape& sh, const uint16_t* X, const uint
   rb.p[1].out_f32 = dA; rb.p[1].ld_f32 = sh.cols; rb.p[1].transpose = 1;
   rb.nprob = 2;
   rb.total_units = u0 + L->da_plan.tiles() * L->da_plan.splits;
+  rb.p[0].flush = rb.p[1].flush = flush;
   rb.b_parts = L->parts == 2 ? 1 : 0;
   rb.err = d.err;
   if (counted(launch_rank(rb, dy_mn, sxa_mn, x_mn, sg_mn, d.num_sms, cs)) != cudaSuccess) return QLORA_ERR_CUDA;

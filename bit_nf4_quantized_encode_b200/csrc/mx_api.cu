@@ -59,6 +59,10 @@ ActLayout act_layout(int format, int64_t m, int64_t k, size_t base) {
 // tiling the tokens over pairs (mx_pair.cu).
 constexpr int64_t kMxStreamTokens = 64;
 
+// The rank contractions' sums leave the tensor core every 512 of the contraction
+// (RankProblem::flush).
+constexpr int kRankFlush = 8;
+
 // What one product needs beside its operands: a streamed one's counters (one per
 // 32 weight rows) and partial tiles.
 struct ProductLayout {
@@ -408,7 +412,7 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, in
         div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
         div.all = all_div;
       }
-      if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, 2, div, 8, true, d, cs)) != QLORA_OK) return st;
+      if ((st = run_rank_xa(sh, X, A, s, XA_out, ws, L.xa, 2, div, kRankFlush, true, d, cs)) != QLORA_OK) return st;
     } else {
       MxXaArgs xa{};
       xa.x = X;
@@ -463,10 +467,10 @@ qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, c
       div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
       div.all = WT->global_scale;
     }
-    if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L.lora, div, d, cs)) != QLORA_OK) return st;
+    if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L.lora, div, kRankFlush, d, cs)) != QLORA_OK) return st;
   }
   if (dX && (st = run_mx_gemm(WT, M, ws, L.product, A, true, sg, r, r ? sh.lora_steps : 0, dX, d, cs)) != QLORA_OK) return st;
-  return r ? run_lora_grads(sh, X, dY, s, XA, dA, dB, ws, &L.lora, d, cs) : QLORA_OK;
+  return r ? run_lora_grads(sh, X, dY, s, XA, dA, dB, ws, &L.lora, kRankFlush, d, cs) : QLORA_OK;
 }
 
 qlora_status qlora_mx_moe_workspace_size(int32_t experts, int64_t hidden, int64_t inner, int64_t M, int32_t top_k,

@@ -65,3 +65,45 @@ def test_adapter_gradients_are_not_taken_from_rounded_operands(qb, rows, cols, m
     check(dA, *gradient_and_bound(dY @ B, X, rows, s, np.abs(dY) @ np.abs(B)), "dA")
     want, bound = gradient_and_bound(X @ A.T, dY, cols, s, np.abs(X) @ np.abs(A).T)
     check(dB, want.T, bound.T, "dB")
+
+
+# A sum of n positive numbers whose parts of 512 are taken on the tensor core, 32 additions off by 2^-22 of the part
+# at most, and added up in fp32, off by 2^-24 each.
+def long_sum(n):
+    return 32 * 2.0 ** -22 + n / 512 * 2.0 ** -24
+
+
+def positive(shape, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.rand(shape, generator=gen, device="cuda").add_(0.5).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_long_contractions_of_the_backward_do_not_drift(qb, fmt):  # noqa: F811
+    """Sums of 65536 positive products, in problems with enough tiles that no
+    contraction is split.  One token per column (row) of X (dY) brings a single G
+    (X A^T) to dA (dB) as it is; a one-hot dY makes G exact and leaves the sum
+    over the tokens."""
+    n, m, r, s = 65536, 148 * 128, 8, 1.0
+    eye = torch.zeros(m, 64, dtype=torch.bfloat16, device="cuda")
+    eye[:64] = torch.eye(64)
+    long = torch.zeros(m, n, dtype=torch.bfloat16, device="cuda")
+    long[:64] = positive((64, n), 1)
+    low, wide = positive((n, r), 2), positive((r, 64), 3)
+    zeros = lambda *z: qb.qlora_mx_quantize(torch.zeros(*z, dtype=torch.bfloat16, device="cuda"), fmt)  # noqa: E731
+    want = f64(long[:64]) @ f64(low)
+    # G = dY B
+    dA = qb.qlora_mx_linear_bwd(zeros(64, n), long, eye, wide, low, s, XA=torch.zeros(m, r, device="cuda"), need_dx=False)[1]
+    check(dA, want.T, (long_sum(n) + PARTS) * want.T, "dA of G")
+    # X A^T, recomputed
+    dB = qb.qlora_mx_linear_bwd(zeros(n, 64), eye, long, low.t().contiguous(), wide.t().contiguous(), s, need_dx=False)[2]
+    check(dB, want, (long_sum(n) + PARTS) * want, "dB of X A^T")
+    # the sum over the tokens
+    del long
+    x = positive((n, m), 4)
+    hot = torch.zeros(n, 64, dtype=torch.bfloat16, device="cuda")
+    hot[:, 0] = 1
+    b = positive((64, r), 5)
+    dA = qb.qlora_mx_linear_bwd(zeros(m, 64), hot, x, positive((r, m), 6), b, s, XA=torch.zeros(n, r, device="cuda"), need_dx=False)[1]
+    want = f64(b)[0][:, None] * f64(sum(p.double().sum(0) for p in x.split(4096)))
+    check(dA, want, (long_sum(n) + 2.0 ** -22) * want, "dA over the tokens")
