@@ -301,7 +301,7 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
           for (int t = 0; t < kN; ++t)
             if (t < m) {
               float y = __uint_as_float(v[t]);
-              if (kFmt == kNvFp4) y = __fmul_rn(__fmul_rn(y, s_g[t]), gw);
+              if (kFmt == kNvFp4) y = mx_scaled(y, s_g[t], gw);
               const __nv_bfloat16 b = __float2bfloat16_rn(y);
               a.out[static_cast<int64_t>(t) * a.rows + row] = *reinterpret_cast<const uint16_t*>(&b);
             }

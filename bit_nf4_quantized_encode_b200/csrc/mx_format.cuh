@@ -74,6 +74,20 @@ __device__ __forceinline__ float mx_global_scale(uint32_t amax_bits) {
 // 1 / g of a power of two in [2^-126, 2^127).
 __device__ __forceinline__ float mx_pow2_inverse(float g) { return __uint_as_float((254u << 23) - __float_as_uint(g)); }
 
+// y gx gw, the value of an accumulator under NVFP4's two global scales (gx a power
+// of two, gw any positive float), rounded once wherever the factors allow it: with
+// their product if that is a normal float (gx gw is exact then), otherwise one
+// after the other, the one first that moves y towards the middle of the range.  A
+// fixed order overflows on the way to a finite result: y = 2^20 under gx = 2^110 and
+// gw = 2^-14 is 2^116, and y gx no float.
+__device__ __forceinline__ float mx_scaled(float y, float gx, float gw) {
+  const float g = __fmul_rn(gx, gw);
+  if (g >= 1.17549435e-38f && g <= 3.402823466e38f) return __fmul_rn(y, g);
+  const bool small = g < 1.0f;               // too small: the larger factor first, too large: the smaller one
+  const float a = small == (gx > gw) ? gx : gw, b = small == (gx > gw) ? gw : gx;
+  return __fmul_rn(__fmul_rn(y, a), b);
+}
+
 // Pairs of floats (sm_100's f32x2 arithmetic, each half rounded to nearest even
 // as the scalar operation is).
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {

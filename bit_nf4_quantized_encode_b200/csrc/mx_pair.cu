@@ -21,6 +21,7 @@
 #include <cstdint>
 
 #include "mx.h"
+#include "mx_format.cuh"
 #include "mx_ptx.cuh"
 
 namespace qlora {
@@ -240,7 +241,7 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
         for (int c = 0; c < 16; ++c) {
           if (row_ok && t0 + c < a.m) {
             float val = __uint_as_float(v[c]);
-            if (kFmt == kNvFp4) val = __fmul_rn(__fmul_rn(val, __ldg(a.x_global + t0 + c)), gw);
+            if (kFmt == kNvFp4) val = mx_scaled(val, __ldg(a.x_global + t0 + c), gw);
             const __nv_bfloat16 b = __float2bfloat16_rn(val);
             __stcs(dst + c * a.rows, *reinterpret_cast<const unsigned short*>(&b));
           }

@@ -27,6 +27,7 @@
 #include <cstdint>
 
 #include "mx.h"
+#include "mx_format.cuh"
 #include "mx_ptx.cuh"
 #include "mx_runs.cuh"
 
@@ -277,7 +278,7 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
       float gw = 1.0f;
       if (kFmt == kNvFp4 && row_ok) gw = __ldg(a.w_global + (a.w_per_row ? row : 0));
       auto store = [&](int t, float v) {
-        if (kFmt == kNvFp4) v = __fmul_rn(__fmul_rn(v, __shfl_sync(0xFFFFFFFFu, t < 32 ? gx0 : gx1, t & 31)), gw);
+        if (kFmt == kNvFp4) v = mx_scaled(v, __shfl_sync(0xFFFFFFFFu, t < 32 ? gx0 : gx1, t & 31), gw);
         if (!row_ok) return;
         const __nv_bfloat16 b = __float2bfloat16_rn(v);
         a.out[t * a.rows + row] = *reinterpret_cast<const uint16_t*>(&b);

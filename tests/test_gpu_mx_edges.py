@@ -1,0 +1,60 @@
+"""Corners of the microscaled operators on the GPU that the shape sweeps do not reach."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mx
+from test_gpu_mx import check, f64, no_device_errors, normal, product_bound, qb, upload  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- the two global scales of NVFP4
+@pytest.mark.parametrize("per_row", [False, True])
+@pytest.mark.parametrize("m", [1, 12, 40, 150])
+def test_results_near_the_ends_of_the_range(qb, m, per_row):  # noqa: F811
+    """Tokens of 2^118 and 2^-100 give the result of tokens of 1, scaled: a result
+    that bf16 holds is not lost on the way to it."""
+    w, x = normal((300, 640), 0.02, 1).cuda(), normal((m, 640), 1.0, 2).cuda()
+    q = qb.qlora_mx_quantize(w, "nvfp4", per_row=per_row)
+    y = qb.qlora_mx_linear_fwd(q, x)[0]
+    for e in (118, -100):
+        got = qb.qlora_mx_linear_fwd(q, x * 2.0 ** e)[0]
+        assert torch.equal(got, y * 2.0 ** e)
+
+
+@pytest.mark.parametrize("m", [1, 12, 40, 150])
+@pytest.mark.parametrize("we,xe,wf,xf,top", [
+    (30, 90, 0, 0, None),              # scales of 2^40 and 2^100; the blocks of 2^30 and of 2^90 get the scale 0
+    (33, 93, 0, 0, 126),               # those of 2^33 and 2^93 are kept
+    (33, 93, -130, -112, -116),        # scales of 2^-90 and 2^-12
+    (33, 93, -130, -150, None)])       # scales of 2^-90 and 2^-50: 2^-154
+def test_global_scales_whose_product_no_float_holds(qb, we, xe, wf, xf, top, m):  # noqa: F811
+    """One value of W below its tensor's scale meets one of X below its token's:
+    a single product, so the result is the exact one, rounded to bf16."""
+    def scaled(t, e):
+        return (t.double() * 2.0 ** e).to(torch.bfloat16)
+
+    w, x = torch.zeros(64, 64, dtype=torch.bfloat16), torch.zeros(m, 64, dtype=torch.bfloat16)
+    w[0, 0], w[1, 16] = 2.0 ** 51, 2.0 ** we
+    x[:, 32], x[:, 16] = 2.0 ** 111, 2.0 ** xe
+    if xf == -150:
+        x[:, 0] = 2.0 ** 111                               # and a product of 2^-118
+    w, x = scaled(w, wf), scaled(x, xf)
+    want = mx.round_trip(f64(x), "nvfp4", True) @ mx.round_trip(f64(w), "nvfp4").T
+    assert top is None or (want[:, 1] == 2.0 ** top).all()
+    got = qb.qlora_mx_linear_fwd(qb.qlora_mx_quantize(w.cuda(), "nvfp4"), x.cuda())[0]
+    assert torch.equal(got.cpu(), torch.from_numpy(want).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("m", [1, 12, 40, 150])
+@pytest.mark.parametrize("g", [1.2345, 3.0e-41])
+def test_a_foreign_global_scale(qb, m, g):  # noqa: F811
+    """Any positive float is taken as a weight's global scale, one below the normal range too."""
+    w, x = f64(normal((200, 320), 1.0, 1)), normal((m, 320), 1.0, 2)
+    q = upload(qb, w, "nvfp4")
+    q.global_scale.fill_(g)
+    x = (x * 2.0 ** 100) if g < 1e-30 else x
+    wv = mx.values(*mx.quantize(w, "nvfp4")[:2], q.global_scale.double().cpu().numpy(), "nvfp4")
+    xv = mx.round_trip(f64(x), "nvfp4", True)
+    check(qb.qlora_mx_linear_fwd(q, x.cuda())[0], xv @ wv.T, product_bound(xv @ wv.T, xv, wv) * (1 + 2.0 ** -20), "Y")
