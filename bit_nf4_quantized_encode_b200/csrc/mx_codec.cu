@@ -289,7 +289,41 @@ __device__ __forceinline__ void mx_levels8(uint32_t w, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
 }
 
-// Codes times their scale -> bf16; one warp per 1024 elements of a row.
+// v g for a g that is no power of two, as floats that rounding to bf16 takes where the
+// exact products go: only a product that fp32 rounds onto a tie of bf16 can go
+// wrong, and is moved one step towards the exact one.  Its remainder is exact where
+// the product's last bit, 2^-33 g at least, is a float; below, the 6 and 24 bits are
+// multiplied in doubles and cut off, the last bit standing for all that follows.
+constexpr float kForeignLeast = 0x1p-116f;
+__device__ __forceinline__ void mx_times_foreign8(float (&v)[8], float g) {
+  bool tie = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) tie |= (__float_as_uint(__fmul_rn(v[i], g)) & 0xFFFFu) == 0x8000u;
+  if (!tie) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], g);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float p = __fmul_rn(v[i], g), left = __fmaf_rn(v[i], g, -p);
+    const uint32_t u = __float_as_uint(p);
+    const uint32_t step = static_cast<uint32_t>((static_cast<int32_t>(u ^ __float_as_uint(left)) >> 31) | 1);
+    v[i] = left != 0.0f && (u & 0xFFFFu) == 0x8000u ? __uint_as_float(u + step) : p;
+  }
+}
+__device__ __forceinline__ void mx_times_tiny8(float (&v)[8], float g) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const double p = static_cast<double>(v[i]) * static_cast<double>(g);
+    const float f = __double2float_rz(p);
+    v[i] = static_cast<double>(f) == p ? f : __uint_as_float(__float_as_uint(f) | 1u);
+  }
+}
+
+// Codes times their scale -> bf16; one warp per 1024 elements of a row.  The global
+// scales that the encoder writes are powers of two, whose product in fp32 is exact
+// wherever bf16 can tell.
 template <int kFmt, bool kVec>
 __global__ void __launch_bounds__(kThreads)
 k_mx_dequant(const uint8_t* codes, const uint8_t* scales, const float* gs, int per_row, int64_t rows, int64_t cols,
@@ -302,6 +336,7 @@ k_mx_dequant(const uint8_t* codes, const uint8_t* scales, const float* gs, int p
        w.row < rows; w.next()) {
     const int64_t c0 = w.seg * 1024 + lane * 8;
     const float g = kFmt == kNvFp4 ? (per_row ? __ldg(gs + w.row) : g0) : 1.0f;
+    const bool foreign = kFmt == kNvFp4 && (__float_as_uint(g) & 0x7FFFFFu) != 0u;
     uint32_t word[4], sb[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -312,35 +347,55 @@ k_mx_dequant(const uint8_t* codes, const uint8_t* scales, const float* gs, int p
         sb[j] = __ldg(scales + mx_scale_offset(w.row, c / mx_block(kFmt), kt));
       }
     }
+    auto store = [&](auto times_g) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t c = c0 + j * 256;
-      if (kVec && c >= cols) continue;
-      const float s = kFmt == kMxFp4 ? mx_e8m0_value(sb[j]) : mx_e4m3_value(sb[j]);
-      uint32_t h[4], o[4];
-      mx_levels8(word[j], h);
+      for (int j = 0; j < 4; ++j) {
+        const int64_t c = c0 + j * 256;
+        if (kVec && c >= cols) continue;
+        const float s = kFmt == kMxFp4 ? mx_e8m0_value(sb[j]) : mx_e4m3_value(sb[j]);
+        uint32_t h[4], o[4];
+        mx_levels8(word[j], h);
+        float v[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-        float lo = __fmul_rn(f.x, s), hi = __fmul_rn(f.y, s);
-        if (kFmt == kNvFp4) { lo = __fmul_rn(lo, g); hi = __fmul_rn(hi, g); }
-        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-        o[i] = *reinterpret_cast<const uint32_t*>(&p);
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+          v[2 * i] = __fmul_rn(f.x, s);
+          v[2 * i + 1] = __fmul_rn(f.y, s);
+        }
+        times_g(v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+          o[i] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        if constexpr (kVec) {
+          *reinterpret_cast<uint4*>(out + w.row * cols + c) = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+          // 32 neighbouring values a store
+          uint4* mine = s_out + (threadIdx.x & ~31);
+          __syncwarp();
+          mine[lane] = make_uint4(o[0], o[1], o[2], o[3]);
+          __syncwarp();
+          const int64_t first = w.seg * 1024 + j * 256;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (first + i * 32 + lane < cols)
+              out[w.row * cols + first + i * 32 + lane] = reinterpret_cast<const uint16_t*>(mine)[i * 32 + lane];
+        }
       }
-      if constexpr (kVec) {
-        *reinterpret_cast<uint4*>(out + w.row * cols + c) = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        // 32 neighbouring values a store
-        uint4* mine = s_out + (threadIdx.x & ~31);
-        __syncwarp();
-        mine[lane] = make_uint4(o[0], o[1], o[2], o[3]);
-        __syncwarp();
-        const int64_t first = w.seg * 1024 + j * 256;
+    };
+    // one branch for all of a warp's 1024 values: inside the loop it costs 12%
+    if constexpr (kFmt == kMxFp4) {
+      store([](float (&)[8]) {});
+    } else if (!foreign) {
+      store([&](float (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (first + i * 32 + lane < cols)
-            out[w.row * cols + first + i * 32 + lane] = reinterpret_cast<const uint16_t*>(mine)[i * 32 + lane];
-      }
+        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], g);
+      });
+    } else if (g >= kForeignLeast) {
+      store([&](float (&v)[8]) { mx_times_foreign8(v, g); });
+    } else {
+      store([&](float (&v)[8]) { mx_times_tiny8(v, g); });
     }
   }
 }

@@ -58,3 +58,40 @@ def test_a_foreign_global_scale(qb, m, g):  # noqa: F811
     wv = mx.values(*mx.quantize(w, "nvfp4")[:2], q.global_scale.double().cpu().numpy(), "nvfp4")
     xv = mx.round_trip(f64(x), "nvfp4", True)
     check(qb.qlora_mx_linear_fwd(q, x.cuda())[0], xv @ wv.T, product_bound(xv @ wv.T, xv, wv) * (1 + 2.0 ** -20), "Y")
+
+
+# ---------------------------------------------------------------- dequantisation
+def bf16_once(v):
+    """float64 values of few bits -> the nearest bf16 value, ties to even, subnormals included."""
+    step = 2.0 ** (np.maximum(np.frexp(v)[1] - 1, -126) - 7.0)
+    return np.rint(v / step) * step
+
+
+def foreign_scales():
+    """(global scales, E4M3 bytes): scales g that put some level * S * g next to a
+    tie of bf16, nearer than fp32 resolves, then random ones down to where the
+    values are subnormal."""
+    lv, g, sb = mx.e4m3_levels(), [], []
+    for s in range(0x38, 0x40):                            # S of 1 .. 1.875
+        for level in (1.0, 1.5):
+            tie = (np.arange(128, 256) + 0.5) / 128
+            c = (tie / (level * lv[s])).astype(np.float32)
+            p = np.float64(c) * level * lv[s]
+            c = c[bf16_once(p) != bf16_once(p.astype(np.float32).astype(np.float64))]
+            g += list(c)
+            sb += [s] * len(c)
+    assert len(g) > 100
+    rng = np.random.default_rng(0)
+    g += list((rng.uniform(1, 2, 600) * 2.0 ** rng.integers(-140, 100, 600)).astype(np.float32))
+    sb += list(rng.integers(1, 127, 600))
+    return np.array(g, np.float32), np.array(sb, np.uint8)
+
+
+@pytest.mark.parametrize("cols", [16, 11])
+def test_dequantize_rounds_once_under_any_global_scale(qb, cols):  # noqa: F811
+    g, sb = foreign_scales()
+    codes = np.broadcast_to(np.arange(16, dtype=np.uint8)[::-1][:cols], (len(g), cols)).copy()
+    q = qb.MXTensor(torch.from_numpy(mx.pack(codes)).reshape(-1).cuda(), torch.from_numpy(mx.tile_scales(sb[:, None])).cuda(),
+                    torch.from_numpy(g).cuda(), len(g), cols, "nvfp4")
+    want = mx.values(codes, sb[:, None], g.astype(np.float64), "nvfp4")
+    assert np.array_equal(f64(qb.qlora_mx_dequantize(q)), bf16_once(want))
