@@ -15,13 +15,19 @@ namespace qlora {
 // 8 kN consecutive elements of a row, from column c (a multiple of 8; zero past
 // cols).  kVec: rows start on 16 bytes (cols % 8 == 0).  Otherwise the 16-byte
 // pieces that hold them are loaded and shifted into place; `limit`: elements from
-// the row's start to the end of the matrix, past which nothing is read.
-template <bool kVec, int kN>
+// the row's start to the end of the matrix, past which nothing is read.  kLate: the
+// elements may have been written after this kernel began (before its
+// griddepcontrol.wait), which the read-only path is not for.
+template <bool kLate, typename T>
+__device__ __forceinline__ T load_in(const T* p) {
+  return kLate ? *p : __ldg(p);
+}
+template <bool kVec, int kN, bool kLate = false>
 __device__ __forceinline__ void load_elems(const uint16_t* row, int64_t c, int64_t cols, int64_t limit, uint4 (&out)[kN]) {
   if constexpr (kVec) {
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-      out[i] = c + 8 * i < cols ? __ldg(reinterpret_cast<const uint4*>(row + c) + i) : make_uint4(0, 0, 0, 0);
+      out[i] = c + 8 * i < cols ? load_in<kLate>(reinterpret_cast<const uint4*>(row + c) + i) : make_uint4(0, 0, 0, 0);
     return;
   }
   const int d = static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 7u);    // elements past a 16-byte border
@@ -33,12 +39,12 @@ __device__ __forceinline__ void load_elems(const uint16_t* row, int64_t c, int64
     const int64_t e = c - d + 8 * i;                      // first element of the piece, counted from the row's start
     if (e < cols) {
       if (e + 8 <= limit) {
-        q = __ldg(reinterpret_cast<const uint4*>(at) + i);
+        q = load_in<kLate>(reinterpret_cast<const uint4*>(at) + i);
       } else {
         uint32_t* qw = &q.x;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (e + k < limit) qw[k >> 1] |= static_cast<uint32_t>(__ldg(at + 8 * i + k)) << (16 * (k & 1));
+          if (e + k < limit) qw[k >> 1] |= static_cast<uint32_t>(load_in<kLate>(at + 8 * i + k)) << (16 * (k & 1));
       }
     }
     w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
@@ -79,10 +85,10 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t c
 struct Elems32 {
   uint4 q[4];
 };
-template <bool kVec>
+template <bool kVec, bool kLate = false>
 __device__ __forceinline__ Elems32 load32(const uint16_t* row, int64_t c, int64_t cols, int64_t limit) {
   Elems32 e;
-  load_elems<kVec, 4>(row, c, cols, limit, e.q);
+  load_elems<kVec, 4, kLate>(row, c, cols, limit, e.q);
   return e;
 }
 

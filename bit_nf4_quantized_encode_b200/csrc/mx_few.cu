@@ -248,7 +248,7 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
       const int64_t c = static_cast<int64_t>(i - t * per_row) * 32;
       const uint16_t* row = a.x + static_cast<int64_t>(t) * a.k;
       const int64_t limit = (m - t) * a.k;
-      return a.vec ? load32<true>(row, c, a.k, limit) : load32<false>(row, c, a.k, limit);
+      return a.vec ? load32<true, true>(row, c, a.k, limit) : load32<false, true>(row, c, a.k, limit);
     };
     Elems32 first = {};
     if (tid < tasks) first = load(tid);
@@ -296,7 +296,7 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
         const int row = (k.unit + unit) * 32 + lane;
         if (row < a.rows) {
           float gw = 1.0f;
-          if (kFmt == kNvFp4) gw = __ldg(a.w_global + (a.w_per_row ? row : 0));
+          if (kFmt == kNvFp4) gw = a.w_global[a.w_per_row ? row : 0];      // as late as X
 #pragma unroll
           for (int t = 0; t < kN; ++t)
             if (t < m) {

@@ -438,7 +438,7 @@ k_moe_product(const MxMoeArgs a, const __grid_constant__ CUtensorMap wmap, const
       if (!kUp) {
 #pragma unroll
         for (int t = 0; t < kSlots; ++t)
-          pr[t] = (info.tokens >> t) & 1u ? __ldg(a.probs + t * a.top_k + static_cast<int>((info.slots >> (4 * t)) & 15u)) : 0.0f;
+          pr[t] = (info.tokens >> t) & 1u ? __ldcg(a.probs + t * a.top_k + static_cast<int>((info.slots >> (4 * t)) & 15u)) : 0.0f;
       }
       if (!mbar_wait_warp(&acc_full[ab], (seg >> 1) & 1u, a.err)) break;
       tc_fence_after();

@@ -236,12 +236,19 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
           if (lane == 0) mbar_arrive_cluster(free_bar);
         }
         const int64_t t0 = static_cast<int64_t>(w.tt) * kBN + cc * 16;
+        // written by the kernel before, which this one's start overlaps: no read-only
+        // loads (the work buffer has whole pieces of 64)
+        float4 gx[4] = {};
+        if (kFmt == kNvFp4 && t0 < a.m) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) gx[c] = __ldcg(reinterpret_cast<const float4*>(a.x_global + t0) + c);
+        }
         uint16_t* dst = a.out + t0 * a.rows + row;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           if (row_ok && t0 + c < a.m) {
             float val = __uint_as_float(v[c]);
-            if (kFmt == kNvFp4) val = mx_scaled(val, __ldg(a.x_global + t0 + c), gw);
+            if (kFmt == kNvFp4) val = mx_scaled(val, (&gx[c >> 2].x)[c & 3], gw);
             const __nv_bfloat16 b = __float2bfloat16_rn(val);
             __stcs(dst + c * a.rows, *reinterpret_cast<const unsigned short*>(&b));
           }

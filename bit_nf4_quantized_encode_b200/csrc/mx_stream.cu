@@ -254,8 +254,8 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
     // lane t: the global scales of tokens t and t + 32
     float gx0 = 1.0f, gx1 = 1.0f;
     if (kFmt == kNvFp4) {
-      if (lane < m) gx0 = __ldg(a.x_global + lane);
-      if (lane + 32 < m) gx1 = __ldg(a.x_global + lane + 32);
+      if (lane < m) gx0 = __ldcg(a.x_global + lane);
+      if (lane + 32 < m) gx1 = __ldcg(a.x_global + lane + 32);
     }
     constexpr int kChunk = kBN < 32 ? kBN : 32;
     const int64_t slot_floats = static_cast<int64_t>(m) * 128;

@@ -95,3 +95,40 @@ def test_dequantize_rounds_once_under_any_global_scale(qb, cols):  # noqa: F811
                     torch.from_numpy(g).cuda(), len(g), cols, "nvfp4")
     want = mx.values(codes, sb[:, None], g.astype(np.float64), "nvfp4")
     assert np.array_equal(f64(qb.qlora_mx_dequantize(q)), bf16_once(want))
+
+
+# ---------------------------------------------------------------- calls that overlap
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("m,size", [(1, 4096), (3, 2048), (5, 1001)])
+def test_one_launch_products_in_a_chain(qb, m, size, fmt):  # noqa: F811
+    """Each product starts while the one that writes its tokens still runs (and the
+    first of a round while its weight is still being quantised); the result is that
+    of the same calls with a wait after each."""
+    ws = [normal((size, size), size ** -0.5, i).cuda() for i in range(4)]
+    x = normal((m, size), 1.0, 9).cuda()
+    out = [qb.empty_mx(size, size, x.device, fmt) for _ in ws]
+
+    def chain(wait):
+        y, all_y = x, []
+        for w, q in zip(ws, out):
+            qb.qlora_mx_quantize(w, out=q)
+            for _ in range(3):
+                y = qb.qlora_mx_linear_fwd(q, y)[0]
+                if wait:
+                    torch.cuda.synchronize()
+                all_y.append(y)
+        return all_y
+
+    want = chain(True)
+    assert all(torch.isfinite(y).all() for y in want)
+    for _ in range(5):
+        for q in out:
+            q.codes.fill_(0x77)
+        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(False)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
