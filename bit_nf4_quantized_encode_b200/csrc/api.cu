@@ -407,7 +407,7 @@ qlora_status qlora_linear_workspace_size(int64_t rows, int64_t cols, int64_t M, 
   const qlora_status st = linear_shape(rows, cols, M, r, &sh);
   if (st != QLORA_OK) return st;
   if (fwd_bytes) *fwd_bytes = fwd_layout(sh).total;
-  if (bwd_bytes) *bwd_bytes = bwd_layout(sh, 1).total;
+  if (bwd_bytes) *bwd_bytes = bwd_layout(sh, 1, sh.decode).total;
   return QLORA_OK;
 }
 
@@ -497,7 +497,7 @@ qlora_status qlora_linear_bwd(const qlora_nf4_tensor* W, const uint16_t* X, cons
       !aligned16(dB) || !aligned16(workspace) || (XA && !aligned16(XA)) || (dX && !aligned16(dX)))
     return QLORA_ERR_ALIGN;
   if (!std::isfinite(s)) return QLORA_ERR_SHAPE;
-  BwdLayout L = bwd_layout(sh, 1);
+  BwdLayout L = bwd_layout(sh, 1, sh.decode);
   if (workspace_bytes < L.total) return QLORA_ERR_WORKSPACE;
   DeviceInfo d;
   if ((st = device_info(&d)) != QLORA_OK) return st;

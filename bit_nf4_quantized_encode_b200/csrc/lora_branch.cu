@@ -99,9 +99,8 @@ XaLayout xa_layout(const LinearShape& s, int parts, size_t base) {
   return l;
 }
 
-// The region cleared by one memset first (counters, and the decode backward's
-// split-K dX accumulator), then the rest.
-BwdLayout bwd_layout(const LinearShape& s, int parts) {
+// The region cleared by one memset first (counters, and dx_acc), then the rest.
+BwdLayout bwd_layout(const LinearShape& s, int parts, bool split_dx) {
   BwdLayout l{};
   l.parts = parts;
   l.g_plan = rank_tiling(s.m, s.rows, s.lora_steps);
@@ -116,7 +115,7 @@ BwdLayout bwd_layout(const LinearShape& s, int parts) {
   size_t o = 0;
   l.cnt1 = o;   o = round_up(o + size_t(l.g_plan.tiles() + l.xa_plan.tiles()) * 4, 256);
   l.cnt2 = o;   o = round_up(o + size_t(l.db_plan.tiles() + l.da_plan.tiles()) * 4, 256);
-  l.dx_acc = o; if (s.decode) o = round_up(o + size_t(s.m) * s.cols * 4, 256);
+  l.dx_acc = o; if (split_dx) o = round_up(o + size_t(s.m) * s.cols * 4, 256);
   l.clear_end = o;
   l.slots1 = o; o = round_up(o + l.slots1_bytes, 256);
   l.slots2 = o; o = round_up(o + l.slots2_bytes, 256);

@@ -45,13 +45,14 @@ XaLayout xa_layout(const LinearShape& s, int parts, size_t base);
 // dX, launch 3 = dY^T (s X A^T) and X^T (s dY B) (more than 16 tokens; with
 // fewer, k_small_grads from the fp32 G and X A^T).  Launch 1's slot space
 // covers both of its forms.  parts: how many bf16 parts s G and s X A^T have (1:
-// rounded; 2: RankProblem::out_parts).
+// rounded; 2: RankProblem::out_parts).  dx_acc: the fp32 [M, cols] in which the
+// decode backward over an NF4 weight adds up dX (split_dx), cleared with the counters.
 struct BwdLayout {
   int parts;
   size_t cnt1, cnt2, dx_acc, clear_end, slots1, slots1_bytes, slots2, slots2_bytes, g, xa, sg, sxa, total;
   RankPlan g_plan, xa_plan, db_plan, da_plan;
 };
-BwdLayout bwd_layout(const LinearShape& s, int parts);
+BwdLayout bwd_layout(const LinearShape& s, int parts, bool split_dx);
 
 // Rank-r activations as out_div of RankProblem; out null: none.
 struct RankDivide {

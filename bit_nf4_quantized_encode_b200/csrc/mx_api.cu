@@ -105,7 +105,7 @@ struct MxBwdLayout {
 };
 MxBwdLayout mx_bwd_layout(int format, int64_t rows, int64_t cols, int64_t m, int r, const LinearShape& sh) {
   MxBwdLayout l{};
-  if (r) l.lora = bwd_layout(sh, 2);
+  if (r) l.lora = bwd_layout(sh, 2, false);
   size_t o = round_up(l.lora.total, 256);
   l.sg_div = o;
   if (r && format == QLORA_NVFP4) o = round_up(o + parts_bytes(m, sh), 256);
