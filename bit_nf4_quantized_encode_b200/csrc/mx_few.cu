@@ -283,9 +283,18 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
     const int quarter = warp & 3;
     for (int c = 0; c < chunks; ++c) {
       const Chunk k = chunk_of(c);
+      // the weight's global scale before waiting for the products (it may be as late as
+      // X: no read-only load)
+      MxRowScale gw = {1.0f, 1.0f};
+      auto load_gw = [&](int i) {
+        const int row = (k.unit + i * 4 + quarter - k.col) * 32 + lane;
+        if (kFmt == kNvFp4 && row < a.rows) gw = mx_row_scale(a.w_global[a.w_per_row ? row : 0]);
+      };
+      const int i0 = warp >= 6 ? 1 : 0;
+      load_gw(i0);
       if (!mbar_wait(&acc_full[c & 1], (c >> 1) & 1u, a.err)) break;
       tc_fence_after();
-      for (int i = warp >= 6 ? 1 : 0; i < k.tiles; i += 2) {
+      for (int i = i0; i < k.tiles; i += 2) {
         const int unit = i * 4 + quarter - k.col;
         if (unit < 0 || unit >= k.n) continue;
         uint32_t v[kN];
@@ -295,8 +304,7 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
         tmem_wait_ld();
         const int row = (k.unit + unit) * 32 + lane;
         if (row < a.rows) {
-          float gw = 1.0f;
-          if (kFmt == kNvFp4) gw = a.w_global[a.w_per_row ? row : 0];      // as late as X
+          if (a.w_per_row && i != i0) load_gw(i);
 #pragma unroll
           for (int t = 0; t < kN; ++t)
             if (t < m) {

@@ -75,17 +75,25 @@ __device__ __forceinline__ float mx_global_scale(uint32_t amax_bits) {
 __device__ __forceinline__ float mx_pow2_inverse(float g) { return __uint_as_float((254u << 23) - __float_as_uint(g)); }
 
 // y gx gw, the value of an accumulator under NVFP4's two global scales (gx a power
-// of two, gw any positive float), rounded once wherever the factors allow it: with
-// their product if that is a normal float (gx gw is exact then), otherwise one
-// after the other, the one first that moves y towards the middle of the range.  A
-// fixed order overflows on the way to a finite result: y = 2^20 under gx = 2^110 and
-// gw = 2^-14 is 2^116, and y gx no float.
-__device__ __forceinline__ float mx_scaled(float y, float gx, float gw) {
-  const float g = __fmul_rn(gx, gw);
-  if (g >= 1.17549435e-38f && g <= 3.402823466e38f) return __fmul_rn(y, g);
-  const bool small = g < 1.0f;               // too small: the larger factor first, too large: the smaller one
-  const float a = small == (gx > gw) ? gx : gw, b = small == (gx > gw) ? gw : gx;
-  return __fmul_rn(__fmul_rn(y, a), b);
+// of two from 2^-126 to 2^117, gw any positive float).  Without a rank-r term y is 0
+// or between 2^-20 and 2^37 or so, so y gw stays a normal float for gw from 2^-106 to
+// 2^91, and times gx is the result; the other order leaves the range on the way (y =
+// 2^20 under gx = 2^110 and gw = 2^-14 is 2^116, y gx no float).  A gw beyond is
+// brought inside by 2^64, which the result gets back.  No element asks for a case:
+// branches in k_mx_pair's epilogue made it slower than the product it runs beside
+// (8192^3: 381 us, 243 this way), and code that the end of a short kernel runs for the
+// first time has to be fetched.
+struct MxRowScale {
+  float g, post;
+};
+__device__ __forceinline__ MxRowScale mx_row_scale(float gw) {
+  MxRowScale r;
+  r.post = gw < 0x1p-106f ? 0x1p-64f : gw > 0x1p91f ? 0x1p64f : 1.0f;
+  r.g = __fmul_rn(gw, gw < 0x1p-106f ? 0x1p64f : gw > 0x1p91f ? 0x1p-64f : 1.0f);
+  return r;
+}
+__device__ __forceinline__ float mx_scaled(float y, float gx, const MxRowScale& r) {
+  return __fmul_rn(__fmul_rn(__fmul_rn(y, r.g), gx), r.post);
 }
 
 // Pairs of floats (sm_100's f32x2 arithmetic, each half rounded to nearest even

@@ -68,6 +68,7 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
   constexpr int kChunks = kBN / 16, kShared = 3;      // 16-column pieces of an accumulator, of them shared (kBN = 256)
 
   extern __shared__ uint8_t smem_raw[];
+  __shared__ float4 s_gx[4][kFmt == kNvFp4 ? kBN / 4 : 1];     // an epilogue warp's token scales
   const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem_gen = smem_raw + (smem0 - smem_u32(smem_raw));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem_gen + kStages * kStageBytes);   // the leader's count both CTAs' bytes
@@ -215,12 +216,23 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
     uint32_t n = 0;
     for (int u = first; u < ntiles; u += stride, ++n) {
       const Tile w = tile_of(u, a);
-      if (!mbar_wait(acc_full, n & 1u, a.err)) break;
-      tc_fence_after();
       const int64_t row = static_cast<int64_t>(w.mt) * 256 + rank * 128 + quarter * 32 + lane;
       const bool row_ok = row < a.rows;
-      float gw = 1.0f;
-      if (a.w_global && row_ok) gw = __ldg(a.w_global + (a.w_per_row ? row : 0));
+      MxRowScale gw = {1.0f, 1.0f};
+      if (kFmt == kNvFp4 && row_ok) gw = mx_row_scale(__ldg(a.w_global + (a.w_per_row ? row : 0)));
+      if (kFmt == kNvFp4) {
+        // the scales are written by the kernel before, which this one's start overlaps:
+        // no read-only loads
+        __syncwarp();                        // all lanes are done with the tile before
+#pragma unroll
+        for (int i = 0; i < kBN / 32; ++i) {
+          const int64_t t = static_cast<int64_t>(w.tt) * kBN + i * 32 + lane;
+          reinterpret_cast<float*>(s_gx[quarter])[i * 32 + lane] = t < a.m ? __ldcg(a.x_global + t) : 1.0f;
+        }
+        __syncwarp();
+      }
+      if (!mbar_wait(acc_full, n & 1u, a.err)) break;
+      tc_fence_after();
       const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (n & 1u) * kAcc1;
       // the columns that the two accumulators share come first
       const int c0 = (n & 1u) ? 0 : (kBN == 256 ? kChunks - kShared : 0);
@@ -236,22 +248,21 @@ k_mx_pair(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const __
           if (lane == 0) mbar_arrive_cluster(free_bar);
         }
         const int64_t t0 = static_cast<int64_t>(w.tt) * kBN + cc * 16;
-        // written by the kernel before, which this one's start overlaps: no read-only
-        // loads (the work buffer has whole pieces of 64)
-        float4 gx[4] = {};
-        if (kFmt == kNvFp4 && t0 < a.m) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) gx[c] = __ldcg(reinterpret_cast<const float4*>(a.x_global + t0) + c);
-        }
         uint16_t* dst = a.out + t0 * a.rows + row;
+        auto store = [&](auto scaled) {
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          if (row_ok && t0 + c < a.m) {
-            float val = __uint_as_float(v[c]);
-            if (kFmt == kNvFp4) val = mx_scaled(val, (&gx[c >> 2].x)[c & 3], gw);
-            const __nv_bfloat16 b = __float2bfloat16_rn(val);
-            __stcs(dst + c * a.rows, *reinterpret_cast<const unsigned short*>(&b));
+          for (int c = 0; c < 16; ++c) {
+            const __nv_bfloat16 b = __float2bfloat16_rn(scaled(__uint_as_float(v[c]), c));
+            if (row_ok && t0 + c < a.m) __stcs(dst + c * a.rows, *reinterpret_cast<const unsigned short*>(&b));
           }
+        };
+        if constexpr (kFmt == kMxFp4) {
+          store([](float y, int) { return y; });
+        } else {
+          float4 gx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) gx[c] = s_gx[quarter][cc * 4 + c];
+          store([&](float y, int c) { return mx_scaled(y, (&gx[c >> 2].x)[c & 3], gw); });
         }
       }
     }

@@ -275,8 +275,8 @@ k_mx_stream(const MxGemmArgs a, const __grid_constant__ CUtensorMap wmap, const 
         p = parts_of(a.slots + rl, slot_floats, total, static_cast<int64_t>(tile) * per_tile, per_tile, runs);
         alone = others_counted(counter, p.n);
       }
-      float gw = 1.0f;
-      if (kFmt == kNvFp4 && row_ok) gw = __ldg(a.w_global + (a.w_per_row ? row : 0));
+      MxRowScale gw = {1.0f, 1.0f};
+      if (kFmt == kNvFp4 && row_ok) gw = mx_row_scale(__ldg(a.w_global + (a.w_per_row ? row : 0)));
       auto store = [&](int t, float v) {
         if (kFmt == kNvFp4) v = mx_scaled(v, __shfl_sync(0xFFFFFFFFu, t < 32 ? gx0 : gx1, t & 31), gw);
         if (!row_ok) return;

@@ -48,13 +48,13 @@ def test_global_scales_whose_product_no_float_holds(qb, we, xe, wf, xf, top, m):
 
 
 @pytest.mark.parametrize("m", [1, 12, 40, 150])
-@pytest.mark.parametrize("g", [1.2345, 3.0e-41])
-def test_a_foreign_global_scale(qb, m, g):  # noqa: F811
+@pytest.mark.parametrize("g,e", [(1.2345, 0), (3.0e-41, 100), (1.0e-33, 80), (1.0e30, -100)])
+def test_a_foreign_global_scale(qb, m, g, e):  # noqa: F811
     """Any positive float is taken as a weight's global scale, one below the normal range too."""
     w, x = f64(normal((200, 320), 1.0, 1)), normal((m, 320), 1.0, 2)
     q = upload(qb, w, "nvfp4")
     q.global_scale.fill_(g)
-    x = (x * 2.0 ** 100) if g < 1e-30 else x
+    x = x * 2.0 ** e
     wv = mx.values(*mx.quantize(w, "nvfp4")[:2], q.global_scale.double().cpu().numpy(), "nvfp4")
     xv = mx.round_trip(f64(x), "nvfp4", True)
     check(qb.qlora_mx_linear_fwd(q, x.cuda())[0], xv @ wv.T, product_bound(xv @ wv.T, xv, wv) * (1 + 2.0 ** -20), "Y")
