@@ -40,9 +40,10 @@ namespace {
 constexpr int kRouteCtas = 8;
 constexpr int kRouteThreads = 512, kRouteWarps = kRouteThreads / 32;
 
-// Order-preserving key of a logit, above 0 (0 marks a taken one); NaN lowest.
+// Order-preserving key of a logit, above 0 (0 marks a taken one); NaN highest, so that
+// it shows in the token's probabilities and y instead of dropping an expert unseen.
 __device__ __forceinline__ uint32_t logit_key(float v) {
-  if (v != v) return 1u;
+  if (v != v) return 0xFFFFFFFFu;
   const uint32_t b = __float_as_uint(__fadd_rn(v, 0.0f));        // -0 is 0
   return (b >> 31) ? ~b : (b | 0x80000000u);
 }

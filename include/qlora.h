@@ -349,7 +349,8 @@ QLORA_EXPORT qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const u
  * A whole mixture-of-experts feed-forward layer for a few tokens over frozen
  * MXFP4 experts: routing, both products of every expert in use and their sum.
  *   logits[t] = X[t] router^T (fp32); the top_k largest of a token are chosen,
- *   the lowest index first among equal ones; p[t] = softmax of their logits;
+ *   the lowest index first among equal ones (a NaN counts as the largest, and makes
+ *   the token's probabilities and Y NaN); p[t] = softmax of their logits;
  *   [g; u] = deq(W13_e) deq(q(X[t])),  h = g / (1 + exp(-g)) * u,
  *   Y[t] = sum_j p[t, j] deq(W2_e) deq(q(h)),  e = ids[t, j].
  * W13 stacks the experts' [2 inner, hidden] (gate rows, then up rows), W2 their

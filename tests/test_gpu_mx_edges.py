@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from oracle import mx
-from test_gpu_mx import check, f64, no_device_errors, normal, product_bound, qb, upload  # noqa: F401
+from test_gpu_mx import check, f64, moe_case, no_device_errors, normal, product_bound, qb, upload  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -132,3 +132,21 @@ def test_one_launch_products_in_a_chain(qb, m, size, fmt):  # noqa: F811
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ---------------------------------------------------------------- routing
+def test_a_nan_logit_is_the_largest(qb):  # noqa: F811
+    """Experts whose logit is NaN for some tokens: chosen first there, the lowest
+    index first, as a descending stable sort has it, and seen in p and Y."""
+    q13, q2, router, x = moe_case(qb, 12, 256, 128, 6, 3)
+    x[:, 7] = 0
+    x[2, 7], x[4, 7] = float("inf"), float("inf")
+    router[:, 7] = 1
+    router[5, 7] = router[9, 7] = 0                        # inf * 0; every other logit of these tokens is inf
+    ids_want = torch.sort(x.float() @ router.float().t(), dim=1, descending=True, stable=True)[1][:, :4]
+    Y, ids, p = qb.qlora_mx_moe_fwd(q13, q2, router, x, 4)
+    assert torch.equal(ids.long(), ids_want) and ids[2].tolist() == [5, 9, 0, 1]
+    for t in range(6):
+        bad = t in (2, 4)
+        assert bool(p[t].isnan().all()) is bad and bool(Y[t].isnan().all()) is bad
+        assert bad or (p[t].sum() - 1).abs() < 1e-5
