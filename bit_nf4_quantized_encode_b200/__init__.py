@@ -510,7 +510,9 @@ def qlora_mx_quantize(W: torch.Tensor, fmt: str = "mxfp4", transpose: bool = Fal
     if rows == 0 or cols == 0:
         return out
     c = out.c_struct()
-    if workspace is None and out.fmt == "nvfp4" and not out.scale_per_row and _mx_quant_workspace(rows, cols):
+    if workspace is not None:
+        _mx_workspace(workspace, 0, W.device)
+    elif out.fmt == "nvfp4" and not out.scale_per_row and _mx_quant_workspace(rows, cols):
         workspace = torch.empty(_mx_quant_workspace(rows, cols), dtype=torch.uint8, device=W.device)
     _on(W.device, "qlora_mx_quantize", _lib.qlora_mx_quantize, W.data_ptr(), int(transpose), c, _addr(workspace),
         _size(workspace))

@@ -14,3 +14,20 @@ def test_backward_of_few_tokens_reserves_no_dx_in_fp32(fmt):
     counters and at most 32 partial tiles of 32 KB, not by [m, cols] floats."""
     wide, narrow = (qb.qlora_mx_linear_workspace_size(4096, c, fmt, 16, 8)[1] for c in (65536, 64))
     assert wide - narrow < 16 * (65536 - 64) * 4 // 2
+
+
+def test_quantize_refuses_a_work_buffer_elsewhere(monkeypatch):
+    """A caller's work buffer on another device, or with gaps, does not reach the library."""
+    import torch
+
+    monkeypatch.setattr(qb, "_need_bf16_cuda", lambda name, t: None)
+    monkeypatch.setattr(qb.MXTensor, "c_struct", lambda self: None)
+    calls = []
+    monkeypatch.setattr(qb, "_on", lambda device, where, fn, *args: calls.append(where))
+    w, out = torch.zeros(1024, 1024, dtype=torch.bfloat16), qb.empty_mx(1024, 1024, "cpu", "nvfp4")
+    for bad in (torch.empty(8192, dtype=torch.uint8, device="meta"), torch.empty(16384, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            qb.qlora_mx_quantize(w, out=out, workspace=bad)
+    assert not calls
+    qb.qlora_mx_quantize(w, out=out, workspace=torch.empty(8192, dtype=torch.uint8))
+    assert calls == ["qlora_mx_quantize"]
