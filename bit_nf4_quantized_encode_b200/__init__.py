@@ -476,8 +476,10 @@ def _on(device, where: str, fn, *args):
         raise QloraError(status, where)
 
 
-# The current stream's handle of a device, without building a Stream object (2 us a call).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The current stream's handle of a device: torch's own getter where this torch has it,
+# which builds no Stream object (2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def qlora_mx_sizes(rows: int, cols: int, fmt: str = "mxfp4", per_row: bool = False) -> dict:

@@ -31,3 +31,12 @@ def test_quantize_refuses_a_work_buffer_elsewhere(monkeypatch):
     assert not calls
     qb.qlora_mx_quantize(w, out=out, workspace=torch.empty(8192, dtype=torch.uint8))
     assert calls == ["qlora_mx_quantize"]
+
+
+def test_import_without_torchs_private_stream_getter():
+    """The stream handle comes from torch's private getter where there is one, else from the public call."""
+    import subprocess
+    import sys
+    code = ("import torch; del torch._C._cuda_getCurrentRawStream; import bit_nf4_quantized_encode_b200 as qb; "
+            "torch.cuda.current_stream = lambda i: type('S', (), {'cuda_stream': 40 + i}); assert qb._raw_stream(2) == 42")
+    subprocess.run([sys.executable, "-c", code], check=True)
