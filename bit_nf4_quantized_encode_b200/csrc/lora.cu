@@ -140,9 +140,9 @@ __device__ __forceinline__ void store_final(const RankProblem& p, int64_t row, i
     if (p.out_parts) store_parts_row(p.out_parts + at, d);
     if (p.out_div) {
       // one divisor after the other: their product may be below what a float holds
-      const float by_row = 1.0f / p.row_div[row], by_all = 1.0f / p.all_div[0];
+      const float by_row = 1.0f / p.row_div[row], all = p.all_div[0];      // row_div: powers of two
 #pragma unroll
-      for (int c = 0; c < 64; ++c) d[c] = __fmul_rn(__fmul_rn(d[c], by_row), by_all);
+      for (int c = 0; c < 64; ++c) d[c] = __fdiv_rn(__fmul_rn(d[c], by_row), all);
       store_parts_row(p.out_div + at, d);
     }
   }

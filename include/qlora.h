@@ -321,7 +321,9 @@ QLORA_EXPORT qlora_status qlora_mx_linear_workspace_size(int64_t rows, int64_t c
  *   r > 0: A [r, cols], B [rows, r] bf16 and XA_out [M, r] float (or NULL) with
  *   the requirements of qlora_linear_fwd; in the rank-r term s X A^T is carried
  *   as the sum of two bf16 numbers, within 2^-17 of each element.  Not with
- *   scale_per_row (QLORA_ERR_UNSUPPORTED).
+ *   scale_per_row (QLORA_ERR_UNSUPPORTED).  QLORA_NVFP4: it is divided by the token's
+ *   and W's global scales on the way, so its elements have to stay below 2^127 times
+ *   their product (2^103 for X and W of 1), or Y is Inf or NaN.
  * Bit-reproducible from run to run on the same device.
  */
 QLORA_EXPORT qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, int64_t M, const uint16_t* A,

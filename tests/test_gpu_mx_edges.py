@@ -150,3 +150,20 @@ def test_a_nan_logit_is_the_largest(qb):  # noqa: F811
         bad = t in (2, 4)
         assert bool(p[t].isnan().all()) is bad and bool(Y[t].isnan().all()) is bad
         assert bad or (p[t].sum() - 1).abs() < 1e-5
+
+
+# ---------------------------------------------------------------- the adapter under far global scales
+@pytest.mark.parametrize("m", [3, 40, 150])
+@pytest.mark.parametrize("g", [2.0e-39, 2.0 ** -140])
+def test_an_adapter_of_zeros_under_a_tiny_global_scale(qb, m, g):  # noqa: F811
+    """1 / g is no float, but the rank-r term of zeros divided by g is zero, forward and backward."""
+    w, x, dy = normal((128, 192), 1.0, 1), normal((m, 192), 1.0, 2).cuda(), normal((m, 128), 1.0, 3).cuda()
+    zero, b = torch.zeros(8, 192, dtype=torch.bfloat16, device="cuda"), normal((128, 8), 0.02, 4).cuda()
+    q, qt = upload(qb, f64(w), "nvfp4"), upload(qb, f64(w).T, "nvfp4")
+    q.global_scale.fill_(g)
+    qt.global_scale.fill_(g)
+    plain, back = qb.qlora_mx_linear_fwd(q, x)[0], qb.qlora_mx_linear_bwd(qt, dy)[0]
+    assert torch.isfinite(plain).all() and torch.isfinite(back).all()
+    assert torch.equal(qb.qlora_mx_linear_fwd(q, x, zero, b, 0.5)[0], plain)
+    a = normal((8, 192), 0.02, 5).cuda()
+    assert torch.equal(qb.qlora_mx_linear_bwd(qt, dy, x, a, torch.zeros_like(b), 0.5)[0], back)
