@@ -115,6 +115,8 @@ _lib.qlora_mx_moe_workspace_size.argtypes = [_i32, _i64, _i64, _i64, _i32, _szp]
 _lib.qlora_mx_moe_workspace_size.restype = ctypes.c_int
 _lib.qlora_mx_moe_fwd.argtypes = [_MX, _MX, _vp, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _sz, _vp]
 _lib.qlora_mx_moe_fwd.restype = ctypes.c_int
+_lib.qlora_selftest_mx_form.argtypes = [_i64, _i64, _i32, _i64, _i32, _i32, _i32, ctypes.POINTER(_i32), ctypes.POINTER(_i32)]
+_lib.qlora_selftest_mx_form.restype = ctypes.c_int
 
 EXPORTED = ["qlora_status_string", "qlora_get_codebook", "qlora_get_levels", "qlora_nf4_sizes", "qlora_quantize_nf4_dq",
             "qlora_dequantize", "qlora_linear_workspace_size", "qlora_linear_fwd", "qlora_linear_fwd_multi",
@@ -122,7 +124,7 @@ EXPORTED = ["qlora_status_string", "qlora_get_codebook", "qlora_get_levels", "ql
             "qlora_time_next_gemm", "qlora_quantize_nf4_dq_noalloc", "qlora_selftest_bounded_wait",
             "qlora_mx_sizes", "qlora_mx_quantize", "qlora_mx_dequantize",
             "qlora_mx_linear_workspace_size", "qlora_mx_linear_fwd", "qlora_mx_linear_bwd",
-            "qlora_mx_moe_workspace_size", "qlora_mx_moe_fwd"]
+            "qlora_mx_moe_workspace_size", "qlora_mx_moe_fwd", "qlora_selftest_mx_form"]
 
 # Largest weight the allocation-free quantize variant accepts.
 NOALLOC_MAX_ELEMENTS = 134217728
@@ -639,6 +641,16 @@ def qlora_mx_linear_bwd(qT: MXTensor, dY: torch.Tensor, X: torch.Tensor | None =
     _on(dev, "qlora_mx_linear_bwd", _lib.qlora_mx_linear_bwd, c, _addr(X), dY.data_ptr(), m, _addr(A), _addr(B), r,
         float(s), _addr(XA), _addr(dX), _addr(dA), _addr(dB), workspace.data_ptr(), _size(workspace))
     return dX, dA, dB
+
+
+def qlora_selftest_mx_form(rows: int, cols: int, fmt: str, m: int, r: int = 0, backward: bool = False,
+                           num_sms: int = 148) -> tuple:
+    """("few", "stream" or "pair", token tile): the kernel that multiplies in a
+    forward or a backward of a layer W [rows, cols] (for tests)."""
+    form, tile = ctypes.c_int32(), ctypes.c_int32()
+    _check(_lib.qlora_selftest_mx_form(rows, cols, MX_FORMATS[fmt], m, r, int(backward), num_sms, form, tile),
+           "qlora_selftest_mx_form")
+    return ("few", "stream", "pair")[form.value], tile.value
 
 
 @functools.lru_cache(maxsize=4096)

@@ -169,14 +169,24 @@ int pair_token_tile(int64_t rows, int64_t m, int num_sms) {
   return narrow < wide ? 128 : 256;
 }
 
+// Which kernel multiplies, and its token tile.  The backward (not `fwd`) always
+// quantises dY in a launch of its own.
+enum class MxForm { few, stream, pair };
+MxForm product_form(int format, int64_t rows, int64_t k, int64_t m, int lora_steps, bool fwd, int num_sms, int* tile) {
+  if (fwd && (*tile = mx_few_tile(format, rows, m, k, lora_steps, num_sms)) != 0) return MxForm::few;
+  const bool pair = m > kMxStreamTokens;
+  *tile = pair ? pair_token_tile(rows, m, num_sms) : m <= 16 ? 16 : m <= 32 ? 32 : 64;
+  return pair ? MxForm::pair : MxForm::stream;
+}
+
 // out [M, W->rows] = q(X) deq(W)^T + lora_x lora_w (see mx_stream.cu); lora_x in two
 // bf16 parts, [M][2 * 64 lora_steps].
 qlora_status run_mx_gemm(const qlora_mx_tensor* W, int64_t M, uint8_t* ws, const ProductLayout& P, const uint16_t* lora_w,
                          bool lora_mn, const uint16_t* lora_x, int r, int lora_steps, uint16_t* out,
                          const DeviceInfo& d, cudaStream_t cs) {
   const ActLayout& L = P.act;
-  const bool pair = M > kMxStreamTokens;
-  const int bn = pair ? pair_token_tile(W->rows, M, d.num_sms) : M <= 16 ? 16 : M <= 32 ? 32 : 64;
+  int bn;
+  const bool pair = product_form(W->format, W->rows, W->cols, M, lora_steps, false, d.num_sms, &bn) == MxForm::pair;
   const int box_x = pair ? bn / 2 : bn;
   const int64_t pitch = mx_pitch(W->cols);
   MxGemmArgs a{};
@@ -399,7 +409,8 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* W, const uint16_t* X, in
   if ((st = device_info(&d)) != QLORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const int few = mx_few_tile(W->format, W->rows, M, W->cols, r ? sh.lora_steps : 0, d.num_sms);
+  int few;
+  if (product_form(W->format, W->rows, W->cols, M, r ? sh.lora_steps : 0, true, d.num_sms, &few) != MxForm::few) few = 0;
   if (!few && quantize_acts(W, X, M, ws, L.product, L.xa.cnt, L.xa.cnt_end, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
   const uint16_t* sxa = nullptr;
   if (r) {
@@ -471,6 +482,19 @@ qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, c
   }
   if (dX && (st = run_mx_gemm(WT, M, ws, L.product, A, true, sg, r, r ? sh.lora_steps : 0, dX, d, cs)) != QLORA_OK) return st;
   return r ? run_lora_grads(sh, X, dY, s, XA, dA, dB, ws, &L.lora, kRankFlush, d, cs) : QLORA_OK;
+}
+
+qlora_status qlora_selftest_mx_form(int64_t rows, int64_t cols, int32_t format, int64_t M, int32_t r, int32_t backward,
+                                    int32_t num_sms, int32_t* form, int32_t* token_tile) {
+  if (format != QLORA_MXFP4 && format != QLORA_NVFP4) return QLORA_ERR_UNSUPPORTED;
+  LinearShape sh{};
+  const qlora_status st = mx_layer_shape(rows, cols, M, r, &sh);
+  if (st != QLORA_OK) return st;
+  if (num_sms < 2) return QLORA_ERR_SHAPE;
+  if (!form || !token_tile) return QLORA_ERR_NULL;
+  *form = static_cast<int32_t>(product_form(format, backward ? cols : rows, backward ? rows : cols, M, r ? sh.lora_steps : 0,
+                                            !backward, num_sms, token_tile));
+  return QLORA_OK;
 }
 
 qlora_status qlora_mx_moe_workspace_size(int32_t experts, int64_t hidden, int64_t inner, int64_t M, int32_t top_k,

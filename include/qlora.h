@@ -410,6 +410,16 @@ QLORA_EXPORT qlora_status qlora_quantize_nf4_dq_noalloc(const uint16_t* W, const
                                                      qlora_stream_t stream);
 
 /*
+ * Which kernel qlora_mx_linear_fwd (backward = 0) or the dX of qlora_mx_linear_bwd
+ * takes for a layer [rows, cols], M tokens and rank r on a GPU of num_sms SMs, so
+ * that tests can tell which one they ran: *form 0 one launch with the tokens'
+ * quantisation, 1 the streamed weight, 2 tiles over pairs of SMs; *token_tile its
+ * tokens per tile.  Host only.
+ */
+QLORA_EXPORT qlora_status qlora_selftest_mx_form(int64_t rows, int64_t cols, int32_t format, int64_t M, int32_t r,
+                                                 int32_t backward, int32_t num_sms, int32_t* form, int32_t* token_tile);
+
+/*
  * Self-test of the failure path (no counterpart on the pages): launches one
  * CTA that waits on an mbarrier nothing arrives on, with the library's bounded
  * wait and a limit of `limit_cycles` SM cycles (0 .. 1e8) instead of the

@@ -40,3 +40,17 @@ def test_import_without_torchs_private_stream_getter():
     code = ("import torch; del torch._C._cuda_getCurrentRawStream; import bit_nf4_quantized_encode_b200 as qb; "
             "torch.cuda.current_stream = lambda i: type('S', (), {'cuda_stream': 40 + i}); assert qb._raw_stream(2) == 42")
     subprocess.run([sys.executable, "-c", code], check=True)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_form_of_a_product(fmt):
+    form = lambda *a, **k: qb.qlora_selftest_mx_form(*a[:2], fmt, *a[2:], **k)  # noqa: E731
+    assert form(22016, 8192, 1) == ("few", 8) and form(8192, 22016, 16, 64) == ("stream", 16)
+    assert form(22016, 8192, 1, backward=True) == ("stream", 16)
+    assert form(512, 512, 17) == ("stream", 32) and form(512, 512, 64) == ("stream", 64)
+    assert form(512, 512, 65) == ("pair", 128)
+    assert form(8192, 8192, 8192) == ("pair", 256) and form(8192, 320, 8192, 64, backward=True)[0] == "pair"
+    f = lib.qlora_selftest_mx_form
+    out = ctypes.c_int32()
+    assert f(64, 64, 7, 4, 0, 0, 148, out, out) == -4 and f(64, 64, 0, 0, 0, 0, 148, out, out) == -2
+    assert f(64, 64, 0, 4, 0, 0, 1, out, out) == -2 and f(64, 64, 0, 4, 0, 0, 148, None, out) == -1
