@@ -377,21 +377,29 @@ cudaError_t launch_t(MxFewArgs a, const MxMaps& m, int num_sms, cudaStream_t str
 
 }  // namespace
 
-// Where one launch is faster than the quantiser's and the streamed product's.
-// Measured on 148 SMs, one token, MXFP4: here a step of 256 costs 0.30 us and 0.045
-// us a unit, or 0.1 us a unit (its 4.3 KB at an SM's share of memory bandwidth),
-// quantising 0.12 us per 1024 elements; there a tile's step costs 0.42 us, and 5.5 us
-// more are spent on the second kernel and on joining.  22016 x 8192: 19.5 us here,
-// 23.7 there; 4096 x 4096: 8.1 and 9.7; 8192 x 8192: 16.6 and 15.4; 8192 x 22016: 62 and 32.
+// Where one launch is faster than the quantiser's and the streamed product's, by a
+// model of both in us on 148 SMs.  Here a chunk's step of 256 (or of 64 ranks) costs
+// `step` and `unit` for each of its units, or `bytes` a unit at least (4.3 KB at an
+// SM's share of memory bandwidth), quantising `quant` per 1024 elements, waiting for X
+// A^T 0.5; there a tile's step of 256 costs `stream` (of 64 ranks a third of it), and
+// the second kernel and the joining 5.5.  Both were timed at 720 calls (512 to 22016
+// rows, 512 to 16384 columns, 1 to 16 tokens, rank 0 to 256): what the model takes is
+// 0.2% (MXFP4) and 0.3% (NVFP4) slower than the faster one on average and 10% at most.
+// MXFP4, one token: 22016 x 8192: 18.4 us here, 21.0 there; 4096 x 4096: 8.0 and 9.0;
+// 8192 x 8192: 13.7 both; 8192 x 16384: 25.0 and 18.3.
 int mx_few_tile(int fmt, int64_t rows, int64_t m, int64_t k, int lora_steps, int num_sms) {
   if (m > 16 || m * k > kMxFewElements) return 0;
   const int n = m <= 8 ? 8 : 16, ksteps = static_cast<int>((k + 255) / 256);
   if (tokens_bytes(fmt, n, ksteps, lora_steps) > kMxFewShared) return 0;
+  struct Costs {
+    double step, unit, bytes, quant, stream;
+  };
+  const Costs c = fmt == kMxFp4 ? Costs{0.30, 0.045, 0.100, 0.12, 0.42} : Costs{0.40, 0.033, 0.127, 0.19, 0.45};
   const int64_t units = (rows + 31) / 32, most = (units + num_sms - 1) / num_sms, chunks = (most + kUnits - 1) / kUnits;
   const double per = static_cast<double>(most) / chunks;
-  const double step = 0.30 + 0.045 * per > 0.1 * per ? 0.30 + 0.045 * per : 0.1 * per;
-  const double here = chunks * (ksteps + lora_steps) * step + 0.12 * m * k / 1024;
-  const double there = 5.5 + 0.42 * static_cast<double>((rows + 127) / 128) * (ksteps + lora_steps) / num_sms;
+  const double step = c.step + c.unit * per > c.bytes * per ? c.step + c.unit * per : c.bytes * per;
+  const double here = chunks * (ksteps + lora_steps) * step + c.quant * m * k / 1024 + (lora_steps ? 0.5 : 0.0);
+  const double there = 5.5 + c.stream * static_cast<double>((rows + 127) / 128) * (ksteps + 0.34 * lora_steps) / num_sms;
   return here < there ? n : 0;
 }
 

@@ -54,3 +54,10 @@ def test_form_of_a_product(fmt):
     out = ctypes.c_int32()
     assert f(64, 64, 7, 4, 0, 0, 148, out, out) == -4 and f(64, 64, 0, 0, 0, 0, 148, out, out) == -2
     assert f(64, 64, 0, 4, 0, 0, 1, out, out) == -2 and f(64, 64, 0, 4, 0, 0, 148, None, out) == -1
+
+
+@pytest.mark.parametrize("rows,cols,m,r", [(2048, 4096, 1, 0), (8192, 4096, 4, 16), (2048, 2048, 8, 0), (4096, 2048, 8, 64)])
+def test_nvfp4_leaves_one_launch_earlier(rows, cols, m, r):
+    """Where the quantisation within the product costs NVFP4 more than a launch (16 to 23% measured)."""
+    assert qb.qlora_selftest_mx_form(rows, cols, "nvfp4", m, r) == ("stream", 16)
+    assert qb.qlora_selftest_mx_form(rows, cols, "mxfp4", 1) == ("few", 8)
