@@ -28,9 +28,12 @@ inline int64_t mx_scale_bytes(int fmt, int64_t rows, int64_t cols) {
 // CTAs of the amax pass of an NVFP4 tensor quantised with one global scale
 // (one partial maximum each).
 constexpr int kMxAmaxGrid = 1184;
-// Up to this many elements every CTA of the quantiser finds the maximum itself:
-// 100 x 1000 takes 6.8 us of the GPU that way and 5.8 us in two launches, but the
-// second launch and its work buffer cost the host 4 us.
+// Up to this many elements every CTA of the quantiser finds the maximum itself.  In
+// us of the GPU, one launch and two: 16384 elements 3.0 and 4.7, 65536 4.7 and 4.6,
+// 100000 6.8 and 5.6, 131072 7.6 and 5.2, 262144 20 and 6.3; from the binding, where
+// the second launch and its work buffer cost the host 5: 8 and 13, 8 and 13, 8 and 15,
+// 10 and 13, 23 and 13.  The limit is the calls'; a graph of many such quantisations
+// loses 2.4 us each at its upper end.
 constexpr int64_t kMxSmallElements = 131072;
 
 struct MxQuantArgs {
