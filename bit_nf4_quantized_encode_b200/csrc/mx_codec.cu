@@ -11,7 +11,7 @@
 // e2m1() and e4m3() round to nearest, ties to even.  Divisions by powers of two
 // are exact; the other two cannot cross a rounding border in 32 bits (a bf16
 // numerator over 6 or over a 4-bit significand is exactly on the border or
-// 2^-9 away from it), so codes and scales are those of exact arithmetic.  A block with
+// 2^-8 away from it), so codes and scales are those of exact arithmetic.  A block with
 // a value that is not finite gets the scale NaN; other blocks do not see it.
 //
 // Bytes per element: 2 in, 0.5 + 1/32 (1/16) out.  MXFP4 is bound by them (8192 x

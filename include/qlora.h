@@ -246,7 +246,9 @@ QLORA_EXPORT qlora_status qlora_linear_bwd(const qlora_nf4_tensor* W, const uint
  *                S = e4m3((amax / g) / 6), code = e2m1((x / g) / S), 0 when S = 0.
  * e2m1() and e4m3() round to nearest, ties to even; codes and scales are those
  * of exact arithmetic.  A block holding a value that is not finite gets the
- * scale NaN (and takes no part in g); the other blocks are as without it.
+ * scale NaN; the other blocks, and g, are as if that value were 0.
+ * In all calls on this format the outputs overlap neither each other nor the
+ * inputs or the work buffer.
  */
 typedef enum { QLORA_MXFP4 = 0, QLORA_NVFP4 = 1 } qlora_mx_format;
 
