@@ -508,7 +508,7 @@ qlora_status qlora_linear_bwd(const qlora_nf4_tensor* W, const uint16_t* X, cons
 
   // 1) G = dY B -> bf16(s G) (+ fp32 G for few tokens), and X A^T -> bf16(s X A^T)
   //    (recomputed when not supplied, else converted from the caller's fp32)
-  if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L, RankDivide(), 0, d, cs)) != QLORA_OK) return st;
+  if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L, true, RankDivide(), 0, false, d, cs)) != QLORA_OK) return st;
 
   // 2) dX = dY deq(W) + (s G) A   (fused dequant GEMM, deq(W)^T as the MN-major operand)
   if (dX) {

@@ -34,6 +34,7 @@
 #include "bf16_parts.cuh"
 #include "lora.h"
 #include "mx_ptx.cuh"
+#include "nf4_device.cuh"
 
 namespace qlora {
 namespace {
@@ -103,14 +104,23 @@ __device__ __forceinline__ void store_bf16_row(const RankProblem& p, int64_t row
     }
 }
 
-// v as two bf16 parts (lora.h), 64 columns: v rounded, then what is left of it
-// rounded (nothing where the first part is not finite).
+// v as two bf16 parts (lora.h), 64 columns.  The end of a kernel of a few
+// microseconds runs this code once, and fetching it takes longer than running it, so
+// it works on pairs and has no other path for what is not finite: there the second
+// part (inf - inf or finite - inf) is bounded by 2^120, which no other reaches (2^119)
+// and which leaves the first one's Inf or NaN as it is.
 __device__ __forceinline__ void store_parts_row(uint16_t* dst, const float (&v)[64]) {
 #pragma unroll
   for (int c = 0; c < 64; c += 8) {
     uint32_t first[4], second[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) bf16_parts2(v[c + 2 * i], v[c + 2 * i + 1], first[i], second[i]);
+    for (int i = 0; i < 4; ++i) {
+      const float a = v[c + 2 * i], b = v[c + 2 * i + 1];
+      first[i] = pack_bf16x2(a, b);
+      second[i] = pack_bf16x2(__fsub_rn(a, bf16_lo(first[i])), __fsub_rn(b, bf16_hi(first[i])));
+      asm("min.bf16x2 %0, %0, %1;" : "+r"(second[i]) : "r"(0x7B807B80u));
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(second[i]) : "r"(0xFB80FB80u));
+    }
     *reinterpret_cast<uint4*>(dst + c) = make_uint4(first[0], first[1], first[2], first[3]);
     *reinterpret_cast<uint4*>(dst + 64 + c) = make_uint4(second[0], second[1], second[2], second[3]);
   }
@@ -140,9 +150,13 @@ __device__ __forceinline__ void store_final(const RankProblem& p, int64_t row, i
     if (p.out_parts) store_parts_row(p.out_parts + at, d);
     if (p.out_div) {
       // one divisor after the other: their product may be below what a float holds
-      const float by_row = 1.0f / p.row_div[row], all = p.all_div[0];      // row_div: powers of two
+      // (row_div: powers of two), and all_div's reciprocal taken where it is a normal
+      // float: 64 divisions of a thread took longer than the contraction of few tokens
+      const float by_row = 1.0f / p.row_div[row], all = p.all_div[0];
+      const float shift = all < 0x1p-126f ? 0x1p64f : all > 0x1p126f ? 0x1p-64f : 1.0f;
+      const float by_all = 1.0f / __fmul_rn(all, shift);
 #pragma unroll
-      for (int c = 0; c < 64; ++c) d[c] = __fdiv_rn(__fmul_rn(d[c], by_row), all);
+      for (int c = 0; c < 64; ++c) d[c] = __fmul_rn(__fmul_rn(__fmul_rn(d[c], by_row), by_all), shift);
       store_parts_row(p.out_div + at, d);
     }
   }

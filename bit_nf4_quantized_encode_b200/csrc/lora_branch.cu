@@ -154,13 +154,14 @@ qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_
 
 qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uint16_t* dY, const uint16_t* A,
                              const uint16_t* B, float s, const float* XA, uint8_t* ws, BwdLayout* L,
-                             const RankDivide& div, int flush, const DeviceInfo& d, cudaStream_t cs) {
+                             bool sg_for_dx, const RankDivide& div, int flush, bool cleared, const DeviceInfo& d,
+                             cudaStream_t cs) {
   float* g32 = sh.decode ? reinterpret_cast<float*>(ws + L->g) : nullptr;     // fp32 G and X A^T: few-token grads
   float* xa32 = sh.decode ? reinterpret_cast<float*>(ws + L->xa) : nullptr;
   uint16_t* sg = reinterpret_cast<uint16_t*>(ws + L->sg);
   uint16_t* sxa = reinterpret_cast<uint16_t*>(ws + L->sxa);
   const bool recompute = XA == nullptr;
-  if (L->clear_end && cudaMemsetAsync(ws, 0, L->clear_end, cs) != cudaSuccess) return QLORA_ERR_CUDA;
+  if (!cleared && cudaMemsetAsync(ws, 0, L->clear_end, cs) != cudaSuccess) return QLORA_ERR_CUDA;
   CUtensorMap dy_k, b_mn, x_k, a_k;
   if (!make_map(&dy_k, dY, sh.rows, sh.m, sh.rows * 2, 128) ||
       !make_map(&b_mn, B, sh.r, sh.rows, sh.r * 2, 64) ||
@@ -190,7 +191,8 @@ qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uin
     ra.p[0].out_f32 = g32; ra.p[0].ld_f32 = sh.rpad;
     const bool two = L->parts == 2;
     ra.p[0].flush = flush;
-    (two ? ra.p[0].out_parts : ra.p[0].out_bf16) = sg;
+    // (its parts only where dA or dX takes them)
+    if (!two || !sh.decode || sg_for_dx) (two ? ra.p[0].out_parts : ra.p[0].out_bf16) = sg;
     ra.p[0].ld_bf16 = sh.rpad; ra.p[0].bf16_cols = sh.rpad; ra.p[0].bf16_scale = s;
     ra.p[0].out_div = div.out; ra.p[0].row_div = div.row; ra.p[0].all_div = div.all;
     ra.nprob = 1;

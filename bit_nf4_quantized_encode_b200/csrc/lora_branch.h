@@ -68,11 +68,13 @@ struct RankDivide {
 qlora_status run_rank_xa(const LinearShape& sh, const uint16_t* X, const uint16_t* A, float s, float* XA_out, uint8_t* ws,
                          const XaLayout& L, int parts, const RankDivide& div, int flush, bool cleared, const DeviceInfo& d,
                          cudaStream_t cs);
-// Launch 1 of the backward (after clearing [0, clear_end)); `div`: s G for dX, beside
-// the one in L->sg; `flush` as RankProblem's.
+// Launch 1 of the backward, after clearing [0, clear_end) (`cleared`: a kernel before
+// has).  dX takes s G from L->sg (sg_for_dx) or divided from `div`; `flush` as
+// RankProblem's.
 qlora_status run_rank_inputs(const LinearShape& sh, const uint16_t* X, const uint16_t* dY, const uint16_t* A,
                              const uint16_t* B, float s, const float* XA, uint8_t* ws, BwdLayout* L,
-                             const RankDivide& div, int flush, const DeviceInfo& d, cudaStream_t cs);
+                             bool sg_for_dx, const RankDivide& div, int flush, bool cleared, const DeviceInfo& d,
+                             cudaStream_t cs);
 // Launch 3: dA and dB.
 qlora_status run_lora_grads(const LinearShape& sh, const uint16_t* X, const uint16_t* dY, float s, const float* XA,
                             float* dA, float* dB, uint8_t* ws, BwdLayout* L, int flush, const DeviceInfo& d,

@@ -48,8 +48,8 @@ struct MxQuantArgs {
   int per_row;
   uint32_t* amax;            // NVFP4, one global scale: partial maxima [amax_n]
   int amax_n;                // 0: none, a small matrix
-  uint32_t* zero;            // words cleared on the way (the counters of the next kernel)
-  int zero_n;
+  uint32_t* zero[2];         // words cleared on the way (the counters of later kernels)
+  int zero_n[2];
 };
 
 cudaError_t launch_mx_amax(const uint16_t* in, int64_t numel, uint32_t* partials, int grid, cudaStream_t stream);

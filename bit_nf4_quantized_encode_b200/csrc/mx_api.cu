@@ -136,8 +136,9 @@ int mx_group(int m_tiles, int64_t pitch) {
 }
 
 // q(X) into the work buffer (NVFP4: a global scale per token).
-// Words of the work buffer that a later kernel of the call counts in ([zero,
-// zero_end) bytes; a streamed product's counters by themselves) are cleared on the way.
+// Words of the work buffer that later kernels of the call count in ([zero, zero_end)
+// bytes, and a streamed product's counters) are cleared on the way: a memset of its
+// own takes 4 us in a graph.
 cudaError_t quantize_acts(const qlora_mx_tensor* W, const uint16_t* X, int64_t M, uint8_t* ws, const ProductLayout& P,
                           size_t zero, size_t zero_end, const DeviceInfo& d, cudaStream_t cs) {
   const ActLayout& L = P.act;
@@ -151,12 +152,10 @@ cudaError_t quantize_acts(const qlora_mx_tensor* W, const uint16_t* X, int64_t M
   a.pitch = mx_pitch(W->cols);
   a.kt = mx_tiles_k(W->format, W->cols);
   a.per_row = W->format == QLORA_NVFP4;
-  if (M <= kMxStreamTokens) {
-    zero = P.counters;
-    zero_end = zero + static_cast<size_t>((W->rows + 127) / 128) * 16;
-  }
-  a.zero = reinterpret_cast<uint32_t*>(ws + zero);
-  a.zero_n = static_cast<int>((zero_end - zero) / 4);
+  a.zero[0] = reinterpret_cast<uint32_t*>(ws + zero);
+  a.zero_n[0] = static_cast<int>((zero_end - zero) / 4);
+  a.zero[1] = reinterpret_cast<uint32_t*>(ws + P.counters);
+  a.zero_n[1] = M <= kMxStreamTokens ? static_cast<int>((W->rows + 127) / 128 * 4) : 0;
   return counted(launch_mx_quant(W->format, false, a, d.num_sms, cs));
 }
 
@@ -467,7 +466,7 @@ qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, c
   if ((st = device_info(&d)) != QLORA_OK) return st;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (dX && quantize_acts(WT, dY, M, ws, L.product, 0, 0, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
+  if (dX && quantize_acts(WT, dY, M, ws, L.product, 0, r ? L.lora.clear_end : 0, d, cs) != cudaSuccess) return QLORA_ERR_CUDA;
   const uint16_t* sg = nullptr;
   if (r) {
     // G = dY B and X A^T as the backward over an NF4 weight has them
@@ -478,7 +477,8 @@ qlora_status qlora_mx_linear_bwd(const qlora_mx_tensor* WT, const uint16_t* X, c
       div.row = reinterpret_cast<const float*>(ws + L.product.act.global);
       div.all = WT->global_scale;
     }
-    if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L.lora, div, kRankFlush, d, cs)) != QLORA_OK) return st;
+    if ((st = run_rank_inputs(sh, X, dY, A, B, s, XA, ws, &L.lora, dX && !div.out, div, kRankFlush, dX != nullptr,
+                              d, cs)) != QLORA_OK) return st;
   }
   if (dX && (st = run_mx_gemm(WT, M, ws, L.product, A, true, sg, r, r ? sh.lora_steps : 0, dX, d, cs)) != QLORA_OK) return st;
   return r ? run_lora_grads(sh, X, dY, s, XA, dA, dB, ws, &L.lora, kRankFlush, d, cs) : QLORA_OK;

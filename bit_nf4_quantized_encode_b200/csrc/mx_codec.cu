@@ -112,7 +112,9 @@ __global__ void __launch_bounds__(kThreads) k_mx_amax(const uint16_t* in, int64_
 __device__ __forceinline__ void open_dependents(const MxQuantArgs& a) {
   asm volatile("griddepcontrol.launch_dependents;");
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.zero_n; i += blockDim.x) a.zero[i] = 0u;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      for (int i = threadIdx.x; i < a.zero_n[j]; i += blockDim.x) a.zero[j][i] = 0u;
 }
 
 // Units (row, segment) of a row-major walk with a fixed stride, without a

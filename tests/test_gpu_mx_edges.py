@@ -167,3 +167,21 @@ def test_an_adapter_of_zeros_under_a_tiny_global_scale(qb, m, g):  # noqa: F811
     assert torch.equal(qb.qlora_mx_linear_fwd(q, x, zero, b, 0.5)[0], plain)
     a = normal((8, 192), 0.02, 5).cuda()
     assert torch.equal(qb.qlora_mx_linear_bwd(qt, dy, x, a, torch.zeros_like(b), 0.5)[0], back)
+
+
+@pytest.mark.parametrize("m", [1, 12, 40, 150])
+def test_a_rank_term_that_overflows_is_infinite(qb, m):  # noqa: F811
+    """X A^T (dY B) of one token and one rank is past fp32's range: the token's Y
+    (dX) takes the sign of B (A), as the formula has it, and the others do not see it."""
+    rows, cols, r = 136, 192, 8
+    w, x, dy = normal((rows, cols), 0.02, 1).cuda(), normal((m, cols), 1.0, 2).cuda(), normal((m, rows), 1.0, 3).cuda()
+    a, b = normal((r, cols), 0.02, 4).cuda(), normal((rows, r), 0.02, 5).cuda()
+    q, qt = qb.qlora_mx_quantize(w), qb.qlora_mx_quantize(w, transpose=True)
+    x[:, 5], dy[:, 7] = 0, 0
+    a[0, 5], b[7, 0] = 2.0 ** 100, 2.0 ** 100
+    clean, back = qb.qlora_mx_linear_fwd(q, x, a, b, 0.5)[0], qb.qlora_mx_linear_bwd(qt, dy, x, a, b, 0.5)[0]
+    x[0, 5], dy[0, 7] = 2.0 ** 60, 2.0 ** 60
+    Y, dX = qb.qlora_mx_linear_fwd(q, x, a, b, 0.5)[0], qb.qlora_mx_linear_bwd(qt, dy, x, a, b, 0.5)[0]
+    assert torch.equal(Y[0].float(), torch.copysign(torch.full((rows,), float("inf"), device="cuda"), b[:, 0].float()))
+    assert torch.equal(dX[0].float(), torch.copysign(torch.full((cols,), float("inf"), device="cuda"), a[0].float()))
+    assert torch.equal(Y[1:], clean[1:]) and torch.equal(dX[1:], back[1:])
