@@ -22,8 +22,8 @@
 // contraction), or that value as two bf16 parts, so no separate convert kernel
 // runs.  A side job converts a caller-supplied fp32 X A^T the same way.  A rank-r
 // operand in two parts (the layer over a microscaled weight) has both beside the
-// one tile of the long operand: dA and dB of 8192 tokens, 22016 x 8192, rank 64:
-// 209 us without dX, 192 us from rounded operands, which put them 1e-3 off.
+// one tile of the long operand: G, dA and dB of 8192 tokens, 8192 x 8192, rank 64, in
+// 98 us; from rounded operands, which put the gradients 1e-3 off, in 87.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -15,8 +15,8 @@
 // a value that is not finite gets the scale NaN; other blocks do not see it.
 //
 // Bytes per element: 2 in, 0.5 + 1/32 (1/16) out.  MXFP4 is bound by them (8192 x
-// 8192: 30 us, 5.6 TB/s), NVFP4 by instruction issue beside them (36 us and a 30 us
-// pass for the maximum; transposed 44; dequantised 31).
+// 8192: 30 us, 5.6 TB/s), NVFP4 by instruction issue beside them (62 us with a pass
+// for the maximum; transposed 70; dequantised 33).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

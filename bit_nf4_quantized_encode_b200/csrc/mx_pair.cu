@@ -7,8 +7,10 @@
 // half of the tokens once, 8 KB a CTA for twice the tile.
 //
 // 8192 x 8192 by 8192 tokens, MXFP4: 192 us, 5.7 PFLOP/s, with the SM clock at 1.6
-// GHz under the power limit (the tensor pipe active 70% of the time; loads alone
-// 155 us).  One CTA with tiles of 128 x 128 took 548 us.
+// GHz under the power limit (the tensor pipe active 66% of the time; loads alone
+// 155 us).  One CTA with tiles of 128 x 128 took 548 us.  NVFP4's epilogue has its
+// token scales in shared memory, fetched while the products run: 243 us with the
+// quantiser, 256 with a read-only load of them per element.
 //
 // TMEM (512 columns): two accumulators of 256 columns that share 48 columns,
 // and the scales of one stage.  The epilogue drains the shared columns first;
