@@ -103,7 +103,9 @@ def test_dequantize_rounds_once_under_any_global_scale(qb, cols):  # noqa: F811
 def test_one_launch_products_in_a_chain(qb, m, size, fmt):  # noqa: F811
     """Each product starts while the one that writes its tokens still runs (and the
     first of a round while its weight is still being quantised); the result is that
-    of the same calls with a wait after each."""
+    of the same calls with a wait after each.  (4096 x 4096 NVFP4 takes two launches.)"""
+    if torch.cuda.get_device_properties(0).multi_processor_count == 148:
+        assert qb.qlora_selftest_mx_form(size, size, fmt, m) == (("stream", 16) if (size, fmt) == (4096, "nvfp4") else ("few", 8))
     ws = [normal((size, size), size ** -0.5, i).cuda() for i in range(4)]
     x = normal((m, size), 1.0, 9).cuda()
     out = [qb.empty_mx(size, size, x.device, fmt) for _ in ws]
