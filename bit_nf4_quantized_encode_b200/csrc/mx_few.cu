@@ -286,8 +286,8 @@ k_mx_few(const MxFewArgs a, const __grid_constant__ CUtensorMap wmap, const __gr
       // the weight's global scale before waiting for the products (it may be as late as
       // X: no read-only load)
       MxRowScale gw = {1.0f, 1.0f};
-      auto load_gw = [&](int i) {
-        const int row = (k.unit + i * 4 + quarter - k.col) * 32 + lane;
+      auto load_gw = [&](int i) {              // (a tile's rows may lie behind the last one, past 32 bits too)
+        const int64_t row = static_cast<int64_t>(k.unit + i * 4 + quarter - k.col) * 32 + lane;
         if (kFmt == kNvFp4 && row < a.rows) gw = mx_row_scale(a.w_global[a.w_per_row ? row : 0]);
       };
       const int i0 = warp >= 6 ? 1 : 0;
